@@ -351,6 +351,84 @@ MHC_API mhc_status mhc_pre_broadcast(const mhc_bf16 *x, const float *phi, const 
                                      float *comb_res_mix_out, void *workspace, size_t workspace_bytes,
                                      void *stream);
 
+/* ---- the 8-bit path around the fused step ------------------------------------------------------
+ * Producers and consumers of the MXFP8 form beside mhc_shifted_post_pre_mxfp8: E4M3 codes with one
+ * UE8M0 scale byte per 32 values in the 128x4 tile layout described there ("scale tiles" below;
+ * mhc_mxfp8_scale_bytes(rows, columns) bytes, padding bytes neither read nor written).  The pages name
+ * the MXFP8 layer input ("[DSV4.1] Four BS=1 critical-path fixes for DSpark decode", "What changed"
+ * item 3) but not what reads it. */
+
+/* Values that share one exponent in a quantized output.  With 128 the same byte is written for the
+ * four blocks of 32 (a last block of fewer than 128 values is allowed), so the scale tiles and
+ * whatever reads them do not change. */
+typedef enum mhc_mx_scale_block { MHC_MX_BLOCK_32 = 32, MHC_MX_BLOCK_128 = 128 } mhc_mx_scale_block;
+
+/* The residual addition with RMSNorm:
+ *   s = bf16(x + residual);  y = bf16(s / sqrt(mean_h s^2 + rmsnorm_eps) * gamma);  MXFP8 of y
+ *   x                [T,H] bf16
+ *   residual         [T,H] bf16, or NULL: s = x
+ *   rmsnorm_weight   [H]   bf16   gamma
+ *   residual_out     [T,H] bf16   s, or NULL (required NULL without residual); may equal residual
+ *   layer_in_out     [T,H] bf16   y, or NULL
+ *   layer_in_fp8, layer_in_scales   MXFP8 of the bf16 y as in mhc_shifted_post_pre_mxfp8 (H % 32 == 0),
+ *                                   or both NULL; one of y's two forms is required
+ *   scale_mode       mhc_mx_scale_mode;  scale_block  mhc_mx_scale_block
+ * One launch, no workspace. */
+MHC_API mhc_status mhc_add_rmsnorm_mxfp8(const mhc_bf16 *x, const mhc_bf16 *residual, const mhc_bf16 *rmsnorm_weight,
+                                         int64_t T, int64_t H, float rmsnorm_eps, mhc_bf16 *residual_out,
+                                         mhc_bf16 *layer_in_out, uint8_t *layer_in_fp8, uint8_t *layer_in_scales,
+                                         int scale_mode, int scale_block, void *stream);
+
+/* The SwiGLU between a gate/up and a down product: MXFP8 of silu(gate) * up.
+ *   gate_up     [T,2F] bf16: columns 0..F-1 gate, F..2F-1 up
+ *   act_fp8     [T,F] codes, act_scales  mhc_mxfp8_scale_bytes(T, F) bytes;  F % 32 == 0
+ * The value is quantized from fp32 or better in one rounding (no bf16 in between).  One launch, no workspace. */
+MHC_API mhc_status mhc_swiglu_mxfp8(const mhc_bf16 *gate_up, int64_t T, int64_t F, uint8_t *act_fp8, uint8_t *act_scales,
+                                    int scale_mode, int scale_block, void *stream);
+
+/* Type of a weight's block scales, and of a product's result. */
+typedef enum mhc_scale_type { MHC_SCALE_UE8M0 = 0, MHC_SCALE_F32 = 1 } mhc_scale_type;
+typedef enum mhc_out_type { MHC_OUT_BF16 = 0, MHC_OUT_F32 = 1 } mhc_out_type;
+
+#define MHC_MAX_EXPERTS 1024
+#define MHC_MAX_LINEAR_OUT (1 << 20)
+
+/* Bytes of workspace of the two products below, whatever their sizes (the device status word that
+ * mhc_check_status reads; zero-filled before the first use, like the other workspaces).  They keep
+ * nothing else in it, so calls in any order and on any streams may share one. */
+MHC_API size_t mhc_linear_workspace_size(void);
+
+/* The 8-bit matrix product: out[t][n] = sum_k x[t][k] w[n][k], accumulated in fp32, with
+ *   x[t][k] = E4M3(x_fp8[t][k]) * 2^(scale of (t, k / 32))
+ *   w[n][k] = E4M3(w_fp8[n][k]) * w_scales[n / 128][k / 128]
+ *   x_fp8     [T,K] E4M3 codes, x_scales  their scale tiles (any exponents; 128-value blocks too)
+ *   w_fp8     [N,K] E4M3 codes
+ *   w_scales  [ceil(N/128)][ceil(K/128)]: UE8M0 bytes (MHC_SCALE_UE8M0: applied by the tensor cores), or
+ *             fp32 (MHC_SCALE_F32: each 128 values of k summed apart, scaled and added in fp32)
+ *   out       [T,N] bf16 (rounded once) or fp32
+ * K % 32 == 0, 32 <= K <= MHC_MAX_HIDDEN; N % 8 == 0, 8 <= N <= MHC_MAX_LINEAR_OUT.  NaN codes and the
+ * NaN scale byte 255 give NaN in the rows (of x) or columns (of w) they belong to.  Deterministic.
+ * One launch. */
+MHC_API mhc_status mhc_linear_mxfp8(const uint8_t *x_fp8, const uint8_t *x_scales, const uint8_t *w_fp8, const void *w_scales,
+                                    int w_scale_type, int64_t T, int64_t K, int64_t N, void *out, int out_type,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* The same product with a weight per expert over ragged groups of rows:
+ *   out[m] = x[rows[m]] w[e]^T   for expert_offsets[e] <= m < expert_offsets[e + 1]
+ *   x_fp8           [R,K] codes, x_scales their scale tiles
+ *   rows            [M] int32 row of x of each output row, or NULL: row m (R == M).  An index outside
+ *                   [0, R) reads nothing and gives a row of NaN
+ *   expert_offsets  [E+1] int32, non-decreasing, on the device (never read by the host).  Rows before the
+ *                   first and behind the last group are left as they were; a bound outside [0, M] is
+ *                   clamped, a group that ends before it begins is empty
+ *   w_fp8           [E,N,K] codes, w_scales [E][ceil(N/128)][ceil(K/128)]
+ *   out             [M,N]
+ * 1 <= E <= MHC_MAX_EXPERTS, M and R at most MHC_MAX_TOKENS.  One launch. */
+MHC_API mhc_status mhc_expert_linear_mxfp8(const uint8_t *x_fp8, const uint8_t *x_scales, int64_t R, const int32_t *rows,
+                                           int64_t M, const int32_t *expert_offsets, int64_t E, const uint8_t *w_fp8,
+                                           const void *w_scales, int w_scale_type, int64_t K, int64_t N, void *out,
+                                           int out_type, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Forces a schedule for every following call of this process (a test hook; the
  * default is MHC_SCHEDULE_AUTO).  Returns MHC_ERR_INVALID_ARG for an unknown value. */
 MHC_API mhc_status mhc_set_schedule(int schedule);

@@ -21,6 +21,7 @@ __all__ = [
     "set_schedule", "auto_schedule", "auto_side_tokens", "check_status", "last_launch_count", "SCHEDULES",
     "post_int8", "post_sqrsum", "pre_broadcast", "shifted_post_pre_split", "shifted_post_pre_mxfp8", "mxfp8_scale_bytes", "MX_SCALE_FLOOR", "MX_SCALE_CEIL", "set_main_kernel_events",
     "packed_phi_bytes", "pack_phi",
+    "add_rmsnorm_mxfp8", "swiglu_mxfp8", "linear_mxfp8", "expert_linear_mxfp8", "linear_workspace_size",
 ]
 MX_SCALE_FLOOR, MX_SCALE_CEIL = 0, 1
 
@@ -86,6 +87,16 @@ def lib():
             L.mhc_post.restype = I
             L.mhc_pre.argtypes = [P, P, P, P, P, I64, I64, F, F, F, F, I, P, P, P, P, P, Z, P]
             L.mhc_pre.restype = I
+            L.mhc_add_rmsnorm_mxfp8.argtypes = [P, P, P, I64, I64, F, P, P, P, P, I, I, P]
+            L.mhc_add_rmsnorm_mxfp8.restype = I
+            L.mhc_swiglu_mxfp8.argtypes = [P, I64, I64, P, P, I, I, P]
+            L.mhc_swiglu_mxfp8.restype = I
+            L.mhc_linear_workspace_size.argtypes = []
+            L.mhc_linear_workspace_size.restype = Z
+            L.mhc_linear_mxfp8.argtypes = [P, P, P, P, I, I64, I64, I64, P, I, P, Z, P]
+            L.mhc_linear_mxfp8.restype = I
+            L.mhc_expert_linear_mxfp8.argtypes = [P, P, I64, P, I64, P, I64, P, P, I, I64, I64, P, I, P, Z, P]
+            L.mhc_expert_linear_mxfp8.restype = I
             L.mhc_set_schedule.argtypes = [I]
             L.mhc_set_schedule.restype = I
             L.mhc_auto_schedule.argtypes = [I64, I64]
@@ -393,6 +404,147 @@ def pre_broadcast(x, phi, bias, mix_scales, rmsnorm_weight, *, hc_norm_eps, rmsn
                                  ws.numel() * ws.element_size(), _stream(stream, dev))
     _check(rc, "mhc_pre_broadcast")
     return o
+
+
+def _arg(t, name, dtypes, shape, dev):
+    """One tensor argument of the calls below, as its address: its type, shape, device and layout."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d).removeprefix('torch.') for d in dtypes)}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+    return t.data_ptr()
+
+
+_types = None
+
+
+def _dtypes():
+    """(bf16 or its bits, E4M3 or its bits, UE8M0 or its bits, fp32, int32) as tuples of torch types."""
+    global _types
+    if _types is None:
+        torch = _torch()
+        _types = ((torch.bfloat16, torch.int16, torch.uint16), (torch.uint8, torch.float8_e4m3fn),
+                  (torch.uint8, torch.float8_e8m0fnu), (torch.float32,), (torch.int32,))
+    return _types
+
+
+def _run(name, dev, stream, *args):
+    """A library call on `stream` (the current stream of the tensors' device) with that device current."""
+    torch = _torch()
+    fn = getattr(lib(), name)
+    handle = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
+    _check(rc, name)
+
+
+def add_rmsnorm_mxfp8(x, residual, rmsnorm_weight, *, rmsnorm_eps, scale_mode=MX_SCALE_FLOOR, scale_block=32,
+                      want_bf16=False, want_mxfp8=True, out=None, stream=None):
+    """mhc_add_rmsnorm_mxfp8: the residual addition (residual may be None) with RMSNorm.  Returns a dict with
+    residual_out [T,H] bf16 (only with a residual), layer_in [T,H] bf16 (only if want_bf16 or given),
+    layer_in_fp8 [T,H] uint8 and layer_in_scales (unless want_mxfp8 is false).  ``out`` may supply any of
+    them; residual_out may be the residual itself."""
+    torch = _torch()
+    T, H = x.shape
+    dev = x.device
+    bf16, fp8, e8m0, _, _ = _dtypes()
+    o = dict(out or {})
+    if residual is not None and "residual_out" not in o:
+        o["residual_out"] = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    if want_bf16 and "layer_in" not in o:
+        o["layer_in"] = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    if want_mxfp8:
+        if "layer_in_fp8" not in o:
+            o["layer_in_fp8"] = torch.empty((T, H), dtype=torch.uint8, device=dev)
+        if "layer_in_scales" not in o:
+            o["layer_in_scales"] = torch.empty(mxfp8_scale_bytes(T, H), dtype=torch.uint8, device=dev)
+
+    def given(k, types, shape):
+        t = o.get(k)
+        return None if t is None else _arg(t, k, types, shape, dev)
+
+    _run("mhc_add_rmsnorm_mxfp8", dev, stream, _arg(x, "x", bf16, (T, H), dev),
+         None if residual is None else _arg(residual, "residual", bf16, (T, H), dev),
+         _arg(rmsnorm_weight, "rmsnorm_weight", bf16, (H,), dev), T, H, rmsnorm_eps,
+         given("residual_out", bf16, (T, H)), given("layer_in", bf16, (T, H)), given("layer_in_fp8", fp8, (T, H)),
+         given("layer_in_scales", e8m0, (mxfp8_scale_bytes(T, H),)), int(scale_mode), int(scale_block))
+    return o
+
+
+def swiglu_mxfp8(gate_up, *, scale_mode=MX_SCALE_FLOOR, scale_block=32, out=None, stream=None):
+    """mhc_swiglu_mxfp8: silu(gate) * up of gate_up [T,2F] bf16 (gate first).  Returns a dict with act_fp8
+    [T,F] uint8 and act_scales; ``out`` may supply them."""
+    torch = _torch()
+    T, F = gate_up.shape[0], gate_up.shape[1] // 2
+    dev = gate_up.device
+    bf16, fp8, e8m0, _, _ = _dtypes()
+    o = dict(out or {})
+    if "act_fp8" not in o:
+        o["act_fp8"] = torch.empty((T, F), dtype=torch.uint8, device=dev)
+    if "act_scales" not in o:
+        o["act_scales"] = torch.empty(mxfp8_scale_bytes(T, F), dtype=torch.uint8, device=dev)
+    _run("mhc_swiglu_mxfp8", dev, stream, _arg(gate_up, "gate_up", bf16, (T, 2 * F), dev), T, F,
+         _arg(o["act_fp8"], "act_fp8", fp8, (T, F), dev),
+         _arg(o["act_scales"], "act_scales", e8m0, (mxfp8_scale_bytes(T, F),), dev), int(scale_mode), int(scale_block))
+    return o
+
+
+def linear_workspace_size() -> int:
+    return int(lib().mhc_linear_workspace_size())
+
+
+def _linear_args(x_fp8, x_scales, w_fp8, w_scales, M, E, out_dtype, out, workspace):
+    """What the two products share: the checked addresses, the weight scales' and the result's types."""
+    torch = _torch()
+    dev = x_fp8.device
+    _, fp8, e8m0, f32, _ = _dtypes()
+    R, K = x_fp8.shape
+    lead = () if E is None else (E,)
+    N = w_fp8.shape[-2]
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out must be {str(out_dtype).removeprefix('torch.')}, got {out.dtype}")
+    if workspace is None:
+        workspace = torch.zeros(linear_workspace_size(), dtype=torch.uint8, device=dev)
+    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
+    wide = w_scales.dtype == torch.float32
+    x = (_arg(x_fp8, "x_fp8", fp8, (R, K), dev), _arg(x_scales, "x_scales", e8m0, (mxfp8_scale_bytes(R, K),), dev))
+    w = (_arg(w_fp8, "w_fp8", fp8, (*lead, N, K), dev),
+         _arg(w_scales, "w_scales", f32 if wide else e8m0, (*lead, (N + 127) // 128, (K + 127) // 128), dev), int(wide))
+    o = (_arg(out, "out", (torch.bfloat16, torch.float32), (M, N), dev), int(out.dtype == torch.float32),
+         workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return dev, R, K, N, x, w, out, o
+
+
+def linear_mxfp8(x_fp8, x_scales, w_fp8, w_scales, *, out_dtype=None, out=None, workspace=None, stream=None):
+    """mhc_linear_mxfp8: x [T,K] (MXFP8 codes and scale tiles) times w [N,K] transposed, w with one scale per
+    128 x 128 block: w_scales [ceil(N/128), ceil(K/128)], uint8 or float8_e8m0fnu (exponents) or float32.
+    Returns out [T,N], bfloat16 (the default) or float32."""
+    dev, T, K, N, x, w, out, o = _linear_args(x_fp8, x_scales, w_fp8, w_scales, x_fp8.shape[0], None, out_dtype, out,
+                                              workspace)
+    _run("mhc_linear_mxfp8", dev, stream, *x, *w, T, K, N, *o)
+    return out
+
+
+def expert_linear_mxfp8(x_fp8, x_scales, w_fp8, w_scales, expert_offsets, *, rows=None, out_dtype=None, out=None,
+                        workspace=None, stream=None):
+    """mhc_expert_linear_mxfp8: out[m] = x[rows[m]] w[e]^T for expert_offsets[e] <= m < expert_offsets[e+1]
+    (int32 on the device; rows None: row m).  w [E,N,K], w_scales [E, ceil(N/128), ceil(K/128)] as in
+    linear_mxfp8.  Rows of out outside every group are left as they were."""
+    M = x_fp8.shape[0] if rows is None else rows.shape[0]
+    E = w_fp8.shape[0]
+    dev, R, K, N, x, w, out, o = _linear_args(x_fp8, x_scales, w_fp8, w_scales, M, E, out_dtype, out, workspace)
+    i32 = _dtypes()[4]
+    _run("mhc_expert_linear_mxfp8", dev, stream, *x, R, None if rows is None else _arg(rows, "rows", i32, (M,), dev), M,
+         _arg(expert_offsets, "expert_offsets", i32, (E + 1,), dev), E, *w, K, N, *o)
+    return out
 
 
 def set_schedule(name_or_id):

@@ -1,0 +1,282 @@
+// Producers of the MXFP8 form besides the fused step: the residual addition with RMSNorm, and the SwiGLU.
+//
+//   add_rmsnorm  s = bf16(x + residual);  y = bf16(s / sqrt(mean_h s^2 + eps) * gamma);  MXFP8 of y
+//   swiglu       MXFP8 of silu(gate) * up
+//
+// One scale per 32 values, or one per 128 (then written four times, so the scale tiles keep their layout and
+// every consumer of them works unchanged).  Both are bound by HBM: each input is read once and each output
+// written once.
+//
+// Roundings.  s and y are held in bf16 between sublayers, so they are rounded there, and the norm and the
+// codes are taken from the rounded values, as in the fused step.  The products s * gamma are exact in fp32
+// (8-bit significands); the reciprocal root is applied as a pair of fp32 values, so y before its rounding is
+// the fp32 value nearest to the exact one, up to the square sum's error.  The SwiGLU's value goes from fp32
+// to its code in one rounding; a value that fp32 cannot place (within a few ulp of a border between two
+// codes, or a maximum at the border of two exponents) is computed again in fp64.
+#include <algorithm>
+#include <cstdint>
+
+#include "mhc_device.cuh"
+#include "mhc_kernels.h"
+
+namespace mhc {
+
+namespace {
+
+// The 16-byte vectors of one row are spread over the threads so that consecutive lanes hold consecutive
+// vectors: 4 lanes hold a block of 32 values, 16 lanes one of 128.
+template <int kLanes>
+__device__ __forceinline__ float group_max(float a) {
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return a;
+}
+
+// 2^-E for E in [-127, 127] (2^-127 is subnormal).
+__device__ __forceinline__ float inv_pow2(int E) {
+    return __uint_as_float(E < 127 ? (uint32_t)(127 - E) << 23 : 0x400000u);
+}
+
+// E4M3 codes of x * 2^-E for 8 values, as two words.
+__device__ __forceinline__ uint2 e4m3_codes(const float (&x)[8], int E) {
+    const float m = inv_pow2(E);
+    const float2 m2 = make_float2(m, m);
+    uint32_t w[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+        w[p] = (uint32_t)__nv_cvt_float2_to_fp8x2(__fmul2_rn(make_float2(x[2 * p], x[2 * p + 1]), m2), __NV_SATFINITE,
+                                                   __NV_E4M3);
+    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// Stores vector v (8 values, exponent E) of token t: its codes, and its scale byte from the first lane of
+// every four (each four lanes are one block of 32 values).
+__device__ __forceinline__ void mx_store(const float (&x)[8], int E, int64_t t, int v, int H, const MxOut &mx) {
+    __stcs(reinterpret_cast<uint2 *>(mx.q + t * (int64_t)H + (int64_t)v * 8), e4m3_codes(x, E));
+    if ((v & 3) == 0) mx.scale[mx_scale_offset(t, v >> 2, H)] = (uint8_t)(E + 127);
+}
+
+// ---- residual addition + RMSNorm ---------------------------------------------------------------------
+// One CTA per token.  Rows of at most kNT * kV vectors stay in registers (kV loads of each input in flight
+// per thread); longer ones (kV == 0) are read again after the square sum, from L2.
+template <int kNT, int kV, int kBlockLanes>
+__global__ void __launch_bounds__(kNT)
+add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, const uint16_t *__restrict__ gamma, int H,
+                   float eps, uint16_t *R_out, uint16_t *__restrict__ X_out, MxOut mx) {
+    __shared__ double sWarp[kNT / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int64_t t = blockIdx.x, base = t * (int64_t)H;
+    const int tid = threadIdx.x, nvec = H / kVec;
+    constexpr int kRegs = kV > 0 ? kV : 1;
+    uint4 s[kRegs];
+    auto load = [&](int v) {  // bf16(x + residual) of one vector
+        uint4 a = ld_stream(x + base + (int64_t)v * kVec);
+        if (residual != nullptr) {
+            float f[8], r[8];
+            unpack8(a, f);
+            unpack8(__ldcs(reinterpret_cast<const uint4 *>(residual + base + (int64_t)v * kVec)), r);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] += r[e];
+            a = pack8_rn(f);
+        }
+        return a;
+    };
+    auto squares = [&](uint4 a) {
+        float f[8];
+        unpack8(a, f);
+        float q = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q = fmaf(f[e], f[e], q);
+        return q;
+    };
+    double sum = 0.0;
+    if constexpr (kV > 0) {
+#pragma unroll
+        for (int k = 0; k < kV; ++k) {
+            const int v = tid + k * kNT;
+            s[k] = v < nvec ? load(v) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        float q = 0.f;
+#pragma unroll
+        for (int k = 0; k < kV; ++k) q += squares(s[k]);
+        sum = q;
+    } else {
+        for (int v = tid; v < nvec; v += kNT) sum += (double)squares(load(v));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((tid & 31) == 0) sWarp[tid >> 5] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < kNT / 32; ++w) sum += sWarp[w];
+    const double rd = rsqrt(sum / (double)H + (double)eps);
+    const float rh = (float)rd, rl = (float)(rd - (double)rh);
+    auto finish = [&](uint4 a, int v) {
+        const bool on = v < nvec;
+        float f[8], g[8];
+        unpack8(a, f);
+        unpack8(on ? ld_ro(gamma + (int64_t)v * kVec) : make_uint4(0u, 0u, 0u, 0u), g);
+        if (on && R_out != nullptr) st_stream(R_out + base + (int64_t)v * kVec, a);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float p = f[e] * g[e];  // exact
+            f[e] = fmaf(p, rh, p * rl);
+        }
+        const uint4 y = pack8_rn(f);
+        if (on && X_out != nullptr) st_stream(X_out + base + (int64_t)v * kVec, y);
+        if (mx.q != nullptr) {
+            unpack8(y, f);
+            float amax = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+            amax = group_max<kBlockLanes>(on ? amax : 0.f);
+            if (on) mx_store(f, mx_exp(amax, mx.mode), t, v, H, mx);
+        }
+    };
+    if constexpr (kV > 0) {
+#pragma unroll
+        for (int k = 0; k < kV; ++k)
+            if (k == 0 || k * kNT < nvec) finish(s[k], tid + k * kNT);
+    } else {
+        for (int v0 = 0; v0 < nvec; v0 += kNT) {  // whole groups of lanes: the maxima are exchanged
+            const int v = v0 + tid;
+            finish(v < nvec ? load(v) : make_uint4(0u, 0u, 0u, 0u), v);
+        }
+    }
+}
+
+// ---- SwiGLU ------------------------------------------------------------------------------------------
+__device__ __forceinline__ float silu_mul(float a, float b) { return a / (1.f + expf(-a)) * b; }
+__device__ __noinline__ double silu_mul_f64(float a, float b) { return (double)a / (1.0 + exp(-(double)a)) * (double)b; }
+
+// Whether fp32 cannot say on which side of a border between two codes u = x * 2^-E lies: its 20 bits below
+// E4M3's significand within kNear of one half.  (Below E4M3's normal range the codes are fixed-point and the
+// test is not exact there; a code off by one of 2^-9 in values of up to 448 is what fp32 leaves.)
+constexpr uint32_t kNear = 16;  // silu_mul is within 16 ulp of 2^-24: expf 2 ulp, three more roundings
+__device__ __forceinline__ bool near_border(float u) {
+    return ((__float_as_uint(u) & 0xFFFFFu) - (0x80000u - kNear)) <= 2 * kNear;
+}
+// The same for a maximum: within kNear of a power of two (or past fp32's range), or of 1.75 times one (mode 1).
+__device__ __forceinline__ bool near_exponent(float a, int mode) {
+    const uint32_t m = __float_as_uint(a) & 0x7FFFFFu;
+    return m + kNear > 0x7FFFFFu || m < kNear || (mode == 1 && m - (0x600000u - kNear) <= 2 * kNear);
+}
+// mx_exp of a value held in fp64 (products beyond fp32's range among them).
+__device__ __noinline__ int mx_exp_f64(double amax, int mode) {
+    if (isinf(amax)) return 120;  // as mx_exp
+    if (!(amax >= 1.1754943508222875e-38)) return -127;  // 2^-126
+    const int e = ilogb(amax);
+    int E = e - 8;
+    if (mode == 1 && amax > scalbn(1.75, e)) E += 1;
+    return E < -127 ? -127 : (E > 127 ? 127 : E);
+}
+
+// One thread per vector of 8 output values; a warp's lanes hold consecutive vectors of one row (rows are
+// padded to whole groups of kBlockLanes lanes).
+template <int kBlockLanes>
+__global__ void __launch_bounds__(256)
+swiglu_kernel(const uint16_t *__restrict__ gu, int64_t T, int F, int lanes_row, MxOut mx) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int64_t n = T * lanes_row;
+    for (int64_t i0 = (int64_t)blockIdx.x * 256; i0 < n; i0 += (int64_t)gridDim.x * 256) {
+        const int64_t i = i0 + threadIdx.x;
+        const int64_t t = i / lanes_row;
+        const int v = (int)(i - t * lanes_row);
+        const bool on = i < n && v * kVec < F;
+        float a[8], b[8], f[8];
+        {
+            const uint16_t *src = gu + t * 2 * (int64_t)F + (int64_t)v * kVec;
+            unpack8(on ? ld_stream(src) : make_uint4(0u, 0u, 0u, 0u), a);
+            unpack8(on ? ld_stream(src + F) : make_uint4(0u, 0u, 0u, 0u), b);
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f[e] = silu_mul(a[e], b[e]);
+            amax = fmaxf(amax, fabsf(f[e]));
+        }
+        amax = group_max<kBlockLanes>(amax);
+        int E = mx_exp(amax, mx.mode);
+        if (__any_sync(0xffffffffu, near_exponent(amax, mx.mode) && on)) {
+            double m = 0.0;
+            for (int e = 0; e < 8; ++e) {
+                const double d = fabs(silu_mul_f64(a[e], b[e]));
+                m = d > m ? d : m;
+            }
+#pragma unroll
+            for (int o = 1; o < kBlockLanes; o <<= 1) {
+                const double d = __shfl_xor_sync(0xffffffffu, m, o);
+                m = d > m ? d : m;
+            }
+            E = mx_exp_f64(m, mx.mode);
+        }
+        if (!on) continue;
+        const float sc = inv_pow2(E);
+        bool near = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) near |= near_border(f[e] * sc);
+        if (near) {
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {
+                // the fp64 value, with whatever fp32 drops of it kept as a sticky last bit, rounds to the same code
+                const double d = silu_mul_f64(a[e], b[e]);
+                float h = __double2float_rz(d);
+                if ((double)h != d) h = __uint_as_float(__float_as_uint(h) | 1u);
+                f[e] = fabs(d) > 3.4028234663852886e38 ? (float)d : h;  // past fp32's range: infinite, the largest code
+            }
+        }
+        mx_store(f, E, t, v, F, mx);
+    }
+}
+
+// A launch that may start while the launch before it drains (it waits for that one's results itself).
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kern)(P...), unsigned grid, unsigned block, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    mark_main_kernel(stream, true);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    mark_main_kernel(stream, false);
+    return e;
+}
+
+template <int kNT, int kV>
+cudaError_t launch_norm_nv(const uint16_t *x, const uint16_t *residual, const uint16_t *gamma, int64_t T, int H, float eps,
+                           uint16_t *R_out, uint16_t *X_out, const MxOut &mx, int block, cudaStream_t stream) {
+    auto kern = block == 128 ? add_rmsnorm_kernel<kNT, kV, 16> : add_rmsnorm_kernel<kNT, kV, 4>;
+    return launch_pdl(kern, (unsigned)T, kNT, stream, x, residual, gamma, H, eps, R_out, X_out, mx);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const uint16_t *x, const uint16_t *residual, const uint16_t *gamma, int64_t T, int H,
+                               float eps, uint16_t *R_out, uint16_t *X_out, const MxOut &mx, int block, int num_sms,
+                               cudaStream_t stream) {
+    (void)num_sms;
+    const int nvec = H / kVec;
+    if (nvec <= 256) return launch_norm_nv<256, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
+    if (nvec <= 512) return launch_norm_nv<256, 2>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
+    if (nvec <= 1024) return launch_norm_nv<256, 4>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
+    return launch_norm_nv<512, 0>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
+}
+
+cudaError_t launch_swiglu(const uint16_t *gate_up, int64_t T, int F, const MxOut &mx, int block, int num_sms,
+                          cudaStream_t stream) {
+    const int group = block == 128 ? 16 : 4;
+    const int lanes_row = (F / kVec + group - 1) / group * group;
+    const int64_t want = (T * lanes_row + 255) / 256, cap = (int64_t)num_sms * 8;
+    auto kern = block == 128 ? swiglu_kernel<16> : swiglu_kernel<4>;
+    return launch_pdl(kern, (unsigned)std::min(want, cap), 256, stream, gate_up, T, F, lanes_row, mx);
+}
+
+}  // namespace mhc

@@ -14,6 +14,8 @@
 #include "mhc.h"
 #include "mhc_kernels.h"
 
+static_assert(MHC_MAX_EXPERTS == mhc::kMaxExperts, "expert bound");
+
 namespace {
 
 thread_local std::string g_last_error;
@@ -712,6 +714,156 @@ mhc_status mhc_pre_prepacked(const mhc_bf16 *residual, const float *phi, const v
                         hc_norm_eps, rmsnorm_eps, hc_post_scale, sinkhorn_eps, sinkhorn_iters, nullptr, layer_in_out,
                         pre_mix_out, post_mix_out, comb_res_mix_out, workspace, workspace_bytes, stream, false,
                         nullptr, nullptr, 0, nullptr, packed_phi);
+}
+
+namespace {
+
+mhc_status check_mx(const uint8_t *codes, const uint8_t *scales, const char *codes_name, int64_t cols, int scale_mode,
+                    int scale_block) {
+    mhc_status st;
+    if (cols % 32 != 0) return fail(MHC_ERR_INVALID_ARG, "the MXFP8 output needs a row of a multiple of 32 values (%lld)", (long long)cols);
+    if (scale_mode != MHC_MX_SCALE_FLOOR && scale_mode != MHC_MX_SCALE_CEIL)
+        return fail(MHC_ERR_INVALID_ARG, "unknown MXFP8 scale mode %d", scale_mode);
+    if (scale_block != MHC_MX_BLOCK_32 && scale_block != MHC_MX_BLOCK_128)
+        return fail(MHC_ERR_INVALID_ARG, "scale_block must be 32 or 128, not %d", scale_block);
+    if ((st = check_ptrs({{codes, codes_name}})) != MHC_OK) return st;
+    if (scales == nullptr) return fail(MHC_ERR_INVALID_ARG, "the scales of %s are NULL", codes_name);
+    return MHC_OK;
+}
+
+mhc_status check_overlaps(std::initializer_list<std::pair<Span, const char *>> outs, std::initializer_list<Span> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span &i : ins)
+            if (overlap(o->first, i)) return fail(MHC_ERR_INVALID_ARG, "%s overlaps an input", o->second);
+        for (auto q = o + 1; q != outs.end(); ++q)
+            if (overlap(o->first, q->first)) return fail(MHC_ERR_INVALID_ARG, "%s overlaps %s", o->second, q->second);
+    }
+    return MHC_OK;
+}
+
+// Common body of the two products (expert_offsets == nullptr: one weight, E == 1).
+mhc_status run_linear(const uint8_t *x, const uint8_t *x_scales, int64_t R, const int32_t *rows, int64_t M,
+                      const int32_t *expert_offsets, int64_t E, const uint8_t *w, const void *w_scales, int w_scale_type,
+                      int64_t K, int64_t N, void *out, int out_type, void *workspace, size_t workspace_bytes, void *stream,
+                      bool experts) {
+    mhc_status st;
+    if (M < 0 || M > MHC_MAX_TOKENS || R < 0 || R > MHC_MAX_TOKENS)
+        return fail(MHC_ERR_INVALID_ARG, "%lld rows of output, %lld of x: outside [0, %d]", (long long)M, (long long)R, MHC_MAX_TOKENS);
+    if (K < 32 || K > MHC_MAX_HIDDEN || K % 32 != 0)
+        return fail(MHC_ERR_INVALID_ARG, "K=%lld must be a multiple of 32 in [32, %d]", (long long)K, MHC_MAX_HIDDEN);
+    if (N < 8 || N > MHC_MAX_LINEAR_OUT || N % 8 != 0)
+        return fail(MHC_ERR_INVALID_ARG, "N=%lld must be a multiple of 8 in [8, %d]", (long long)N, MHC_MAX_LINEAR_OUT);
+    if (E < 1 || E > MHC_MAX_EXPERTS) return fail(MHC_ERR_INVALID_ARG, "E=%lld outside [1, %d]", (long long)E, MHC_MAX_EXPERTS);
+    if (w_scale_type != MHC_SCALE_UE8M0 && w_scale_type != MHC_SCALE_F32)
+        return fail(MHC_ERR_INVALID_ARG, "unknown weight scale type %d", w_scale_type);
+    if (out_type != MHC_OUT_BF16 && out_type != MHC_OUT_F32) return fail(MHC_ERR_INVALID_ARG, "unknown output type %d", out_type);
+    if (M == 0) return MHC_OK;
+    if (R == 0) return fail(MHC_ERR_INVALID_ARG, "x has no rows");
+    if (rows == nullptr && R != M) return fail(MHC_ERR_INVALID_ARG, "without rows x has as many rows as out (%lld, %lld)", (long long)R, (long long)M);
+    if ((st = check_ptrs({{x, "x_fp8"}, {x_scales, "x_scales"}, {w, "w_fp8"}, {w_scales, "w_scales"}, {out, "out"}})) != MHC_OK)
+        return st;
+    if (experts && (st = check_ptrs({{expert_offsets, "expert_offsets"}})) != MHC_OK) return st;
+    if (rows != nullptr && (st = check_ptrs({{rows, "rows"}})) != MHC_OK) return st;
+    if (workspace == nullptr) return fail(MHC_ERR_WORKSPACE, "workspace is NULL");
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(MHC_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    if (workspace_bytes < mhc::kControlBytes)
+        return fail(MHC_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, mhc::kControlBytes);
+    const size_t blocks = (size_t)E * (size_t)((N + 127) / 128) * (size_t)((K + 127) / 128);
+    if ((st = check_overlaps({{{out, (size_t)M * N * (out_type == MHC_OUT_F32 ? 4 : 2)}, "out"},
+                              {{workspace, mhc::kControlBytes}, "workspace"}},
+                             {{x, (size_t)R * K}, {x_scales, mx_scale_bytes(R, K)}, {w, (size_t)E * N * K},
+                              {w_scales, blocks * (w_scale_type == MHC_SCALE_F32 ? 4 : 1)}, {rows, rows != nullptr ? (size_t)M * 4 : 0},
+                              {expert_offsets, experts ? (size_t)(E + 1) * 4 : 0}})) != MHC_OK)
+        return st;
+    Device dev;
+    if ((st = current_device(dev)) != MHC_OK) return st;
+    mhc::LinearArgs a{};
+    a.x = x; a.x_scales = x_scales; a.w = w; a.w_scales = w_scales; a.rows = rows; a.offsets = expert_offsets; a.out = out;
+    a.M = M; a.R = R; a.N = (int)N; a.K = (int)K; a.E = (int)E;
+    a.w_scales_f32 = w_scale_type == MHC_SCALE_F32;
+    a.out_f32 = out_type == MHC_OUT_F32;
+    a.status = static_cast<unsigned int *>(workspace);
+    cudaError_t e = mhc::launch_linear(a, dev.sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
+    g_launches = 1;
+    return MHC_OK;
+}
+
+}  // namespace
+
+mhc_status mhc_add_rmsnorm_mxfp8(const mhc_bf16 *x, const mhc_bf16 *residual, const mhc_bf16 *rmsnorm_weight, int64_t T,
+                                 int64_t H, float rmsnorm_eps, mhc_bf16 *residual_out, mhc_bf16 *layer_in_out,
+                                 uint8_t *layer_in_fp8, uint8_t *layer_in_scales, int scale_mode, int scale_block,
+                                 void *stream) {
+    mhc_status st;
+    g_launches = 0;
+    if ((st = check_sizes(T, H)) != MHC_OK) return st;
+    if (!std::isfinite(rmsnorm_eps) || rmsnorm_eps < 0.f)
+        return fail(MHC_ERR_INVALID_ARG, "rmsnorm_eps must be finite and >= 0");
+    if (T == 0) return MHC_OK;
+    if ((st = check_ptrs({{x, "x"}, {rmsnorm_weight, "rmsnorm_weight"}})) != MHC_OK) return st;
+    if (residual != nullptr && (st = check_ptrs({{residual, "residual"}})) != MHC_OK) return st;
+    if (residual_out != nullptr) {
+        if (residual == nullptr) return fail(MHC_ERR_INVALID_ARG, "residual_out without residual");
+        if ((st = check_ptrs({{residual_out, "residual_out"}})) != MHC_OK) return st;
+    }
+    const bool mx = layer_in_fp8 != nullptr || layer_in_scales != nullptr;
+    if (layer_in_out != nullptr && (st = check_ptrs({{layer_in_out, "layer_in_out"}})) != MHC_OK) return st;
+    if (!mx && layer_in_out == nullptr) return fail(MHC_ERR_INVALID_ARG, "layer_in_out and layer_in_fp8 are NULL");
+    if (mx && (st = check_mx(layer_in_fp8, layer_in_scales, "layer_in_fp8", H, scale_mode, scale_block)) != MHC_OK) return st;
+    const size_t n = (size_t)T * (size_t)H;
+    const bool in_place = residual_out != nullptr && residual_out == residual;
+    if ((st = check_overlaps({{{residual_out, n * 2}, "residual_out"}, {{layer_in_out, n * 2}, "layer_in_out"},
+                              {{layer_in_fp8, n}, "layer_in_fp8"}, {{layer_in_scales, mx ? mx_scale_bytes(T, H) : 0}, "layer_in_scales"}},
+                             {{x, n * 2}, {in_place ? nullptr : residual, n * 2}, {rmsnorm_weight, (size_t)H * 2}})) != MHC_OK)
+        return st;
+    Device dev;
+    if ((st = current_device(dev)) != MHC_OK) return st;
+    cudaError_t e = mhc::launch_add_rmsnorm(x, residual, rmsnorm_weight, T, (int)H, rmsnorm_eps, residual_out, layer_in_out,
+                                            mhc::MxOut{layer_in_fp8, layer_in_scales, scale_mode}, mx ? scale_block : 32,
+                                            dev.sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
+    g_launches = 1;
+    return MHC_OK;
+}
+
+mhc_status mhc_swiglu_mxfp8(const mhc_bf16 *gate_up, int64_t T, int64_t F, uint8_t *act_fp8, uint8_t *act_scales,
+                            int scale_mode, int scale_block, void *stream) {
+    mhc_status st;
+    g_launches = 0;
+    if ((st = check_sizes(T, F)) != MHC_OK) return st;
+    if (T == 0) return MHC_OK;
+    if ((st = check_ptrs({{gate_up, "gate_up"}})) != MHC_OK) return st;
+    if ((st = check_mx(act_fp8, act_scales, "act_fp8", F, scale_mode, scale_block)) != MHC_OK) return st;
+    const size_t n = (size_t)T * (size_t)F;
+    if ((st = check_overlaps({{{act_fp8, n}, "act_fp8"}, {{act_scales, mx_scale_bytes(T, F)}, "act_scales"}}, {{gate_up, n * 4}})) != MHC_OK)
+        return st;
+    Device dev;
+    if ((st = current_device(dev)) != MHC_OK) return st;
+    cudaError_t e = mhc::launch_swiglu(gate_up, T, (int)F, mhc::MxOut{act_fp8, act_scales, scale_mode}, scale_block, dev.sms,
+                                       static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
+    g_launches = 1;
+    return MHC_OK;
+}
+
+size_t mhc_linear_workspace_size(void) { return mhc::kControlBytes; }
+
+mhc_status mhc_linear_mxfp8(const uint8_t *x_fp8, const uint8_t *x_scales, const uint8_t *w_fp8, const void *w_scales,
+                            int w_scale_type, int64_t T, int64_t K, int64_t N, void *out, int out_type, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    g_launches = 0;
+    return run_linear(x_fp8, x_scales, T, nullptr, T, nullptr, 1, w_fp8, w_scales, w_scale_type, K, N, out, out_type,
+                      workspace, workspace_bytes, stream, false);
+}
+
+mhc_status mhc_expert_linear_mxfp8(const uint8_t *x_fp8, const uint8_t *x_scales, int64_t R, const int32_t *rows, int64_t M,
+                                   const int32_t *expert_offsets, int64_t E, const uint8_t *w_fp8, const void *w_scales,
+                                   int w_scale_type, int64_t K, int64_t N, void *out, int out_type, void *workspace,
+                                   size_t workspace_bytes, void *stream) {
+    g_launches = 0;
+    return run_linear(x_fp8, x_scales, R, rows, M, expert_offsets, E, w_fp8, w_scales, w_scale_type, K, N, out, out_type,
+                      workspace, workspace_bytes, stream, true);
 }
 
 mhc_status mhc_set_schedule(int schedule) {

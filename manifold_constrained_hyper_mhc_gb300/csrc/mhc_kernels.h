@@ -146,6 +146,31 @@ bool bcast_supported(int64_t T, int64_t H);
 size_t bcast_workspace_bytes(int64_t T, int64_t H);  // after the control block
 cudaError_t launch_bcast_pre(const BcastArgs &a, unsigned int *status, void *scratch, int num_sms, cudaStream_t stream);
 
+// s = bf16(x + residual) (residual == nullptr: s = x), RMSNorm(s) * gamma as bf16 and MXFP8
+// (kernels_norm.cu).  Any of R_out, X_out and mx.q may be nullptr; mx needs H % 32 == 0.  block: values
+// per scale, 32 or 128.
+cudaError_t launch_add_rmsnorm(const uint16_t *x, const uint16_t *residual, const uint16_t *gamma, int64_t T, int H,
+                               float eps, uint16_t *R_out, uint16_t *X_out, const MxOut &mx, int block, int num_sms,
+                               cudaStream_t stream);
+// silu(gate) * up of [T][2F] rows (gate first) as MXFP8 [T][F] (kernels_norm.cu); F % 32 == 0.
+cudaError_t launch_swiglu(const uint16_t *gate_up, int64_t T, int F, const MxOut &mx, int block, int num_sms,
+                          cudaStream_t stream);
+
+// The 8-bit matrix products (kernels_linear.cu).
+constexpr int kMaxExperts = 1024;
+struct LinearArgs {
+    const uint8_t *x, *x_scales, *w;  // [R][K] codes and their scale tiles, [E][N][K] codes
+    const void *w_scales;             // [E][ceil(N/128)][ceil(K/128)]: UE8M0 bytes, or fp32 (w_scales_f32)
+    const int32_t *rows;              // [M] row of x of each output row (nullptr: the same row; R == M)
+    const int32_t *offsets;           // [E + 1] first output row of each expert (nullptr: one weight, E == 1)
+    void *out;                        // [M][N] bf16, or fp32 (out_f32)
+    int64_t M, R;
+    int N, K, E;
+    bool w_scales_f32, out_f32;
+    unsigned int *status;             // bit 0 is set when a bounded wait gives up
+};
+cudaError_t launch_linear(const LinearArgs &a, int num_sms, cudaStream_t stream);
+
 cudaError_t launch_post(const uint16_t *R, const uint16_t *Y, const float *prev_post,
                         const float *prev_comb, int64_t T, int H, uint16_t *R_out, int num_sms,
                         cudaStream_t stream);
