@@ -13,8 +13,8 @@
 //   - fp32 weight scales (kWF32) are not representable there: the operand's scales are 1, every k block
 //     gets its own accumulator, and the epilogue warps add it to fp32 registers times the block's scale.
 //
-// Roles of a CTA: warp 0 copies operands, warp 1 issues the MMAs, warps 2 and 3 load scales (3 also owns the
-// tensor memory), the others are the epilogue.  They hand work over through mbarriers: a ring of stages (one
+// Roles of a CTA: warp 0 copies operands, warp 1 issues the MMAs, warp 2 (and 3) loads scales and owns the
+// tensor memory, the others are the epilogue (and copy gathered rows).  They hand work over through mbarriers: a ring of stages (one
 // k block each) and two accumulators, so one tile's epilogue overlaps the next tile's products.
 //
 // Few tiles (decode) are split over k in a cluster: each CTA of the cluster sums its range, then the ranges
@@ -42,41 +42,50 @@ namespace {
 using namespace ptx;
 
 constexpr int kBM = 128;       // output channels per CTA (the MMA's M; one weight scale block)
-constexpr int kBK = 128;       // k values per stage (one 128-byte swizzled row; one weight scale block)
-constexpr int kSfBlocks = 4;   // k blocks per chunk of scales
-constexpr int kGatherWarps = 3;
-constexpr int kSfSlots = 3;    // chunks in the scales' ring
+constexpr int kBK = 128;       // k values per block (one 128-byte swizzled row; one weight scale block)
+constexpr int kSB = 2;         // k blocks per stage: each has its own barriers, but the MMA warp tests and issues a stage at
+                               // a time (its waits and loop cost about 350 cycles, nearly a block's MMAs of the largest tile)
+constexpr int kSF = 4;         // k blocks per chunk of scales, and the chunks of their ring (a chunk takes a memory latency, a
+constexpr int kSfSlots = 3;    // fence and an arrival at the pair's leader, about 2,000 cycles, whatever its size)
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s per wait
 constexpr int kSmemMax = 227 * 1024;
 // More than half of an SM's shared memory, always: two CTAs that allocate tensor memory then never share an
 // SM, so no allocation waits for another (clusters that wait for each other's columns could block forever).
 constexpr int kSmemMin = kSmemMax / 2 + 1024;
 
-template <int TN, int CG, bool kGather>
+template <int TN, int CG, bool kWF32, bool kGather>
 struct Cfg {
-    static constexpr int EW = 4 * CG;                          // epilogue warps
-    static constexpr int GW = kGather ? kGatherWarps : 0;      // extra copy warps, the last ones
-    static constexpr int W_GATHER = 4 + EW;
+    // Epilogue warps: SH of them share the columns of each lane quadrant.  With fp32 weight scales they read every
+    // accumulator of one k block, so there are more of them, each with at most 64 columns (and sums in registers).
+    static constexpr int SH = kWF32 ? (TN + 63) / 64 : CG;
+    static constexpr int EW = 4 * SH;
+    static constexpr int SW = kWF32 ? 1 : 2;                   // warps that load scales
+    static constexpr int W_EPI = 2 + SW, W_GATHER = W_EPI + EW;
+    static constexpr int GW = !kGather ? 0 : kWF32 ? 1 : 3;    // extra warps that copy gathered rows, the last ones
     static constexpr int NT = 32 * (W_GATHER + GW);            // threads
     static constexpr int NB = (TN + 127) / 128;                // token scale atoms (128 rows x 4 bytes)
-    static constexpr int A_BYTES = kBM * kBK;
     static constexpr int TNC = TN / CG;                        // token rows this CTA copies
-    static constexpr int B_BYTES = TNC * kBK;
-    static constexpr int SF_BYTES = 512 * (1 + NB);            // weight atom, token atoms
+    static constexpr int A_BLOCK = kBM * kBK, B_BLOCK = TNC * kBK, SF_BLOCK = 512 * (1 + NB);  // bytes of one k block
+    static constexpr int A_BYTES = kSB * A_BLOCK, B_BYTES = kSB * B_BLOCK, SF_BYTES = kSF * SF_BLOCK;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int SF_CHUNK = kSfBlocks * SF_BYTES;      // scales come in chunks of k blocks, in their own ring
-    static constexpr int FIXED = 1024 /*alignment*/ + 1024 /*barriers*/ + (kMaxExperts + 1) * 4 + kSfSlots * SF_CHUNK;
+    static constexpr int FIXED = 1024 /*alignment*/ + 1024 /*barriers*/ + (kMaxExperts + 1) * 4 + kSfSlots * SF_BYTES;
     static constexpr int NS_FIT = (kSmemMax - FIXED) / STAGE;
-    static constexpr int NS = NS_FIT > 10 ? 10 : NS_FIT;       // ring stages
-    static constexpr int CW = (TN / 16 + CG - 1) / CG;         // 16-column chunks of a warp (CG warps share the columns)
-    static constexpr int COL_SFA = 2 * TN;                     // tensor memory columns: accumulators, scales (two sets)
-    static constexpr int COL_SFB = COL_SFA + 8;
-    static constexpr int COLS_USED = COL_SFB + 8 * NB;
+    static constexpr int NS = NS_FIT > 6 ? 6 : NS_FIT;         // ring stages
+    static constexpr int CC = !kWF32 || TN < 32 ? 16 : 32;     // columns per tensor-memory load
+    static constexpr int CW = (TN / CC + SH - 1) / SH;         // loads of a warp
+    // Accumulators: one being summed, one being stored; with fp32 weight scales one per k block in flight (the hand-over
+    // to the epilogue and back takes longer than a k block's MMAs).
+    static constexpr int NA = !kWF32 ? 2 : TN <= 64 ? 4 : TN > 160 ? 2 : 3;
+    static constexpr int SFA_SETS = kWF32 ? 1 : kSB;           // (fp32 weight scales: the operand's are all ones)
+    static constexpr int COL_SFA = NA * TN;                    // tensor memory columns: accumulators, scales (two sets)
+    static constexpr int COL_SFB = COL_SFA + 4 * SFA_SETS;
+    static constexpr int COLS_USED = COL_SFB + kSB * 4 * NB;
     static constexpr int COLS = COLS_USED <= 64 ? 64 : COLS_USED <= 128 ? 128 : COLS_USED <= 256 ? 256 : 512;
     static constexpr int SMEM = FIXED + NS * STAGE;
     static_assert(COLS_USED <= 512, "tensor memory");
     static_assert(TN % (16 * CG) == 0 && TN <= 256 && TNC % 8 == 0, "MMA N");
-    static_assert(NS >= 3, "stages");
+    static_assert(NS >= 3 && 2 * kSB * NS + 2 * kSfSlots + 2 * NA + 2 <= 1024 / 8, "stages");
+    static_assert(kSF % kSB == 0, "a stage's scales are in one chunk");
 };
 
 struct LinearMaps {
@@ -100,11 +109,30 @@ __device__ __forceinline__ void bwait(uint64_t *bar, uint32_t parity, bool &dead
     mbar_wait_timed(bar, parity, dead, kWaitLimitNs);
 }
 
-// A wait by a whole warp: `dead` stays the same in all lanes.
+// A wait by a whole warp: `dead` stays the same in all lanes.  kEager: back-to-back tests (each suspends for a while by
+// itself), for the warps whose reaction the ring waits for; the others hand the issue slots on.
+template <bool kEager>
 __device__ __forceinline__ void wwait(uint64_t *bar, uint32_t parity, bool &dead) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || dead) return;
-    mbar_wait_timed(bar, parity, dead, kWaitLimitNs);
+    if constexpr (kEager) {
+        const uint64_t t0 = globaltimer_ns();
+        do {
+            for (int i = 0; i < 64; ++i)
+                if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
+        } while (globaltimer_ns() - t0 <= kWaitLimitNs);
+        dead = true;
+    } else {
+        mbar_wait_timed(bar, parity, dead, kWaitLimitNs);
+    }
     dead = __any_sync(0xffffffffu, dead);
+}
+// The waits for a stage's blocks, all tested before any is waited for.
+__device__ __forceinline__ void wwait_blocks(uint64_t *blocks, uint32_t parity, bool &dead) {
+    bool ok = true;
+#pragma unroll
+    for (int h = 0; h < kSB; ++h) ok &= mbar_try_wait(blocks + h, parity);
+    if (__all_sync(0xffffffffu, ok) || dead) return;
+    for (int h = 0; h < kSB; ++h) wwait<true>(blocks + h, parity, dead);
 }
 // One lane of the (converged) warp.  The tensor-core and copy instructions take their operands from uniform
 // registers: loops around them run in the whole warp with values that are the same in every lane, and only the
@@ -260,6 +288,20 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     return v;
 }
 
+// 16 or 32 accumulator columns of this warp's lane quadrant.
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
 // A tile of the schedule: weight e, token rows [m0, m0 + valid) (at most TN), output channels from n0 (this CTA's
 // 128 of the pair's 256).  The MMA's N is what the tile has, in steps of 16 (32 for a pair, of which each CTA copies
 // half the rows).
@@ -318,16 +360,16 @@ __device__ __forceinline__ void store_out(const LinearParams &p, int64_t m, int 
 }
 
 template <int TN, int CG, bool kWF32, bool kGather>
-__global__ void __launch_bounds__(Cfg<TN, CG, kGather>::NT, 1)
+__global__ void __launch_bounds__(Cfg<TN, CG, kWF32, kGather>::NT, 1)
 linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
-    using C = Cfg<TN, CG, kGather>;
+    using C = Cfg<TN, CG, kWF32, kGather>;
     constexpr int NS = C::NS;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char *sA = smem, *sB = sA + NS * C::A_BYTES, *sSF = sB + NS * C::B_BYTES;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sSF + kSfSlots * C::SF_CHUNK);
-    uint64_t *full = bars, *empty = full + NS, *full_sf = empty + NS, *empty_sf = full_sf + kSfSlots, *acc_full = empty_sf + kSfSlots,
-             *acc_empty = acc_full + 2, *drained = acc_empty + 2;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sSF + kSfSlots * C::SF_BYTES);
+    uint64_t *full = bars, *empty = full + kSB * NS, *full_sf = empty + kSB * NS, *empty_sf = full_sf + kSfSlots,
+             *acc_full = empty_sf + kSfSlots, *acc_empty = acc_full + C::NA, *drained = acc_empty + C::NA;
     uint32_t *sTmem = reinterpret_cast<uint32_t *>(drained + 1);
     int *sCum = reinterpret_cast<int *>(reinterpret_cast<unsigned char *>(bars) + 1024);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -339,7 +381,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
     bool dead = false;
 
     if (warp == 1 && lane == 0) {
-        for (int i = 0; i < NS; ++i) {
+        for (int i = 0; i < kSB * NS; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
@@ -347,14 +389,14 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
             mbar_init(&full_sf[i], CG);
             mbar_init(&empty_sf[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::NA; ++i) {
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], CG * C::EW);
         }
         mbar_init(drained, 1);
         fence_mbar_init();
     }
-    if (warp == 3) {
+    if (warp == 2) {
         tmem_take<CG>(sTmem, C::COLS);
     }
     // up to here only this CTA's own memory; from here on the previous launch's results
@@ -389,8 +431,10 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
     const uint32_t tbase = *sTmem;
     const int64_t ntiles = (p.offsets != nullptr ? (int64_t)sCum[p.E] : nT) * nN;
     const int64_t first = blockIdx.x / (S * CG), step = gridDim.x / (S * CG);
-    // this CTA's share of the k blocks
-    const int kb0 = (int)((int64_t)nKB * rank / S), kb1 = (int)((int64_t)nKB * (rank + 1) / S);
+    // this CTA's share of the stages, and of their k blocks
+    const int nKS = (nKB + kSB - 1) / kSB;
+    const int ks0 = (int)((int64_t)nKS * rank / S), ks1 = (int)((int64_t)nKS * (rank + 1) / S);
+    const int kb0 = ks0 * kSB, kb1 = min(ks1 * kSB, nKB);
 
     if (warp == 0 || warp >= C::W_GATHER) {
         // ================================ operand copies (gathered rows: by the extra warps too)
@@ -399,7 +443,8 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
         constexpr int kRows4Part = (kRows4 + kParts - 1) / kParts;
         const int part = warp == 0 ? 0 : warp - C::W_GATHER + 1;
         Ring<NS> st;
-        int it = 0;
+        int last_st = -1;  // the last block copied, and its phase
+        uint32_t last_ph = 0;
         for (int64_t i = first; i < ntiles && !dead; i += step) {
             const Tile t = tile_at<TN, CG>(i, p, sCum, nN, nT, pair);
             const int q0 = CG == 1 ? 0 : pair * (t.width<CG>() / 2);  // this CTA's part of the tile's rows
@@ -419,75 +464,114 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) r[g][j] = __shfl_sync(0xffffffffu, mine[j], (part + g * kParts) & 31);
             }
-            for (int kb = kb0; kb < kb1; ++kb, ++it, st.next()) {
-                wwait(&empty[st.s], st.ph ^ 1u, dead);
-                if (dead) break;
-                const uint32_t bar = lead<CG>(&full[st.s]);
-                unsigned char *da = sA + st.s * C::A_BYTES, *db = sB + st.s * C::B_BYTES;
-                if (part == 0 && elect_one()) {
-                    // the leader expects the pair's bytes (the peer's may land before: the phase waits for this arrival)
-                    if (pair == 0) mbar_arrive_expect_tx(&full[st.s], CG * (C::A_BYTES + C::B_BYTES));
-                    load_w<CG>(da, &maps.w, kb * kBK, t.n0, t.e, bar);
-                    if (!kGather) load_x<CG>(db, &maps.x, kb * kBK, (int)t.m0 + q0, bar);
-                }
-                if (kGather && elect_one()) {
+            for (int ks = ks0; ks < ks1 && !dead; ++ks, st.next()) {
 #pragma unroll
-                    for (int g = 0; g < kRows4Part; ++g)
-                        if (part + g * kParts < kRows4) load_x_rows<CG>(db + (part + g * kParts) * 512, &maps.x, kb * kBK, r[g], bar);
+                for (int h = 0; h < kSB; ++h) {
+                    const int at = st.s * kSB + h, x = (ks * kSB + h) * kBK;
+                    wwait<true>(&empty[at], st.ph ^ 1u, dead);
+                    if (dead) break;
+                    const uint32_t bar = lead<CG>(&full[at]);
+                    if (x >= p.K) {  // no such block: nothing to copy
+                        if (part == 0 && pair == 0 && elect_one()) mbar_arrive(&full[at]);
+                        continue;
+                    }
+                    unsigned char *da = sA + st.s * C::A_BYTES + h * C::A_BLOCK, *db = sB + st.s * C::B_BYTES + h * C::B_BLOCK;
+                    if (part == 0 && elect_one()) {
+                        // the leader expects the pair's bytes (the peer's may land before: the phase waits for this arrival)
+                        if (pair == 0) mbar_arrive_expect_tx(&full[at], CG * (C::A_BLOCK + C::B_BLOCK));
+                        load_w<CG>(da, &maps.w, x, t.n0, t.e, bar);
+                        if (!kGather) load_x<CG>(db, &maps.x, x, (int)t.m0 + q0, bar);
+                    }
+                    if (kGather && elect_one()) {
+#pragma unroll
+                        for (int g = 0; g < kRows4Part; ++g)
+                            if (part + g * kParts < kRows4) load_x_rows<CG>(db + (part + g * kParts) * 512, &maps.x, x, r[g], bar);
+                    }
+                    last_st = at;
+                    last_ph = st.ph;
                 }
             }
         }
         if (dead) {  // the copies in flight must land before the CTA's shared memory goes
-            bool gave_up = false;  // (a pair's land on its leader's barriers; the cluster barrier below holds the peer)
-            for (int j = it > NS ? it - NS : 0; j < it && pair == 0; ++j) bwait(&full[j % NS], (uint32_t)((j / NS) & 1), gave_up);
+            // (a pair's land on its leader's barriers; the cluster barrier below holds the peer).  Barrier by barrier, the
+            // last phase that was armed; those of a phase that has long passed return at once.
+            bool gave_up = false;
+            for (int j = 0; j < kSB * NS && last_st >= 0 && pair == 0; ++j) bwait(&full[j], j <= last_st ? last_ph : last_ph ^ 1u, gave_up);
         }
     } else if (warp == 1) {
         // ================================ MMA issue
         if (pair == 0) {
             Ring<NS> st;
-            Ring<2> ac;
+            Ring<C::NA> ac;
             Ring<kSfSlots> sc;
-            Ring<2> sf;  // the two sets of scale columns
+            bool have_sfa = false;
             const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(sA), 1024), db0 = sdesc_kmajor_sw128(smem_u32(sB), 1024),
                            ds0 = sdesc_scales(smem_u32(sSF));
             for (int64_t i = first; i < ntiles && !dead; i += step) {
                 const uint32_t idesc = idesc_mxf8(kBM * CG, tile_at<TN, CG>(i, p, sCum, nN, nT, pair).template width<CG>());
-                int left = kSfBlocks;  // k blocks left in the chunk of scales
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    const bool fresh = kWF32 || kb == kb0;  // starts an accumulator
-                    if (fresh) wwait(&acc_empty[ac.s], ac.ph ^ 1u, dead);
-                    if (left == kSfBlocks) wwait(&full_sf[sc.s], sc.ph, dead);
-                    wwait(&full[st.s], st.ph, dead);
+                if (!kWF32) wwait<true>(&acc_empty[ac.s], ac.ph ^ 1u, dead);
+                int in_chunk = 0;  // k blocks of the chunk of scales that are used
+                for (int ks = ks0; ks < ks1; ++ks) {
+                    if (in_chunk == 0) wwait<true>(full_sf + sc.s, sc.ph, dead);
+                    wwait_blocks(full + st.s * kSB, st.ph, dead);
                     if (dead) break;
                     tmem_fence_after();
-                    const bool last = kb + 1 == kb1, chunk_done = last || left == 1;
-                    const uint32_t sfa = tbase + C::COL_SFA + 4 * sf.s, sfb = tbase + C::COL_SFB + 4 * C::NB * sf.s;
-                    const uint64_t ds = ds0 + (uint64_t)((sc.s * C::SF_CHUNK + (kSfBlocks - left) * C::SF_BYTES) >> 4);
-                    const uint64_t a = da0 + (uint64_t)((st.s * C::A_BYTES) >> 4), b = db0 + (uint64_t)((st.s * C::B_BYTES) >> 4);
-                    const uint32_t d = tbase + (uint32_t)(ac.s * TN);
-                    const int nk = min(4, (p.K - kb * kBK) / 32);  // past K the scale bytes are padding: no MMA there
-                    if (elect_one()) {
-                        tmem_cp_scales<CG>(sfa, ds);
+                    const bool last = ks + 1 == ks1, chunk_done = last || in_chunk + kSB == kSF;
+                    const uint64_t ds = ds0 + (uint64_t)((sc.s * C::SF_BYTES + in_chunk * C::SF_BLOCK) >> 4), a = da0 + (uint64_t)((st.s * C::A_BYTES) >> 4),
+                                   b = db0 + (uint64_t)((st.s * C::B_BYTES) >> 4);
+                    // the stage's k steps of 32 inside K: past it the scale bytes are padding, so no MMA there
+                    const int nk = min(4 * kSB, (p.K - ks * kSB * kBK) / 32);
+                    // one k block: its scales to tensor memory, then its MMAs (in order in the tensor pipe)
+                    auto block = [&](int h, uint32_t d, bool fresh) {
+                        const uint32_t sfa = tbase + C::COL_SFA + (kWF32 ? 0 : 4 * h), sfb = tbase + C::COL_SFB + 4 * C::NB * h;
+                        const uint64_t dsh = ds + (uint64_t)(h * C::SF_BLOCK >> 4);
+                        if (!kWF32 || !have_sfa) tmem_cp_scales<CG>(sfa, dsh);  // fp32 weight scales: all ones, once
 #pragma unroll
-                        for (int n = 0; n < C::NB; ++n) tmem_cp_scales<CG>(sfb + 4 * n, ds + 32 * (1 + n));
+                        for (int n = 0; n < C::NB; ++n) tmem_cp_scales<CG>(sfb + 4 * n, dsh + 32 * (1 + n));
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (k < nk)
-                                umma_mxf8<CG>(d, a + 2 * k, b + 2 * k, idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), sfa, sfb,
-                                              (uint32_t)(!fresh || k > 0));
-                        commit<CG>(&empty[st.s]);
-                        if (chunk_done) commit<CG>(&empty_sf[sc.s]);
-                        if (kWF32 || last) commit<CG>(&acc_full[ac.s]);
+                            if (4 * h + k < nk)
+                                umma_mxf8<CG>(d, a + (uint64_t)((h * C::A_BLOCK >> 4) + 2 * k), b + (uint64_t)((h * C::B_BLOCK >> 4) + 2 * k),
+                                              idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), sfa, sfb, (uint32_t)(!fresh || k > 0));
+                    };
+                    if constexpr (kWF32) {
+#pragma unroll
+                        for (int h = 0; h < kSB; ++h) {
+                            if (4 * h >= nk) break;
+                            wwait<true>(&acc_empty[ac.s], ac.ph ^ 1u, dead);
+                            if (dead) break;
+                            tmem_fence_after();
+                            if (elect_one()) {
+                                block(h, tbase + (uint32_t)(ac.s * TN), true);
+                                commit<CG>(&acc_full[ac.s]);
+                                commit<CG>(&empty[st.s * kSB + h]);
+                                if (h + 1 < kSB && 4 * (h + 1) >= nk) commit<CG>(&empty[st.s * kSB + h + 1]);
+                                if (chunk_done && (h + 1 == kSB || 4 * (h + 1) >= nk)) commit<CG>(&empty_sf[sc.s]);
+                            }
+                            __syncwarp();
+                            have_sfa = true;
+                            ac.next();
+                        }
+                    } else {
+                        if (elect_one()) {
+#pragma unroll
+                            for (int h = 0; h < kSB; ++h) {
+                                if (4 * h < nk) block(h, tbase + (uint32_t)(ac.s * TN), h == 0 && ks == ks0);
+                                commit<CG>(&empty[st.s * kSB + h]);
+                            }
+                            if (chunk_done) commit<CG>(&empty_sf[sc.s]);
+                            if (last) commit<CG>(&acc_full[ac.s]);
+                        }
                     }
                     __syncwarp();
-                    if (kWF32 || last) ac.next();
-                    if (--left == 0 || last) {
-                        left = kSfBlocks;
+                    in_chunk += kSB;
+                    if (chunk_done) {
+                        in_chunk = 0;
                         sc.next();
                     }
-                    sf.next();
                     st.next();
                 }
+                if (!kWF32) ac.next();
             }
             if (dead) {  // the MMAs in flight must end before their operands and accumulators go
                 if (elect_one()) commit<CG>(drained);
@@ -496,12 +580,13 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
             }
         }
         __syncwarp();
-    } else if (warp < 4) {
-        // ================================ scales: the two warps take every other chunk
+    } else if (warp < C::W_EPI) {
+        // ================================ scales: each of the SW warps takes every SW-th chunk
         // A chunk's loads are all in flight in registers before its slot is waited for; then they are written to
-        // shared memory and made visible to the copies with one fence (a fence per k block, with cp.async loads
-        // behind it, cost a memory latency each: 0.7-1.1 us per k block).
-        int ch = 0;
+        // shared memory and made visible to the copies with one fence (cp.async loads with a fence behind each k
+        // block's cost a memory latency each: 0.7-1.1 us per k block).
+        Ring<kSfSlots> sc;
+        int turn = 0;
         for (int64_t i = first; i < ntiles && !dead; i += step) {
             const Tile t = tile_at<TN, CG>(i, p, sCum, nN, nT, pair);
             const int KT = (p.K / 32 + 3) / 4;
@@ -521,45 +606,44 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
             }
             // (the second half of a pair's last tile may lie past N: any scale does, its rows are zeros)
             const uint8_t *ws = reinterpret_cast<const uint8_t *>(p.w_scales) + ((int64_t)t.e * nNB + min(t.n0 / kBM, nNB - 1)) * nKB;
-            for (int kb = kb0; kb < kb1; kb += kSfBlocks, ++ch) {
-                if ((ch & 1) != (warp & 1)) continue;
-                uint32_t v[kSfBlocks][(TN + 31) / 32], w[kSfBlocks];
+            for (int kb = kb0; kb < kb1; kb += kSF, sc.next(), turn = turn + 1 == C::SW ? 0 : turn + 1) {
+                if (turn != warp - 2) continue;
+                uint32_t v[kSF][(TN + 31) / 32], w[kSF];
 #pragma unroll
-                for (int b = 0; b < kSfBlocks; ++b) {
-                    const bool on = kb + b < kb1;
-                    w[b] = kWF32 ? 0x7Fu /* 2^0 */ : on ? __ldg(ws + kb + b) : 0u;
+                for (int h = 0; h < kSF; ++h) {
+                    const bool on = kb + h < kb1;
+                    w[h] = kWF32 ? 0x7Fu /* 2^0 */ : on ? __ldg(ws + kb + h) : 0u;
 #pragma unroll
                     for (int j = 0; j < (TN + 31) / 32; ++j) {
-                        v[b][j] = ok[j] < 0 ? 0xFFFFFFFFu : 0u;
-                        if (on && ok[j] > 0) v[b][j] = __ldg(reinterpret_cast<const uint32_t *>(src[j] + (int64_t)(kb + b) * 512));
+                        v[h][j] = ok[j] < 0 ? 0xFFFFFFFFu : 0u;
+                        if (on && ok[j] > 0) v[h][j] = __ldg(reinterpret_cast<const uint32_t *>(src[j] + (int64_t)(kb + h) * 512));
                     }
                 }
-                const int sl = ch % kSfSlots;
-                bwait(&empty_sf[sl], (uint32_t)((ch / kSfSlots) & 1) ^ 1u, dead);
-                if (__any_sync(0xffffffffu, dead)) { dead = true; break; }
+                wwait<true>(&empty_sf[sc.s], sc.ph ^ 1u, dead);
+                if (dead) break;
 #pragma unroll
-                for (int b = 0; b < kSfBlocks; ++b) {
-                    unsigned char *sf = sSF + sl * C::SF_CHUNK + b * C::SF_BYTES;
-                    const uint32_t w4 = w[b] * 0x01010101u;
+                for (int h = 0; h < kSF; ++h) {
+                    unsigned char *sf = sSF + sc.s * C::SF_BYTES + h * C::SF_BLOCK;
+                    const uint32_t w4 = w[h] * 0x01010101u;
                     *reinterpret_cast<uint4 *>(sf + lane * 16) = make_uint4(w4, w4, w4, w4);
 #pragma unroll
                     for (int j = 0; j < (TN + 31) / 32; ++j)
-                        *reinterpret_cast<uint32_t *>(sf + 512 * (1 + j / 4) + lane * 16 + (j % 4) * 4) = v[b][j];
+                        *reinterpret_cast<uint32_t *>(sf + 512 * (1 + j / 4) + lane * 16 + (j % 4) * 4) = v[h][j];
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (pair == 0) mbar_arrive(&full_sf[sl]);
-                    else arrive_release_at(lead<CG>(&full_sf[sl]));
+                    if (pair == 0) mbar_arrive(&full_sf[sc.s]);
+                    else arrive_release_at(lead<CG>(&full_sf[sc.s]));
                 }
             }
         }
     } else {
         // ================================ epilogue: warp w holds the accumulator's lanes 32 (w % 4) ...
         const int q = warp & 3;
-        const int half = (warp - 4) >> 2;  // of a pair's CTA: the even or the odd 16-column chunks
+        const int share = (warp - C::W_EPI) >> 2;  // this warp's columns: loads share, share + SH, ...
         const uint32_t tq = tbase + ((uint32_t)(32 * q) << 16);
-        int at = 0;
+        Ring<C::NA> ac;
         float *red = reinterpret_cast<float *>(sA);  // split: this CTA's sums [token][128], in the stages (free by then)
         auto release = [&](uint64_t *bar) {
             tmem_fence_before();
@@ -577,55 +661,59 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
                 else if (n < p.N) store_out(p, t.m0 + tok, n, v);
             };
             if constexpr (kWF32) {
-                float acc[C::CW][16];
+                float2 acc[C::CW][C::CC / 2];
 #pragma unroll
                 for (int c = 0; c < C::CW; ++c)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) acc[c][j] = 0.f;
+                    for (int j = 0; j < C::CC / 2; ++j) acc[c][j] = make_float2(0.f, 0.f);
                 const float *ws = reinterpret_cast<const float *>(p.w_scales) + ((int64_t)t.e * nNB + min(t.n0 / kBM, nNB - 1)) * nKB;
                 float mine = 0.f;
-                for (int kb = kb0; kb < kb1; ++kb, ++at) {
+                for (int kb = kb0; kb < kb1; ++kb, ac.next()) {
                     if (((kb - kb0) & 31) == 0) mine = kb + lane < kb1 ? __ldg(ws + kb + lane) : 0.f;
-                    bwait(&acc_full[at & 1], (uint32_t)((at >> 1) & 1), dead);
-                    if (__any_sync(0xffffffffu, dead)) { dead = true; break; }
-                    tmem_fence_after();
                     const float sc = __shfl_sync(0xffffffffu, mine, (kb - kb0) & 31);
+                    const float2 s2 = make_float2(sc, sc);
+                    wwait<false>(&acc_full[ac.s], ac.ph, dead);
+                    if (dead) break;
+                    tmem_fence_after();
 #pragma unroll
                     for (int c = 0; c < C::CW; ++c) {
-                        const int col = (c * CG + half) * 16;
+                        const int col = (c * C::SH + share) * C::CC;
+                        uint32_t v[C::CC];
                         if (col < t.valid) {
-                            uint32_t v[16];
-                            tmem_ld16(tq + (uint32_t)((at & 1) * TN + col), v);
+                            tmem_load(tq + (uint32_t)(ac.s * TN + col), v);
                             tmem_wait_ld();
+                        }
+                        if (c == C::CW - 1) release(&acc_empty[ac.s]);  // all loads are back
+                        if (col < t.valid) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) acc[c][j] = fmaf(__uint_as_float(v[j]), sc, acc[c][j]);
+                            for (int j = 0; j < C::CC / 2; ++j)
+                                acc[c][j] = __ffma2_rn(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), s2, acc[c][j]);
                         }
                     }
-                    release(&acc_empty[at & 1]);
                 }
                 if (!dead) {
 #pragma unroll
                     for (int c = 0; c < C::CW; ++c)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const int tok = (c * CG + half) * 16 + j;
-                            if (tok < t.valid) emit(tok, acc[c][j]);
+                        for (int j = 0; j < C::CC; ++j) {
+                            const int tok = (c * C::SH + share) * C::CC + j;
+                            if (tok < t.valid) emit(tok, j & 1 ? acc[c][j / 2].y : acc[c][j / 2].x);
                         }
                 }
             } else {
-                bwait(&acc_full[at & 1], (uint32_t)((at >> 1) & 1), dead);
-                if (__any_sync(0xffffffffu, dead)) { dead = true; break; }
+                wwait<false>(&acc_full[ac.s], ac.ph, dead);
+                if (dead) break;
                 tmem_fence_after();
-                for (int c = half * 16; c < t.valid; c += CG * 16) {
-                    uint32_t v[16];
-                    tmem_ld16(tq + (uint32_t)((at & 1) * TN + c), v);
+                for (int c = share * C::CC; c < t.valid; c += C::SH * C::CC) {
+                    uint32_t v[C::CC];
+                    tmem_load(tq + (uint32_t)(ac.s * TN + c), v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                    for (int j = 0; j < C::CC; ++j)
                         if (c + j < t.valid) emit(c + j, __uint_as_float(v[j]));
                 }
-                release(&acc_empty[at & 1]);
-                ++at;
+                release(&acc_empty[ac.s]);
+                ac.next();
             }
         }
     }
@@ -651,7 +739,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
         if (CG == 2) cluster_sync_all();  // nothing of the pair still reads or signals the other's memory
     }
     tmem_fence_after();
-    if (warp == 3) tmem_give<CG>(tbase, C::COLS);
+    if (warp == 2) tmem_give<CG>(tbase, C::COLS);
 }
 
 std::mutex g_mu;
@@ -673,7 +761,7 @@ int64_t token_tiles(const LinearArgs &a, int tn) {
 
 template <int TN, int CG, bool kWF32, bool kGather>
 cudaError_t launch_one(const LinearArgs &a, int num_sms, cudaStream_t stream) {
-    using C = Cfg<TN, CG, kGather>;
+    using C = Cfg<TN, CG, kWF32, kGather>;
     tma::EncodeTiledFn fn;
     cudaError_t e = tma::encoder(fn);
     if (e != cudaSuccess) return e;
@@ -722,7 +810,7 @@ cudaError_t launch_one(const LinearArgs &a, int num_sms, cudaStream_t stream) {
     }
     const int64_t nN = (a.N + kBM * CG - 1) / (kBM * CG), nKB = (a.K + kBK - 1) / kBK;
     const int64_t bound = token_tiles(a, TN) * nN;
-    int64_t S = CG == 2 ? 1 : std::min<int64_t>(std::min<int64_t>(num_sms / bound, 8), nKB / 2);
+    int64_t S = CG == 2 ? 1 : std::min<int64_t>(std::min<int64_t>(num_sms / bound, 8), (nKB + kSB - 1) / kSB);
     if (S < 1) S = 1;
     LinearParams p{};
     p.x_scales = a.x_scales; p.w_scales = a.w_scales; p.rows = a.rows; p.offsets = a.offsets; p.out = a.out;
@@ -736,25 +824,30 @@ cudaError_t launch_one(const LinearArgs &a, int num_sms, cudaStream_t stream) {
     return e;
 }
 
-template <int TN, int CG>
+template <int TN, int CG, bool kWF32>
 cudaError_t launch_tn(const LinearArgs &a, int num_sms, cudaStream_t stream) {
-    if (a.w_scales_f32)
-        return a.rows != nullptr ? launch_one<TN, CG, true, true>(a, num_sms, stream) : launch_one<TN, CG, true, false>(a, num_sms, stream);
-    return a.rows != nullptr ? launch_one<TN, CG, false, true>(a, num_sms, stream) : launch_one<TN, CG, false, false>(a, num_sms, stream);
+    return a.rows != nullptr ? launch_one<TN, CG, kWF32, true>(a, num_sms, stream) : launch_one<TN, CG, kWF32, false>(a, num_sms, stream);
 }
 
-constexpr int kPairTN = 224;  // two accumulators and the scales in 512 columns; a multiple of 32
+// Token tile of a pair, a multiple of 32: two accumulators (three with fp32 weight scales) and the scales in 512 columns.
+constexpr int kPairTN = 224, kPairTNF32 = 192;
+
+template <bool kWF32>
+cudaError_t launch_scaled(const LinearArgs &a, int num_sms, cudaStream_t stream) {
+    constexpr int kPair = kWF32 ? kPairTNF32 : kPairTN;
+    const int64_t per = a.offsets != nullptr ? (a.M + a.E - 1) / a.E : a.M;  // tokens a weight meets
+    if (per <= 16) return launch_tn<16, 1, kWF32>(a, num_sms, stream);
+    if (per <= 32) return launch_tn<32, 1, kWF32>(a, num_sms, stream);
+    if (per <= 64) return launch_tn<64, 1, kWF32>(a, num_sms, stream);
+    const int64_t pairs = token_tiles(a, kPair) * ((a.N + 2 * kBM - 1) / (2 * kBM));
+    if (per <= 128 || pairs < num_sms / 2) return launch_tn<128, 1, kWF32>(a, num_sms, stream);
+    return launch_tn<kPair, 2, kWF32>(a, num_sms, stream);
+}
 
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs &a, int num_sms, cudaStream_t stream) {
-    const int64_t per = a.offsets != nullptr ? (a.M + a.E - 1) / a.E : a.M;  // tokens a weight meets
-    if (per <= 16) return launch_tn<16, 1>(a, num_sms, stream);
-    if (per <= 32) return launch_tn<32, 1>(a, num_sms, stream);
-    if (per <= 64) return launch_tn<64, 1>(a, num_sms, stream);
-    const int64_t pairs = token_tiles(a, kPairTN) * ((a.N + 2 * kBM - 1) / (2 * kBM));
-    if (per <= 128 || pairs < num_sms / 2) return launch_tn<128, 1>(a, num_sms, stream);
-    return launch_tn<kPairTN, 2>(a, num_sms, stream);
+    return a.w_scales_f32 ? launch_scaled<true>(a, num_sms, stream) : launch_scaled<false>(a, num_sms, stream);
 }
 
 }  // namespace mhc
