@@ -72,7 +72,6 @@ struct Cfg {
     static constexpr int NS_FIT = (kSmemMax - FIXED) / STAGE;
     static constexpr int NS = NS_FIT > 6 ? 6 : NS_FIT;         // ring stages
     static constexpr int CC = !kWF32 || TN < 32 ? 16 : 32;     // columns per tensor-memory load
-    static constexpr int CW = (TN / CC + SH - 1) / SH;         // loads of a warp
     // Accumulators: one being summed, one being stored; with fp32 weight scales one per k block in flight (the hand-over
     // to the epilogue and back takes longer than a k block's MMAs).
     static constexpr int NA = !kWF32 ? 2 : TN <= 64 ? 4 : TN > 160 ? 2 : 3;
@@ -282,9 +281,9 @@ __device__ __forceinline__ void load_x_rows(void *dst, const CUtensorMap *map, i
             "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
             : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
 
@@ -357,6 +356,11 @@ __device__ __forceinline__ Tile tile_at(int64_t i, const LinearParams &p, const 
 __device__ __forceinline__ void store_out(const LinearParams &p, int64_t m, int n, float v) {
     if (p.out_f32) __stcs(reinterpret_cast<float *>(p.out) + m * p.N + n, v);
     else __stcs(reinterpret_cast<unsigned short *>(p.out) + m * p.N + n, __bfloat16_as_ushort(__float2bfloat16_rn(v)));
+}
+
+__device__ __forceinline__ void store_out4(const LinearParams &p, int64_t m, int n, float4 v) {
+    if (p.out_f32) __stcs(reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.out) + m * p.N + n), v);
+    else __stcs(reinterpret_cast<uint2 *>(reinterpret_cast<unsigned short *>(p.out) + m * p.N + n), make_uint2(pack2_rn(v.x, v.y), pack2_rn(v.z, v.w)));
 }
 
 template <int TN, int CG, bool kWF32, bool kGather>
@@ -661,9 +665,10 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
                 else if (n < p.N) store_out(p, t.m0 + tok, n, v);
             };
             if constexpr (kWF32) {
-                float2 acc[C::CW][C::CC / 2];
+                constexpr int kLoads = (TN / C::CC + C::SH - 1) / C::SH;
+                float2 acc[kLoads][C::CC / 2];
 #pragma unroll
-                for (int c = 0; c < C::CW; ++c)
+                for (int c = 0; c < kLoads; ++c)
 #pragma unroll
                     for (int j = 0; j < C::CC / 2; ++j) acc[c][j] = make_float2(0.f, 0.f);
                 const float *ws = reinterpret_cast<const float *>(p.w_scales) + ((int64_t)t.e * nNB + min(t.n0 / kBM, nNB - 1)) * nKB;
@@ -676,14 +681,14 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
                     if (dead) break;
                     tmem_fence_after();
 #pragma unroll
-                    for (int c = 0; c < C::CW; ++c) {
+                    for (int c = 0; c < kLoads; ++c) {
                         const int col = (c * C::SH + share) * C::CC;
                         uint32_t v[C::CC];
                         if (col < t.valid) {
                             tmem_load(tq + (uint32_t)(ac.s * TN + col), v);
                             tmem_wait_ld();
                         }
-                        if (c == C::CW - 1) release(&acc_empty[ac.s]);  // all loads are back
+                        if (c == kLoads - 1) release(&acc_empty[ac.s]);  // all loads are back
                         if (col < t.valid) {
 #pragma unroll
                             for (int j = 0; j < C::CC / 2; ++j)
@@ -693,7 +698,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
                 }
                 if (!dead) {
 #pragma unroll
-                    for (int c = 0; c < C::CW; ++c)
+                    for (int c = 0; c < kLoads; ++c)
 #pragma unroll
                         for (int j = 0; j < C::CC; ++j) {
                             const int tok = (c * C::SH + share) * C::CC + j;
@@ -719,17 +724,22 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
     }
     if (dead) atomicOr(p.status, 1u);
     if (S > 1) {
-        // the cluster's ranges of k, added in rank order; this CTA takes every S-th token
+        // the cluster's ranges of k, added in rank order; this CTA takes every S-th token, a warp one at a time (a lane
+        // four output channels)
         const bool gave_up = __syncthreads_or(dead) != 0;
         cluster_sync_all();
         if (first < ntiles && !gave_up) {
             const Tile t = tile_at<TN, CG>(first, p, sCum, nN, nT, pair);
-            const int n = t.n0 + (tid & (kBM - 1));
-            const uint32_t mine = smem_u32(sA) + (uint32_t)(tid & (kBM - 1)) * 4;
-            for (int tok = rank + S * (tid / kBM); tok < t.valid && tid < C::NT / kBM * kBM; tok += S * (C::NT / kBM)) {
-                float v = 0.f;
-                for (int r = 0; r < S; ++r) v += ld_cluster_f32(mapa(mine, (uint32_t)r) + (uint32_t)tok * kBM * 4);
-                if (n < p.N) store_out(p, t.m0 + tok, n, v);
+            const int n = t.n0 + 4 * lane;
+            const uint32_t mine = smem_u32(sA) + (uint32_t)lane * 16;
+            for (int tok = rank + S * warp; tok < t.valid; tok += S * (C::NT / 32)) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int r = 0; r < S; ++r) {
+                    const float4 a = ld_cluster_f32x4(mapa(mine, (uint32_t)r) + (uint32_t)tok * kBM * 4);
+                    v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+                }
+                if (n < p.N) store_out4(p, t.m0 + tok, n, v);  // N % 8 == 0: all four or none
             }
         }
         __syncwarp();
