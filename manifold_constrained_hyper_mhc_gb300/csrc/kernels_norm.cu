@@ -23,6 +23,17 @@ namespace mhc {
 
 namespace {
 
+// Packed bf16 arithmetic on the two halves of a word.
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<__nv_bfloat162 *>(&w); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 b) { return *reinterpret_cast<uint32_t *>(&b); }
+__device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) { return as_u32(__hadd2_rn(as_bf162(a), as_bf162(b))); }
+// The largest magnitude of 8 bf16 values (NaN counts as none).
+__device__ __forceinline__ float absmax8(uint4 a) {
+    const uint32_t w[4] = {a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu, a.z & 0x7FFF7FFFu, a.w & 0x7FFF7FFFu};
+    const __nv_bfloat162 m = __hmax2(__hmax2(as_bf162(w[0]), as_bf162(w[1])), __hmax2(as_bf162(w[2]), as_bf162(w[3])));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
 // The 16-byte vectors of one row are spread over the threads so that consecutive lanes hold consecutive
 // vectors: 4 lanes hold a block of 32 values, 16 lanes one of 128.
 template <int kLanes>
@@ -63,7 +74,7 @@ template <int kNT, int kV, int kBlockLanes>
 __global__ void __launch_bounds__(kNT)
 add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, const uint16_t *__restrict__ gamma, int H,
                    float eps, uint16_t *R_out, uint16_t *__restrict__ X_out, MxOut mx) {
-    __shared__ double sWarp[kNT / 32];
+    __shared__ float sWarp[kNT / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int64_t t = blockIdx.x, base = t * (int64_t)H;
@@ -73,46 +84,51 @@ add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, con
     auto load = [&](int v) {  // bf16(x + residual) of one vector
         uint4 a = ld_stream(x + base + (int64_t)v * kVec);
         if (residual != nullptr) {
-            float f[8], r[8];
-            unpack8(a, f);
-            unpack8(__ldcs(reinterpret_cast<const uint4 *>(residual + base + (int64_t)v * kVec)), r);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] += r[e];
-            a = pack8_rn(f);
+            const uint4 b = __ldcs(reinterpret_cast<const uint4 *>(residual + base + (int64_t)v * kVec));
+            a = make_uint4(add2(a.x, b.x), add2(a.y, b.y), add2(a.z, b.z), add2(a.w, b.w));
         }
         return a;
     };
     auto squares = [&](uint4 a) {
         float f[8];
         unpack8(a, f);
-        float q = 0.f;
+        float2 q = __fmul2_rn(make_float2(f[0], f[1]), make_float2(f[0], f[1]));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q = fmaf(f[e], f[e], q);
-        return q;
+        for (int e = 2; e < 8; e += 2) q = __ffma2_rn(make_float2(f[e], f[e + 1]), make_float2(f[e], f[e + 1]), q);
+        return q.x + q.y;
     };
-    double sum = 0.0;
+    float sum = 0.f;
     if constexpr (kV > 0) {
 #pragma unroll
         for (int k = 0; k < kV; ++k) {
             const int v = tid + k * kNT;
             s[k] = v < nvec ? load(v) : make_uint4(0u, 0u, 0u, 0u);
         }
-        float q = 0.f;
 #pragma unroll
-        for (int k = 0; k < kV; ++k) q += squares(s[k]);
-        sum = q;
+        for (int k = 0; k < kV; ++k) sum += squares(s[k]);
     } else {
-        for (int v = tid; v < nvec; v += kNT) sum += (double)squares(load(v));
+        for (int v = tid; v < nvec; v += kNT) sum += squares(load(v));
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sum = warp_sum(sum);
     if ((tid & 31) == 0) sWarp[tid >> 5] = sum;
     __syncthreads();
-    sum = 0.0;
+    // the warps' sums and the mean as pairs of fp32 values (hi + lo)
+    float hi = sWarp[0], lo = 0.f;
 #pragma unroll
-    for (int w = 0; w < kNT / 32; ++w) sum += sWarp[w];
-    const double rd = rsqrt(sum / (double)H + (double)eps);
-    const float rh = (float)rd, rl = (float)(rd - (double)rh);
+    for (int w = 1; w < kNT / 32; ++w) {
+        const float b = sWarp[w], t2 = hi + b, z = t2 - hi;
+        lo += (hi - (t2 - z)) + (b - z);
+        hi = t2;
+    }
+    // 1 / sqrt(v), v = sum / H + eps, as rh + rl: an approximation and one Newton step whose residual 1 - v rh^2 is taken
+    // with exact products (fp64 here took 1.25 TFLOP/s' worth of the prefill: 151 us against 79)
+    const float inv = 1.f / (float)H, inv_lo = fmaf(-inv, (float)H, 1.f) * inv;
+    const float mh = hi * inv, ml = fmaf(hi, inv, -mh) + fmaf(hi, inv_lo, lo * inv);
+    const float vh = mh + eps, vz = vh - mh, vl = ((mh - (vh - vz)) + (eps - vz)) + ml;
+    const float rh = rsqrtf(vh);
+    const float ph = rh * rh, pl = fmaf(rh, rh, -ph);
+    const float res = fmaf(-vh, ph, 1.f) - fmaf(vh, pl, vl * ph);
+    const float rl = vh > 0.f && vh < __int_as_float(0x7f800000) ? 0.5f * rh * res : 0.f;
     auto finish = [&](uint4 a, int v) {
         const bool on = v < nvec;
         float f[8], g[8];
@@ -120,18 +136,17 @@ add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, con
         unpack8(on ? ld_ro(gamma + (int64_t)v * kVec) : make_uint4(0u, 0u, 0u, 0u), g);
         if (on && R_out != nullptr) st_stream(R_out + base + (int64_t)v * kVec, a);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float p = f[e] * g[e];  // exact
-            f[e] = fmaf(p, rh, p * rl);
+        for (int e = 0; e < 8; e += 2) {
+            const float2 q = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(g[e], g[e + 1]));  // exact
+            const float2 o = __ffma2_rn(q, make_float2(rh, rh), __fmul2_rn(q, make_float2(rl, rl)));
+            f[e] = o.x;
+            f[e + 1] = o.y;
         }
         const uint4 y = pack8_rn(f);
         if (on && X_out != nullptr) st_stream(X_out + base + (int64_t)v * kVec, y);
         if (mx.q != nullptr) {
             unpack8(y, f);
-            float amax = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
-            amax = group_max<kBlockLanes>(on ? amax : 0.f);
+            const float amax = group_max<kBlockLanes>(on ? absmax8(y) : 0.f);
             if (on) mx_store(f, mx_exp(amax, mx.mode), t, v, H, mx);
         }
     };
@@ -148,20 +163,24 @@ add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, con
 }
 
 // ---- SwiGLU ------------------------------------------------------------------------------------------
-__device__ __forceinline__ float silu_mul(float a, float b) { return a / (1.f + expf(-a)) * b; }
+// a / (1 + exp(-a)) * b with the hardware's exponential and reciprocal.  Its error is at most near_ulps(a) units of the
+// last place for a >= kGateMin: the exponential 2 + 1.173 |a| ulp (times e / (1 + e) < 1), the reciprocal 1, four
+// roundings 1/2 each; a unit counts up to twice where the scaled value is just below a power of two.
+constexpr float kGateMin = -80.f;  // below it the reciprocal's argument comes near fp32's largest values
+__device__ __forceinline__ float silu_mul(float a, float b) { return a * rcp_approx(1.f + __expf(-a)) * b; }
+__device__ __forceinline__ uint32_t near_ulps(float amin) { return (uint32_t)(int)fmaf(fminf(amin, 0.f), -3.f, 16.f); }
+constexpr uint32_t kNearMax = 16 + 3 * 80;
 __device__ __noinline__ double silu_mul_f64(float a, float b) { return (double)a / (1.0 + exp(-(double)a)) * (double)b; }
 
-// Whether fp32 cannot say on which side of a border between two codes u = x * 2^-E lies: its 20 bits below
-// E4M3's significand within kNear of one half.  (Below E4M3's normal range the codes are fixed-point and the
-// test is not exact there; a code off by one of 2^-9 in values of up to 448 is what fp32 leaves.)
-constexpr uint32_t kNear = 16;  // silu_mul is within 16 ulp of 2^-24: expf 2 ulp, three more roundings
-__device__ __forceinline__ bool near_border(float u) {
-    return ((__float_as_uint(u) & 0xFFFFFu) - (0x80000u - kNear)) <= 2 * kNear;
-}
-// The same for a maximum: within kNear of a power of two (or past fp32's range), or of 1.75 times one (mode 1).
+// Whether u = x * 2^-E may lie on the other side of a border between two codes, being `ulps` off: its 20 bits below
+// E4M3's significand within that of one half, i.e. border_key(u, ulps) <= ulps << 13.  (Below E4M3's normal range the
+// codes are fixed-point and the test is not exact there; a code off by one of 2^-9 in values of up to 448 is what fp32
+// leaves.)
+__device__ __forceinline__ uint32_t border_key(float u, uint32_t ulps) { return (__float_as_uint(u) + 0x80000u + ulps) << 12; }
+// The same for a maximum: near a power of two (or past fp32's range), or near 1.75 times one (mode 1).
 __device__ __forceinline__ bool near_exponent(float a, int mode) {
     const uint32_t m = __float_as_uint(a) & 0x7FFFFFu;
-    return m + kNear > 0x7FFFFFu || m < kNear || (mode == 1 && m - (0x600000u - kNear) <= 2 * kNear);
+    return m + kNearMax > 0x7FFFFFu || m < kNearMax || (mode == 1 && m - (0x600000u - kNearMax) <= 2 * kNearMax);
 }
 // mx_exp of a value held in fp64 (products beyond fp32's range among them).
 __device__ __noinline__ int mx_exp_f64(double amax, int mode) {
@@ -173,54 +192,51 @@ __device__ __noinline__ int mx_exp_f64(double amax, int mode) {
     return E < -127 ? -127 : (E > 127 ? 127 : E);
 }
 
-// One thread per vector of 8 output values; a warp's lanes hold consecutive vectors of one row (rows are
-// padded to whole groups of kBlockLanes lanes).
+// One vector of 8 output values of a lane (consecutive lanes hold consecutive vectors of a row; `on`: inside the row).
 template <int kBlockLanes>
-__global__ void __launch_bounds__(256)
-swiglu_kernel(const uint16_t *__restrict__ gu, int64_t T, int F, int lanes_row, MxOut mx) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
-    const int64_t n = T * lanes_row;
-    for (int64_t i0 = (int64_t)blockIdx.x * 256; i0 < n; i0 += (int64_t)gridDim.x * 256) {
-        const int64_t i = i0 + threadIdx.x;
-        const int64_t t = i / lanes_row;
-        const int v = (int)(i - t * lanes_row);
-        const bool on = i < n && v * kVec < F;
-        float a[8], b[8], f[8];
-        {
-            const uint16_t *src = gu + t * 2 * (int64_t)F + (int64_t)v * kVec;
-            unpack8(on ? ld_stream(src) : make_uint4(0u, 0u, 0u, 0u), a);
-            unpack8(on ? ld_stream(src + F) : make_uint4(0u, 0u, 0u, 0u), b);
-        }
-        float amax = 0.f;
+__device__ __forceinline__ void swiglu_vec(uint4 ga, uint4 ub, bool on, int64_t t, int v, int F, const MxOut &mx) {
+    float a[8], b[8], f[8];
+    unpack8(ga, a);
+    unpack8(ub, b);
+    float amax = 0.f, amin = a[0];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        f[e] = silu_mul(a[e], b[e]);
+        amax = fmaxf(amax, fabsf(f[e]));
+        amin = fminf(amin, a[e]);
+    }
+    amax = group_max<kBlockLanes>(amax);
+    int E = mx_exp(amax, mx.mode);
+    const bool low = on && amin < kGateMin;
+    const bool wide = near_exponent(amax, mx.mode) && on;
+    if (__any_sync(0xffffffffu, wide || low)) {
+        // the block's maximum in fp64, from the values that can be it
+        double m = 0.0;
+        const float cut = amax * 0.9999f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            f[e] = silu_mul(a[e], b[e]);
-            amax = fmaxf(amax, fabsf(f[e]));
-        }
-        amax = group_max<kBlockLanes>(amax);
-        int E = mx_exp(amax, mx.mode);
-        if (__any_sync(0xffffffffu, near_exponent(amax, mx.mode) && on)) {
-            double m = 0.0;
-            for (int e = 0; e < 8; ++e) {
+            if (on && (a[e] < kGateMin || !(fabsf(f[e]) < cut))) {
                 const double d = fabs(silu_mul_f64(a[e], b[e]));
                 m = d > m ? d : m;
             }
-#pragma unroll
-            for (int o = 1; o < kBlockLanes; o <<= 1) {
-                const double d = __shfl_xor_sync(0xffffffffu, m, o);
-                m = d > m ? d : m;
-            }
-            E = mx_exp_f64(m, mx.mode);
         }
-        if (!on) continue;
-        const float sc = inv_pow2(E);
-        bool near = false;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) near |= near_border(f[e] * sc);
-        if (near) {
-#pragma unroll 1
-            for (int e = 0; e < 8; ++e) {
+        for (int o = 1; o < kBlockLanes; o <<= 1) {
+            const double d = __shfl_xor_sync(0xffffffffu, m, o);
+            m = d > m ? d : m;
+        }
+        E = mx_exp_f64(m, mx.mode);
+    }
+    if (!on) return;
+    const float sc = inv_pow2(E);
+    const uint32_t ulps = near_ulps(fmaxf(amin, kGateMin));
+    uint32_t key = 0xFFFFFFFFu;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) key = min(key, border_key(f[e] * sc, ulps));
+    if (key <= ulps << 13 || low) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (border_key(f[e] * sc, ulps) <= ulps << 13 || a[e] < kGateMin) {
                 // the fp64 value, with whatever fp32 drops of it kept as a sticky last bit, rounds to the same code
                 const double d = silu_mul_f64(a[e], b[e]);
                 float h = __double2float_rz(d);
@@ -228,7 +244,48 @@ swiglu_kernel(const uint16_t *__restrict__ gu, int64_t T, int F, int lanes_row, 
                 f[e] = fabs(d) > 3.4028234663852886e38 ? (float)d : h;  // past fp32's range: infinite, the largest code
             }
         }
-        mx_store(f, E, t, v, F, mx);
+    }
+    mx_store(f, E, t, v, F, mx);
+}
+
+// A thread takes two vectors at a time, `step` apart (four 16-byte loads in flight); rows are padded to whole groups of
+// kBlockLanes lanes.
+constexpr int kSwigluNT = 256;
+template <int kBlockLanes>
+__global__ void __launch_bounds__(kSwigluNT)
+swiglu_kernel(const uint16_t *__restrict__ gu, int64_t T, int F, int lanes_row, MxOut mx) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int64_t step = (int64_t)gridDim.x * kSwigluNT, first = (int64_t)blockIdx.x * kSwigluNT + threadIdx.x;
+    const int64_t dt = step / lanes_row;
+    const int dv = (int)(step - dt * lanes_row);
+    int64_t t = first / lanes_row;
+    int v = (int)(first - t * lanes_row);
+    auto advance = [&]() {
+        t += dt;
+        v += dv;
+        if (v >= lanes_row) {
+            v -= lanes_row;
+            ++t;
+        }
+    };
+    for (int64_t n = (int64_t)blockIdx.x * kSwigluNT; n < T * lanes_row; n += 2 * step) {  // the same for the whole block
+        uint4 g[2], u[2];
+        int64_t tt[2];
+        int vv[2];
+        bool on[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            tt[k] = t;
+            vv[k] = v;
+            on[k] = t < T && v * kVec < F;
+            const uint16_t *src = gu + t * 2 * (int64_t)F + (int64_t)v * kVec;
+            g[k] = on[k] ? ld_stream(src) : make_uint4(0u, 0u, 0u, 0u);
+            u[k] = on[k] ? ld_stream(src + F) : make_uint4(0u, 0u, 0u, 0u);
+            advance();
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) swiglu_vec<kBlockLanes>(g[k], u[k], on[k], tt[k], vv[k], F, mx);
     }
 }
 
@@ -274,9 +331,9 @@ cudaError_t launch_swiglu(const uint16_t *gate_up, int64_t T, int F, const MxOut
                           cudaStream_t stream) {
     const int group = block == 128 ? 16 : 4;
     const int lanes_row = (F / kVec + group - 1) / group * group;
-    const int64_t want = (T * lanes_row + 255) / 256, cap = (int64_t)num_sms * 8;
+    const int64_t want = (T * lanes_row + kSwigluNT - 1) / kSwigluNT, cap = (int64_t)num_sms * 8;
     auto kern = block == 128 ? swiglu_kernel<16> : swiglu_kernel<4>;
-    return launch_pdl(kern, (unsigned)std::min(want, cap), 256, stream, gate_up, T, F, lanes_row, mx);
+    return launch_pdl(kern, (unsigned)std::min(want, cap), kSwigluNT, stream, gate_up, T, F, lanes_row, mx);
 }
 
 }  // namespace mhc
