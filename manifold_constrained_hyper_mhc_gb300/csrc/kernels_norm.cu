@@ -60,18 +60,35 @@ __device__ __forceinline__ uint2 e4m3_codes(const float (&x)[8], int E) {
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-// Stores vector v (8 values, exponent E) of token t: its codes, and its scale byte from the first lane of
-// every four (each four lanes are one block of 32 values).
-__device__ __forceinline__ void mx_store(const float (&x)[8], int E, int64_t t, int v, int H, const MxOut &mx) {
-    __stcs(reinterpret_cast<uint2 *>(mx.q + t * (int64_t)H + (int64_t)v * 8), e4m3_codes(x, E));
-    if ((v & 3) == 0) mx.scale[mx_scale_offset(t, v >> 2, H)] = (uint8_t)(E + 127);
+// Stores vector v (8 values, exponent E) of token t: its codes, and the scale bytes of 128 values as one word from the
+// first of their 16 lanes (a row's last word may be incomplete: then byte by byte, the padding is not written).  Every
+// lane of the warp calls it.
+template <int kBlockLanes>
+__device__ __forceinline__ void mx_store(const float (&x)[8], int E, bool on, int64_t t, int v, int H, const MxOut &mx) {
+    if (on) __stcs(reinterpret_cast<uint2 *>(mx.q + t * (int64_t)H + (int64_t)v * 8), e4m3_codes(x, E));
+    uint32_t w = (uint32_t)(E + 127);
+    if (kBlockLanes == 16) {
+        w *= 0x01010101u;
+    } else {
+        w |= __shfl_down_sync(0xffffffffu, w, 4) << 8;   // blocks k, k + 1
+        w |= __shfl_down_sync(0xffffffffu, w, 8) << 16;  // and k + 2, k + 3
+    }
+    if (on && (v & 15) == 0) {
+        uint8_t *dst = mx.scale + mx_scale_offset(t, v >> 2, H);
+        const int left = H / 32 - (v >> 2);
+        if (left >= 4) {
+            *reinterpret_cast<uint32_t *>(dst) = w;
+        } else {
+            for (int b = 0; b < left; ++b) dst[b] = (uint8_t)(w >> (8 * b));
+        }
+    }
 }
 
 // ---- residual addition + RMSNorm ---------------------------------------------------------------------
 // One CTA per token.  Rows of at most kNT * kV vectors stay in registers (kV loads of each input in flight
 // per thread); longer ones (kV == 0) are read again after the square sum, from L2.
 template <int kNT, int kV, int kBlockLanes>
-__global__ void __launch_bounds__(kNT)
+__global__ void __launch_bounds__(kNT, 2048 / kNT > 4 ? 4 : 2048 / kNT)
 add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, const uint16_t *__restrict__ gamma, int H,
                    float eps, uint16_t *R_out, uint16_t *__restrict__ X_out, MxOut mx) {
     __shared__ float sWarp[kNT / 32];
@@ -147,7 +164,7 @@ add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, con
         if (mx.q != nullptr) {
             unpack8(y, f);
             const float amax = group_max<kBlockLanes>(on ? absmax8(y) : 0.f);
-            if (on) mx_store(f, mx_exp(amax, mx.mode), t, v, H, mx);
+            mx_store<kBlockLanes>(f, mx_exp(amax, mx.mode), on, t, v, H, mx);
         }
     };
     if constexpr (kV > 0) {
@@ -163,24 +180,32 @@ add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, con
 }
 
 // ---- SwiGLU ------------------------------------------------------------------------------------------
-// a / (1 + exp(-a)) * b with the hardware's exponential and reciprocal.  Its error is at most near_ulps(a) units of the
-// last place for a >= kGateMin: the exponential 2 + 1.173 |a| ulp (times e / (1 + e) < 1), the reciprocal 1, four
-// roundings 1/2 each; a unit counts up to twice where the scaled value is just below a power of two.
+// a / (1 + exp(-a)) * b with the hardware's exponential and reciprocal, the exponential's argument as a pair (its rounding
+// alone would cost |a| ulp).  For a >= kGateMin the relative error is at most 4.5 2^-23: the exponential 2^-22, the
+// reciprocal 2^-23, three roundings 2^-24 each; twice that in units of the last place of a scaled value just below a
+// power of two: within kNear.
 constexpr float kGateMin = -80.f;  // below it the reciprocal's argument comes near fp32's largest values
-__device__ __forceinline__ float silu_mul(float a, float b) { return a * rcp_approx(1.f + __expf(-a)) * b; }
-__device__ __forceinline__ uint32_t near_ulps(float amin) { return (uint32_t)(int)fmaf(fminf(amin, 0.f), -3.f, 16.f); }
-constexpr uint32_t kNearMax = 16 + 3 * 80;
+constexpr uint32_t kNear = 12;
+__device__ __forceinline__ float silu_mul(float a, float b) {
+    constexpr float kL2E = 1.44269504f, kL2ELo = 1.92596303e-8f, kLn2 = 0.693147181f;  // log2(e) as a pair
+    const float x = fminf(a, 100.f);  // beyond, the exponential is 0 beside 1 (and the pair would overflow)
+    const float t = -x * kL2E, tl = fmaf(-x, kL2E, -t) - x * kL2ELo;
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    e = fmaf(e, tl * kLn2, e);
+    return a * rcp_approx(1.f + e) * b;
+}
 __device__ __noinline__ double silu_mul_f64(float a, float b) { return (double)a / (1.0 + exp(-(double)a)) * (double)b; }
 
-// Whether u = x * 2^-E may lie on the other side of a border between two codes, being `ulps` off: its 20 bits below
-// E4M3's significand within that of one half, i.e. border_key(u, ulps) <= ulps << 13.  (Below E4M3's normal range the
+// Whether u = x * 2^-E may lie on the other side of a border between two codes, being kNear units off: its 20 bits below
+// E4M3's significand within that of one half, i.e. border_key(u) <= kNear << 13.  (Below E4M3's normal range the
 // codes are fixed-point and the test is not exact there; a code off by one of 2^-9 in values of up to 448 is what fp32
 // leaves.)
-__device__ __forceinline__ uint32_t border_key(float u, uint32_t ulps) { return (__float_as_uint(u) + 0x80000u + ulps) << 12; }
+__device__ __forceinline__ uint32_t border_key(float u) { return (__float_as_uint(u) + 0x80000u + kNear) << 12; }
 // The same for a maximum: near a power of two (or past fp32's range), or near 1.75 times one (mode 1).
 __device__ __forceinline__ bool near_exponent(float a, int mode) {
     const uint32_t m = __float_as_uint(a) & 0x7FFFFFu;
-    return m + kNearMax > 0x7FFFFFu || m < kNearMax || (mode == 1 && m - (0x600000u - kNearMax) <= 2 * kNearMax);
+    return m + kNear > 0x7FFFFFu || m < kNear || (mode == 1 && m - (0x600000u - kNear) <= 2 * kNear);
 }
 // mx_exp of a value held in fp64 (products beyond fp32's range among them).
 __device__ __noinline__ int mx_exp_f64(double amax, int mode) {
@@ -212,7 +237,7 @@ __device__ __forceinline__ void swiglu_vec(uint4 ga, uint4 ub, bool on, int64_t 
     if (__any_sync(0xffffffffu, wide || low)) {
         // the block's maximum in fp64, from the values that can be it
         double m = 0.0;
-        const float cut = amax * 0.9999f;
+        const float cut = amax * 0.99999f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (on && (a[e] < kGateMin || !(fabsf(f[e]) < cut))) {
@@ -227,16 +252,14 @@ __device__ __forceinline__ void swiglu_vec(uint4 ga, uint4 ub, bool on, int64_t 
         }
         E = mx_exp_f64(m, mx.mode);
     }
-    if (!on) return;
     const float sc = inv_pow2(E);
-    const uint32_t ulps = near_ulps(fmaxf(amin, kGateMin));
     uint32_t key = 0xFFFFFFFFu;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) key = min(key, border_key(f[e] * sc, ulps));
-    if (key <= ulps << 13 || low) {
+    for (int e = 0; e < 8; ++e) key = min(key, border_key(f[e] * sc));
+    if (on && (key <= kNear << 13 || low)) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (border_key(f[e] * sc, ulps) <= ulps << 13 || a[e] < kGateMin) {
+            if (border_key(f[e] * sc) <= kNear << 13 || a[e] < kGateMin) {
                 // the fp64 value, with whatever fp32 drops of it kept as a sticky last bit, rounds to the same code
                 const double d = silu_mul_f64(a[e], b[e]);
                 float h = __double2float_rz(d);
@@ -245,14 +268,14 @@ __device__ __forceinline__ void swiglu_vec(uint4 ga, uint4 ub, bool on, int64_t 
             }
         }
     }
-    mx_store(f, E, t, v, F, mx);
+    mx_store<kBlockLanes>(f, E, on, t, v, F, mx);
 }
 
-// A thread takes two vectors at a time, `step` apart (four 16-byte loads in flight); rows are padded to whole groups of
-// kBlockLanes lanes.
+// A thread takes one vector at a time (two, with four loads in flight, were no faster: the registers cost as many warps);
+// rows are padded to whole groups of 16 lanes (128 values: a word of scales).
 constexpr int kSwigluNT = 256;
 template <int kBlockLanes>
-__global__ void __launch_bounds__(kSwigluNT)
+__global__ void __launch_bounds__(kSwigluNT, 4)
 swiglu_kernel(const uint16_t *__restrict__ gu, int64_t T, int F, int lanes_row, MxOut mx) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
@@ -261,31 +284,18 @@ swiglu_kernel(const uint16_t *__restrict__ gu, int64_t T, int F, int lanes_row, 
     const int dv = (int)(step - dt * lanes_row);
     int64_t t = first / lanes_row;
     int v = (int)(first - t * lanes_row);
-    auto advance = [&]() {
+    for (int64_t n = (int64_t)blockIdx.x * kSwigluNT; n < T * lanes_row; n += step) {  // the same for the whole block
+        const bool on = t < T && v * kVec < F;
+        const uint16_t *src = gu + t * 2 * (int64_t)F + (int64_t)v * kVec;
+        const uint4 g = on ? ld_stream(src) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 u = on ? ld_stream(src + F) : make_uint4(0u, 0u, 0u, 0u);
+        swiglu_vec<kBlockLanes>(g, u, on, t, v, F, mx);
         t += dt;
         v += dv;
         if (v >= lanes_row) {
             v -= lanes_row;
             ++t;
         }
-    };
-    for (int64_t n = (int64_t)blockIdx.x * kSwigluNT; n < T * lanes_row; n += 2 * step) {  // the same for the whole block
-        uint4 g[2], u[2];
-        int64_t tt[2];
-        int vv[2];
-        bool on[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            tt[k] = t;
-            vv[k] = v;
-            on[k] = t < T && v * kVec < F;
-            const uint16_t *src = gu + t * 2 * (int64_t)F + (int64_t)v * kVec;
-            g[k] = on[k] ? ld_stream(src) : make_uint4(0u, 0u, 0u, 0u);
-            u[k] = on[k] ? ld_stream(src + F) : make_uint4(0u, 0u, 0u, 0u);
-            advance();
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) swiglu_vec<kBlockLanes>(g[k], u[k], on[k], tt[k], vv[k], F, mx);
     }
 }
 
@@ -323,14 +333,14 @@ cudaError_t launch_add_rmsnorm(const uint16_t *x, const uint16_t *residual, cons
     const int nvec = H / kVec;
     if (nvec <= 256) return launch_norm_nv<256, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
     if (nvec <= 512) return launch_norm_nv<256, 2>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
-    if (nvec <= 1024) return launch_norm_nv<256, 4>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
+    if (nvec <= 896) return launch_norm_nv<448, 2>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
+    if (nvec <= 1024) return launch_norm_nv<512, 2>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
     return launch_norm_nv<512, 0>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
 }
 
 cudaError_t launch_swiglu(const uint16_t *gate_up, int64_t T, int F, const MxOut &mx, int block, int num_sms,
                           cudaStream_t stream) {
-    const int group = block == 128 ? 16 : 4;
-    const int lanes_row = (F / kVec + group - 1) / group * group;
+    const int lanes_row = (F / kVec + 15) / 16 * 16;
     const int64_t want = (T * lanes_row + kSwigluNT - 1) / kSwigluNT, cap = (int64_t)num_sms * 8;
     auto kern = block == 128 ? swiglu_kernel<16> : swiglu_kernel<4>;
     return launch_pdl(kern, (unsigned)std::min(want, cap), kSwigluNT, stream, gate_up, T, F, lanes_row, mx);
