@@ -406,15 +406,17 @@ def pre_broadcast(x, phi, bias, mix_scales, rmsnorm_weight, *, hc_norm_eps, rmsn
     return o
 
 
+# The calls below run at decode sizes too, so what they do per call on the host stays cheap: one pass over the
+# arguments, no library call besides the operator's own, no stream or device object.
 def _arg(t, name, dtypes, shape, dev):
-    """One tensor argument of the calls below, as its address: its type, shape, device and layout."""
+    """One tensor argument, as its address: its type, shape, device and layout are checked."""
+    if t.device == dev and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d).removeprefix('torch.') for d in dtypes)}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_cuda or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous tensor on {dev}")
 
 
 _types = None
@@ -430,17 +432,34 @@ def _dtypes():
     return _types
 
 
+def _cuda(t, name):
+    """The device of the first argument: the others have to be on it."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return t.device
+
+
 def _run(name, dev, stream, *args):
     """A library call on `stream` (the current stream of the tensors' device) with that device current."""
-    torch = _torch()
-    fn = getattr(lib(), name)
-    handle = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    cuda = _torch().cuda
+    fn = getattr(_lib or lib(), name)
+    if stream is not None:
+        handle = stream.cuda_stream
+    else:  # the handle alone where torch offers it (2 us less than the stream object)
+        raw = getattr(_torch_mod._C, "_cuda_getCurrentRawStream", None)
+        handle = raw(dev.index) if raw is not None else cuda.current_stream(dev).cuda_stream
+    if cuda.current_device() == dev.index:
         rc = fn(*args, handle)
     else:
-        with torch.cuda.device(dev):
+        with cuda.device(dev):
             rc = fn(*args, handle)
-    _check(rc, name)
+    if rc != OK:
+        raise MhcError(rc, name)
+
+
+def _scale_shape(rows, cols):
+    """The shape of the scale tiles (mhc_mxfp8_scale_bytes)."""
+    return ((rows + 127) // 128 * 128 * ((cols // 32 + 3) // 4 * 4),) if cols % 32 == 0 else (0,)
 
 
 def add_rmsnorm_mxfp8(x, residual, rmsnorm_weight, *, rmsnorm_eps, scale_mode=MX_SCALE_FLOOR, scale_block=32,
@@ -451,9 +470,10 @@ def add_rmsnorm_mxfp8(x, residual, rmsnorm_weight, *, rmsnorm_eps, scale_mode=MX
     them; residual_out may be the residual itself."""
     torch = _torch()
     T, H = x.shape
-    dev = x.device
+    dev = _cuda(x, "x")
     bf16, fp8, e8m0, _, _ = _dtypes()
-    o = dict(out or {})
+    o = dict(out) if out else {}
+    shape, tiles = (T, H), _scale_shape(T, H)
     if residual is not None and "residual_out" not in o:
         o["residual_out"] = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
     if want_bf16 and "layer_in" not in o:
@@ -462,17 +482,15 @@ def add_rmsnorm_mxfp8(x, residual, rmsnorm_weight, *, rmsnorm_eps, scale_mode=MX
         if "layer_in_fp8" not in o:
             o["layer_in_fp8"] = torch.empty((T, H), dtype=torch.uint8, device=dev)
         if "layer_in_scales" not in o:
-            o["layer_in_scales"] = torch.empty(mxfp8_scale_bytes(T, H), dtype=torch.uint8, device=dev)
-
-    def given(k, types, shape):
-        t = o.get(k)
-        return None if t is None else _arg(t, k, types, shape, dev)
-
-    _run("mhc_add_rmsnorm_mxfp8", dev, stream, _arg(x, "x", bf16, (T, H), dev),
-         None if residual is None else _arg(residual, "residual", bf16, (T, H), dev),
+            o["layer_in_scales"] = torch.empty(tiles, dtype=torch.uint8, device=dev)
+    ro, li, q, sc = o.get("residual_out"), o.get("layer_in"), o.get("layer_in_fp8"), o.get("layer_in_scales")
+    _run("mhc_add_rmsnorm_mxfp8", dev, stream, _arg(x, "x", bf16, shape, dev),
+         None if residual is None else _arg(residual, "residual", bf16, shape, dev),
          _arg(rmsnorm_weight, "rmsnorm_weight", bf16, (H,), dev), T, H, rmsnorm_eps,
-         given("residual_out", bf16, (T, H)), given("layer_in", bf16, (T, H)), given("layer_in_fp8", fp8, (T, H)),
-         given("layer_in_scales", e8m0, (mxfp8_scale_bytes(T, H),)), int(scale_mode), int(scale_block))
+         None if ro is None else _arg(ro, "residual_out", bf16, shape, dev),
+         None if li is None else _arg(li, "layer_in", bf16, shape, dev),
+         None if q is None else _arg(q, "layer_in_fp8", fp8, shape, dev),
+         None if sc is None else _arg(sc, "layer_in_scales", e8m0, tiles, dev), scale_mode, scale_block)
     return o
 
 
@@ -481,16 +499,17 @@ def swiglu_mxfp8(gate_up, *, scale_mode=MX_SCALE_FLOOR, scale_block=32, out=None
     [T,F] uint8 and act_scales; ``out`` may supply them."""
     torch = _torch()
     T, F = gate_up.shape[0], gate_up.shape[1] // 2
-    dev = gate_up.device
+    dev = _cuda(gate_up, "gate_up")
     bf16, fp8, e8m0, _, _ = _dtypes()
-    o = dict(out or {})
+    o = dict(out) if out else {}
+    tiles = _scale_shape(T, F)
     if "act_fp8" not in o:
         o["act_fp8"] = torch.empty((T, F), dtype=torch.uint8, device=dev)
     if "act_scales" not in o:
-        o["act_scales"] = torch.empty(mxfp8_scale_bytes(T, F), dtype=torch.uint8, device=dev)
+        o["act_scales"] = torch.empty(tiles, dtype=torch.uint8, device=dev)
     _run("mhc_swiglu_mxfp8", dev, stream, _arg(gate_up, "gate_up", bf16, (T, 2 * F), dev), T, F,
          _arg(o["act_fp8"], "act_fp8", fp8, (T, F), dev),
-         _arg(o["act_scales"], "act_scales", e8m0, (mxfp8_scale_bytes(T, F),), dev), int(scale_mode), int(scale_block))
+         _arg(o["act_scales"], "act_scales", e8m0, tiles, dev), scale_mode, scale_block)
     return o
 
 
@@ -501,7 +520,7 @@ def linear_workspace_size() -> int:
 def _linear_args(x_fp8, x_scales, w_fp8, w_scales, M, E, out_dtype, out, workspace):
     """What the two products share: the checked addresses, the weight scales' and the result's types."""
     torch = _torch()
-    dev = x_fp8.device
+    dev = _cuda(x_fp8, "x_fp8")
     _, fp8, e8m0, f32, _ = _dtypes()
     R, K = x_fp8.shape
     lead = () if E is None else (E,)
@@ -512,10 +531,10 @@ def _linear_args(x_fp8, x_scales, w_fp8, w_scales, M, E, out_dtype, out, workspa
         raise TypeError(f"out must be {str(out_dtype).removeprefix('torch.')}, got {out.dtype}")
     if workspace is None:
         workspace = torch.zeros(linear_workspace_size(), dtype=torch.uint8, device=dev)
-    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     wide = w_scales.dtype == torch.float32
-    x = (_arg(x_fp8, "x_fp8", fp8, (R, K), dev), _arg(x_scales, "x_scales", e8m0, (mxfp8_scale_bytes(R, K),), dev))
+    x = (_arg(x_fp8, "x_fp8", fp8, (R, K), dev), _arg(x_scales, "x_scales", e8m0, _scale_shape(R, K), dev))
     w = (_arg(w_fp8, "w_fp8", fp8, (*lead, N, K), dev),
          _arg(w_scales, "w_scales", f32 if wide else e8m0, (*lead, (N + 127) // 128, (K + 127) // 128), dev), int(wide))
     o = (_arg(out, "out", (torch.bfloat16, torch.float32), (M, N), dev), int(out.dtype == torch.float32),

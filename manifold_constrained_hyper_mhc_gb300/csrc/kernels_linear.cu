@@ -47,6 +47,7 @@ constexpr int kSB = 2;         // k blocks per stage: each has its own barriers,
                                // a time (its waits and loop cost about 350 cycles, nearly a block's MMAs of the largest tile)
 constexpr int kSF = 4;         // k blocks per chunk of scales, and the chunks of their ring (a chunk takes a memory latency, a
 constexpr int kSfSlots = 3;    // fence and an arrival at the pair's leader, about 2,000 cycles, whatever its size)
+constexpr int kMaxSplit = 8;   // CTAs a tile's k range is split among (a portable cluster)
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s per wait
 constexpr int kSmemMax = 227 * 1024;
 // More than half of an SM's shared memory, always: two CTAs that allocate tensor memory then never share an
@@ -802,29 +803,41 @@ cudaError_t launch_one(const LinearArgs &a, int num_sms, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    int resident = num_sms;  // CTAs, or pairs, at once
+    const int64_t nN = (a.N + kBM * CG - 1) / (kBM * CG), nKB = (a.K + kBK - 1) / kBK;
+    const int64_t bound = token_tiles(a, TN) * nN;
+    // Few tiles: each is split over k among the S CTAs of a cluster, as many as keep every cluster resident at once (a
+    // second wave of clusters costs more than the larger share: 256 x 7168 x 1024, 16 clusters of 8: 26 us, of 4: 15).
+    int S = 1, resident;
     {
         int dev = 0;
         if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
         if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-        static int ready[64];
+        static int fits[64][kMaxSplit + 1];  // clusters of CG * S CTAs resident at once
         std::lock_guard<std::mutex> lock(g_mu);
-        if (ready[dev] == 0) {
-            if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-            int n = num_sms;
-            if (CG == 2 && (e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
-            if (n < 1) return cudaErrorInvalidConfiguration;
-            ready[dev] = n;
+        if (fits[dev][1] == 0 && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+            return e;
+        const int64_t most = CG == 2 ? 1 : std::min<int64_t>(std::min<int64_t>(num_sms / bound, kMaxSplit), (nKB + kSB - 1) / kSB);
+        for (S = most < 1 ? 1 : (int)most;; --S) {
+            int &n = fits[dev][S];
+            if (n == 0) {
+                attr[0].val.clusterDim.x = (unsigned)(CG * S);
+                cfg.gridDim = dim3((unsigned)(CG * S));
+                if (CG * S == 1) n = num_sms;
+                else if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
+                if (n < 1) {
+                    n = 0;
+                    if (S == 1) return cudaErrorInvalidConfiguration;
+                }
+            }
+            if (S == 1 || n >= bound) {
+                resident = n;
+                break;
+            }
         }
-        resident = ready[dev];
     }
-    const int64_t nN = (a.N + kBM * CG - 1) / (kBM * CG), nKB = (a.K + kBK - 1) / kBK;
-    const int64_t bound = token_tiles(a, TN) * nN;
-    int64_t S = CG == 2 ? 1 : std::min<int64_t>(std::min<int64_t>(num_sms / bound, 8), (nKB + kSB - 1) / kSB);
-    if (S < 1) S = 1;
     LinearParams p{};
     p.x_scales = a.x_scales; p.w_scales = a.w_scales; p.rows = a.rows; p.offsets = a.offsets; p.out = a.out;
-    p.M = a.M; p.R = a.R; p.N = a.N; p.K = a.K; p.E = a.E; p.out_f32 = a.out_f32; p.split = (int)S;
+    p.M = a.M; p.R = a.R; p.N = a.N; p.K = a.K; p.E = a.E; p.out_f32 = a.out_f32; p.split = S;
     p.status = a.status;
     attr[0].val.clusterDim.x = (unsigned)(CG * S);
     cfg.gridDim = dim3((unsigned)(S > 1 ? bound * S : std::min<int64_t>(bound, resident) * CG));
