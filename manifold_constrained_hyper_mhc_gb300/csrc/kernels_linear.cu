@@ -58,7 +58,7 @@ template <int TN, int CG, bool kWF32, bool kGather>
 struct Cfg {
     // Epilogue warps: SH of them share the columns of each lane quadrant.  With fp32 weight scales they read every
     // accumulator of one k block, so there are more of them, each with at most 64 columns (and sums in registers).
-    static constexpr int SH = kWF32 ? (TN + 63) / 64 : CG;
+    static constexpr int SH = kWF32 ? (TN + 63) / 64 : TN >= 64 ? 2 : 1;
     static constexpr int EW = 4 * SH;
     static constexpr int SW = kWF32 ? 1 : 2;                   // warps that load scales
     static constexpr int W_EPI = 2 + SW, W_GATHER = W_EPI + EW;
@@ -354,9 +354,18 @@ __device__ __forceinline__ Tile tile_at(int64_t i, const LinearParams &p, const 
     return t;
 }
 
-__device__ __forceinline__ void store_out(const LinearParams &p, int64_t m, int n, float v) {
-    if (p.out_f32) __stcs(reinterpret_cast<float *>(p.out) + m * p.N + n, v);
-    else __stcs(reinterpret_cast<unsigned short *>(p.out) + m * p.N + n, __bfloat16_as_ushort(__float2bfloat16_rn(v)));
+// The output channels of lanes 2 i and 2 i + 1 for two tokens, v0 of token m and v1 of token m + 1: the lanes exchange a
+// value, so that the even one stores both channels of token m and the odd one those of token m + 1 (n: this lane's channel;
+// on0, on1: whether the tokens exist; N is even, so a pair of channels is inside it or not).
+__device__ __forceinline__ void store_out2(const LinearParams &p, int64_t m, int n, float v0, float v1, bool on0, bool on1) {
+    const bool odd = n & 1;
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+    const float a = odd ? got : v0, b = odd ? v1 : got;
+    if (n < p.N && (odd ? on1 : on0)) {
+        const int64_t at = (m + (odd ? 1 : 0)) * p.N + (n & ~1);
+        if (p.out_f32) __stcs(reinterpret_cast<float2 *>(reinterpret_cast<float *>(p.out) + at), make_float2(a, b));
+        else __stcs(reinterpret_cast<unsigned int *>(reinterpret_cast<unsigned short *>(p.out) + at), pack2_rn(a, b));
+    }
 }
 
 __device__ __forceinline__ void store_out4(const LinearParams &p, int64_t m, int n, float4 v) {
@@ -385,6 +394,10 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
     const int64_t nT = (p.M + TN - 1) / TN;
     bool dead = false;
 
+    if (warp == 0 && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&maps.w)) : "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&maps.x)) : "memory");
+    }
     if (warp == 1 && lane == 0) {
         for (int i = 0; i < kSB * NS; ++i) {
             mbar_init(&full[i], 1);
@@ -661,9 +674,13 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
         for (int64_t i = first; i < ntiles && !dead; i += step) {
             const Tile t = tile_at<TN, CG>(i, p, sCum, nN, nT, pair);
             const int n = t.n0 + 32 * q + lane;
-            auto emit = [&](int tok, float v) {
-                if (S > 1) red[tok * kBM + 32 * q + lane] = v;
-                else if (n < p.N) store_out(p, t.m0 + tok, n, v);
+            auto emit = [&](int tok, float v0, float v1) {  // tokens tok and tok + 1 (both inside TN)
+                if (S > 1) {
+                    red[tok * kBM + 32 * q + lane] = v0;
+                    red[(tok + 1) * kBM + 32 * q + lane] = v1;
+                } else {
+                    store_out2(p, t.m0 + tok, n, v0, v1, tok < t.valid, tok + 1 < t.valid);
+                }
             };
             if constexpr (kWF32) {
                 constexpr int kLoads = (TN / C::CC + C::SH - 1) / C::SH;
@@ -701,9 +718,9 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
 #pragma unroll
                     for (int c = 0; c < kLoads; ++c)
 #pragma unroll
-                        for (int j = 0; j < C::CC; ++j) {
+                        for (int j = 0; j < C::CC; j += 2) {
                             const int tok = (c * C::SH + share) * C::CC + j;
-                            if (tok < t.valid) emit(tok, j & 1 ? acc[c][j / 2].y : acc[c][j / 2].x);
+                            if (tok < t.valid) emit(tok, acc[c][j / 2].x, acc[c][j / 2].y);
                         }
                 }
             } else {
@@ -715,8 +732,8 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
                     tmem_load(tq + (uint32_t)(ac.s * TN + c), v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < C::CC; ++j)
-                        if (c + j < t.valid) emit(c + j, __uint_as_float(v[j]));
+                    for (int j = 0; j < C::CC; j += 2)
+                        if (c + j < t.valid) emit(c + j, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
                 }
                 release(&acc_empty[ac.s]);
                 ac.next();
