@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -872,16 +873,28 @@ cudaError_t launch_tn(const LinearArgs &a, int num_sms, cudaStream_t stream) {
 // Token tile of a pair, a multiple of 32: two accumulators (three with fp32 weight scales) and the scales in 512 columns.
 constexpr int kPairTN = 224, kPairTNF32 = 192;
 
+// About how many rounds of tiles a call takes on `units` CTAs or pairs (experts: half a tile per expert is lost on
+// average); fewer tiles than half the CTAs are split over k.
+double rounds(const LinearArgs &a, int tn, int cg, int num_sms) {
+    const double nt = a.offsets == nullptr ? (double)((a.M + tn - 1) / tn) : std::min((double)a.M, (double)a.M / tn + 0.5 * a.E);
+    const double tiles = nt * (double)((a.N + kBM * cg - 1) / (kBM * cg)), units = num_sms / cg;
+    if (tiles > units) return std::ceil(tiles / units);
+    return cg == 2 ? 1.0 : 1.0 / std::min<double>(std::floor(units / tiles), kMaxSplit);
+}
+
 template <bool kWF32>
 cudaError_t launch_scaled(const LinearArgs &a, int num_sms, cudaStream_t stream) {
-    constexpr int kPair = kWF32 ? kPairTNF32 : kPairTN;
     const int64_t per = a.offsets != nullptr ? (a.M + a.E - 1) / a.E : a.M;  // tokens a weight meets
     if (per <= 16) return launch_tn<16, 1, kWF32>(a, num_sms, stream);
     if (per <= 32) return launch_tn<32, 1, kWF32>(a, num_sms, stream);
     if (per <= 64) return launch_tn<64, 1, kWF32>(a, num_sms, stream);
-    const int64_t pairs = token_tiles(a, kPair) * ((a.N + 2 * kBM - 1) / (2 * kBM));
-    if (per <= 128 || pairs < num_sms / 2) return launch_tn<128, 1, kWF32>(a, num_sms, stream);
-    return launch_tn<kPair, 2, kWF32>(a, num_sms, stream);
+    // A k block costs a tile of either kind about the same 0.31 us (its operands' copies: 31-33 KB an SM); with fp32 weight
+    // scales (the accumulators' hand-over) 0.42 us a CTA's and 0.50 us a pair's.  Measured, k = n = 7168: 300 tokens 37 us
+    // in two rounds of CTAs, 26 in one of pairs; 256 tokens 23 us in one round of CTAs, 26 of pairs.
+    constexpr int kPair = kWF32 ? kPairTNF32 : kPairTN;
+    const double pair_cost = kWF32 ? 0.50 / 0.42 : 1.0;
+    if (rounds(a, kPair, 2, num_sms) * pair_cost < rounds(a, 128, 1, num_sms)) return launch_tn<kPair, 2, kWF32>(a, num_sms, stream);
+    return launch_tn<128, 1, kWF32>(a, num_sms, stream);
 }
 
 }  // namespace
