@@ -48,24 +48,20 @@ __device__ __forceinline__ float inv_pow2(int E) {
     return __uint_as_float(E < 127 ? (uint32_t)(127 - E) << 23 : 0x400000u);
 }
 
-// E4M3 codes of x * 2^-E for 8 values, as two words.
-__device__ __forceinline__ uint2 e4m3_codes(const float (&x)[8], int E) {
-    const float m = inv_pow2(E);
-    const float2 m2 = make_float2(m, m);
+// E4M3 codes of 8 scaled values, as two words.
+__device__ __forceinline__ uint2 e4m3_codes(const float2 (&u)[4]) {
     uint32_t w[4];
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
-        w[p] = (uint32_t)__nv_cvt_float2_to_fp8x2(__fmul2_rn(make_float2(x[2 * p], x[2 * p + 1]), m2), __NV_SATFINITE,
-                                                   __NV_E4M3);
+    for (int p = 0; p < 4; ++p) w[p] = (uint32_t)__nv_cvt_float2_to_fp8x2(u[p], __NV_SATFINITE, __NV_E4M3);
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-// Stores vector v (8 values, exponent E) of token t: its codes, and the scale bytes of 128 values as one word from the
-// first of their 16 lanes (a row's last word may be incomplete: then byte by byte, the padding is not written).  Every
-// lane of the warp calls it.
+// Stores vector v (8 scaled values of exponent E) of a row: its codes at `q`, and the scale bytes of 128 values as one
+// word from the first of their 16 lanes, at `scale` + mx_scale_col (a row's last word may be incomplete: then byte by
+// byte, the padding is not written).  Every lane of the warp calls it.
 template <int kBlockLanes>
-__device__ __forceinline__ void mx_store(const float (&x)[8], int E, bool on, int64_t t, int v, int H, const MxOut &mx) {
-    if (on) __stcs(reinterpret_cast<uint2 *>(mx.q + t * (int64_t)H + (int64_t)v * 8), e4m3_codes(x, E));
+__device__ __forceinline__ void mx_store(const float2 (&u)[4], int E, bool on, uint8_t *q, uint8_t *scale, int v, int H) {
+    if (on) __stcs(reinterpret_cast<uint2 *>(q), e4m3_codes(u));
     uint32_t w = (uint32_t)(E + 127);
     if (kBlockLanes == 16) {
         w *= 0x01010101u;
@@ -74,7 +70,7 @@ __device__ __forceinline__ void mx_store(const float (&x)[8], int E, bool on, in
         w |= __shfl_down_sync(0xffffffffu, w, 8) << 16;  // and k + 2, k + 3
     }
     if (on && (v & 15) == 0) {
-        uint8_t *dst = mx.scale + mx_scale_offset(t, v >> 2, H);
+        uint8_t *dst = scale + (v >> 4) * 512;  // mx_scale_col(v / 4)
         const int left = H / 32 - (v >> 2);
         if (left >= 4) {
             *reinterpret_cast<uint32_t *>(dst) = w;
@@ -86,7 +82,9 @@ __device__ __forceinline__ void mx_store(const float (&x)[8], int E, bool on, in
 
 // ---- residual addition + RMSNorm ---------------------------------------------------------------------
 // One CTA per token.  Rows of at most kNT * kV vectors stay in registers (kV loads of each input in flight
-// per thread); longer ones (kV == 0) are read again after the square sum, from L2.
+// per thread); longer ones (kV == 0) are read again after the square sum, from L2.  8192 x 7168 with the residual
+// (413 MB): 75 us, 5.5 TB/s, with 448 threads of two vectors, four CTAs an SM; 224 threads of four 83-98 us, 896 of one
+// 162 us (a CTA waits for its row's sum, so what counts is how many rows an SM has in flight).
 template <int kNT, int kV, int kBlockLanes>
 __global__ void __launch_bounds__(kNT, 2048 / kNT > 4 ? 4 : 2048 / kNT)
 add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, const uint16_t *__restrict__ gamma, int H,
@@ -94,14 +92,15 @@ add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, con
     __shared__ float sWarp[kNT / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int64_t t = blockIdx.x, base = t * (int64_t)H;
+    const int64_t t = blockIdx.x, at = t * (int64_t)H + (int64_t)threadIdx.x * kVec;  // this thread's first vector
     const int tid = threadIdx.x, nvec = H / kVec;
     constexpr int kRegs = kV > 0 ? kV : 1;
     uint4 s[kRegs];
-    auto load = [&](int v) {  // bf16(x + residual) of one vector
-        uint4 a = ld_stream(x + base + (int64_t)v * kVec);
-        if (residual != nullptr) {
-            const uint4 b = __ldcs(reinterpret_cast<const uint4 *>(residual + base + (int64_t)v * kVec));
+    const uint16_t *const xr = x + at, *const rr = residual != nullptr ? residual + at : nullptr;
+    auto load = [&](int off) {  // bf16(x + residual) of one vector, `off` values after the first
+        uint4 a = ld_stream(xr + off);
+        if (rr != nullptr) {
+            const uint4 b = __ldcs(reinterpret_cast<const uint4 *>(rr + off));
             a = make_uint4(add2(a.x, b.x), add2(a.y, b.y), add2(a.z, b.z), add2(a.w, b.w));
         }
         return a;
@@ -119,63 +118,63 @@ add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, con
 #pragma unroll
         for (int k = 0; k < kV; ++k) {
             const int v = tid + k * kNT;
-            s[k] = v < nvec ? load(v) : make_uint4(0u, 0u, 0u, 0u);
+            s[k] = v < nvec ? load(k * kNT * kVec) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int k = 0; k < kV; ++k) sum += squares(s[k]);
     } else {
-        for (int v = tid; v < nvec; v += kNT) sum += squares(load(v));
+        for (int v = tid; v < nvec; v += kNT) sum += squares(load((v - tid) * kVec));
     }
     sum = warp_sum(sum);
     if ((tid & 31) == 0) sWarp[tid >> 5] = sum;
     __syncthreads();
-    // the warps' sums and the mean as pairs of fp32 values (hi + lo)
-    float hi = sWarp[0], lo = 0.f;
-#pragma unroll
-    for (int w = 1; w < kNT / 32; ++w) {
-        const float b = sWarp[w], t2 = hi + b, z = t2 - hi;
-        lo += (hi - (t2 - z)) + (b - z);
-        hi = t2;
-    }
+    float hi = (tid & 31) < kNT / 32 ? sWarp[tid & 31] : 0.f;
+    hi = warp_sum(hi);
     // 1 / sqrt(v), v = sum / H + eps, as rh + rl: an approximation and one Newton step whose residual 1 - v rh^2 is taken
     // with exact products (fp64 here took 1.25 TFLOP/s' worth of the prefill: 151 us against 79)
     const float inv = 1.f / (float)H, inv_lo = fmaf(-inv, (float)H, 1.f) * inv;
-    const float mh = hi * inv, ml = fmaf(hi, inv, -mh) + fmaf(hi, inv_lo, lo * inv);
+    const float mh = hi * inv, ml = fmaf(hi, inv, -mh) + hi * inv_lo;
     const float vh = mh + eps, vz = vh - mh, vl = ((mh - (vh - vz)) + (eps - vz)) + ml;
     const float rh = rsqrtf(vh);
     const float ph = rh * rh, pl = fmaf(rh, rh, -ph);
     const float res = fmaf(-vh, ph, 1.f) - fmaf(vh, pl, vl * ph);
     const float rl = vh > 0.f && vh < __int_as_float(0x7f800000) ? 0.5f * rh * res : 0.f;
-    auto finish = [&](uint4 a, int v) {
+    uint8_t *const scale = mx.q != nullptr ? mx.scale + mx_scale_row(t, H) : nullptr;
+    const float2 rh2 = make_float2(rh, rh), rl2 = make_float2(rl, rl);
+    auto finish = [&](uint4 a, int off) {
+        const int v = tid + off / kVec;
         const bool on = v < nvec;
         float f[8], g[8];
         unpack8(a, f);
-        unpack8(on ? ld_ro(gamma + (int64_t)v * kVec) : make_uint4(0u, 0u, 0u, 0u), g);
-        if (on && R_out != nullptr) st_stream(R_out + base + (int64_t)v * kVec, a);
+        unpack8(on ? ld_ro(gamma + tid * kVec + off) : make_uint4(0u, 0u, 0u, 0u), g);
+        if (on && R_out != nullptr) st_stream(R_out + at + off, a);
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
             const float2 q = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(g[e], g[e + 1]));  // exact
-            const float2 o = __ffma2_rn(q, make_float2(rh, rh), __fmul2_rn(q, make_float2(rl, rl)));
+            const float2 o = __ffma2_rn(q, rh2, __fmul2_rn(q, rl2));
             f[e] = o.x;
             f[e + 1] = o.y;
         }
         const uint4 y = pack8_rn(f);
-        if (on && X_out != nullptr) st_stream(X_out + base + (int64_t)v * kVec, y);
+        if (on && X_out != nullptr) st_stream(X_out + at + off, y);
         if (mx.q != nullptr) {
             unpack8(y, f);
             const float amax = group_max<kBlockLanes>(on ? absmax8(y) : 0.f);
-            mx_store<kBlockLanes>(f, mx_exp(amax, mx.mode), on, t, v, H, mx);
+            const int E = mx_exp(amax, mx.mode);
+            const float sc = inv_pow2(E);
+            float2 u[4];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) u[e / 2] = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(sc, sc));
+            mx_store<kBlockLanes>(u, E, on, mx.q + at + off, scale, v, H);
         }
     };
     if constexpr (kV > 0) {
 #pragma unroll
         for (int k = 0; k < kV; ++k)
-            if (k == 0 || k * kNT < nvec) finish(s[k], tid + k * kNT);
+            if (k == 0 || k * kNT < nvec) finish(s[k], k * kNT * kVec);
     } else {
-        for (int v0 = 0; v0 < nvec; v0 += kNT) {  // whole groups of lanes: the maxima are exchanged
-            const int v = v0 + tid;
-            finish(v < nvec ? load(v) : make_uint4(0u, 0u, 0u, 0u), v);
-        }
+        for (int v0 = 0; v0 < nvec; v0 += kNT)  // whole groups of lanes: the maxima are exchanged
+            finish(v0 + tid < nvec ? load(v0 * kVec) : make_uint4(0u, 0u, 0u, 0u), v0 * kVec);
     }
 }
 
@@ -186,14 +185,20 @@ add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, con
 // power of two: within kNear.
 constexpr float kGateMin = -80.f;  // below it the reciprocal's argument comes near fp32's largest values
 constexpr uint32_t kNear = 12;
-__device__ __forceinline__ float silu_mul(float a, float b) {
+// (Above kGateMax the pair overflows.)
+constexpr float kGateMax = 1e38f;
+__device__ __forceinline__ bool gate_far(float a) { return a < kGateMin || a > kGateMax; }
+__device__ __forceinline__ float2 silu_mul2(float2 a, float2 b) {
     constexpr float kL2E = 1.44269504f, kL2ELo = 1.92596303e-8f, kLn2 = 0.693147181f;  // log2(e) as a pair
-    const float x = fminf(a, 100.f);  // beyond, the exponential is 0 beside 1 (and the pair would overflow)
-    const float t = -x * kL2E, tl = fmaf(-x, kL2E, -t) - x * kL2ELo;
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    e = fmaf(e, tl * kLn2, e);
-    return a * rcp_approx(1.f + e) * b;
+    const float2 t = __fmul2_rn(a, make_float2(-kL2E, -kL2E));
+    float2 tl = __ffma2_rn(a, make_float2(-kL2E, -kL2E), make_float2(-t.x, -t.y));
+    tl = __ffma2_rn(a, make_float2(-kL2ELo, -kL2ELo), tl);
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = __ffma2_rn(e, __fmul2_rn(tl, make_float2(kLn2, kLn2)), e);
+    const float2 d = __fadd2_rn(e, make_float2(1.f, 1.f));
+    return __fmul2_rn(__fmul2_rn(a, make_float2(rcp_approx(d.x), rcp_approx(d.y))), b);
 }
 __device__ __noinline__ double silu_mul_f64(float a, float b) { return (double)a / (1.0 + exp(-(double)a)) * (double)b; }
 
@@ -201,7 +206,7 @@ __device__ __noinline__ double silu_mul_f64(float a, float b) { return (double)a
 // E4M3's significand within that of one half, i.e. border_key(u) <= kNear << 13.  (Below E4M3's normal range the
 // codes are fixed-point and the test is not exact there; a code off by one of 2^-9 in values of up to 448 is what fp32
 // leaves.)
-__device__ __forceinline__ uint32_t border_key(float u) { return (__float_as_uint(u) + 0x80000u + kNear) << 12; }
+__device__ __forceinline__ uint32_t border_key(float u) { return (__float_as_uint(u) << 12) + ((0x80000u + kNear) << 12); }
 // The same for a maximum: near a power of two (or past fp32's range), or near 1.75 times one (mode 1).
 __device__ __forceinline__ bool near_exponent(float a, int mode) {
     if (a < 7.7e-34f) return false;  // 2^-110: the exponent is the smallest one on either side (rows of zeros)
@@ -218,30 +223,33 @@ __device__ __noinline__ int mx_exp_f64(double amax, int mode) {
     return E < -127 ? -127 : (E > 127 ? 127 : E);
 }
 
-// One vector of 8 output values of a lane (consecutive lanes hold consecutive vectors of a row; `on`: inside the row).
+// One vector of 8 output values of a lane (consecutive lanes hold consecutive vectors of a row; `on`: inside the row):
+// its codes go to `q`, the row's scales are at `scale`.
 template <int kBlockLanes>
-__device__ __forceinline__ void swiglu_vec(uint4 ga, uint4 ub, bool on, int64_t t, int v, int F, const MxOut &mx) {
+__device__ __forceinline__ void swiglu_vec(uint4 ga, uint4 ub, bool on, uint8_t *q, uint8_t *scale, int v, int F, int mode) {
     float a[8], b[8], f[8];
     unpack8(ga, a);
     unpack8(ub, b);
-    float amax = 0.f, amin = a[0];
+    float amax = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        f[e] = silu_mul(a[e], b[e]);
-        amax = fmaxf(amax, fabsf(f[e]));
-        amin = fminf(amin, a[e]);
+    for (int e = 0; e < 8; e += 2) {
+        const float2 y = silu_mul2(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+        f[e] = y.x;
+        f[e + 1] = y.y;
+        amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
     }
+    const __nv_bfloat162 lo2 = __hmin2(__hmin2(as_bf162(ga.x), as_bf162(ga.y)), __hmin2(as_bf162(ga.z), as_bf162(ga.w))),
+                         hi2 = __hmax2(__hmax2(as_bf162(ga.x), as_bf162(ga.y)), __hmax2(as_bf162(ga.z), as_bf162(ga.w)));
+    const bool far = on && (gate_far(fminf(__low2float(lo2), __high2float(lo2))) || gate_far(fmaxf(__low2float(hi2), __high2float(hi2))));
     amax = group_max<kBlockLanes>(amax);
-    int E = mx_exp(amax, mx.mode);
-    const bool low = on && amin < kGateMin;
-    const bool wide = near_exponent(amax, mx.mode) && on;
-    if (__any_sync(0xffffffffu, wide || low)) {
+    int E = mx_exp(amax, mode);
+    if (__any_sync(0xffffffffu, far || (on && near_exponent(amax, mode)))) {
         // the block's maximum in fp64, from the values that can be it
         double m = 0.0;
         const float cut = amax * 0.99999f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (on && (a[e] < kGateMin || !(fabsf(f[e]) < cut))) {
+            if (on && (gate_far(a[e]) || !(fabsf(f[e]) < cut))) {
                 const double d = fabs(silu_mul_f64(a[e], b[e]));
                 m = d > m ? d : m;
             }
@@ -251,52 +259,69 @@ __device__ __forceinline__ void swiglu_vec(uint4 ga, uint4 ub, bool on, int64_t 
             const double d = __shfl_xor_sync(0xffffffffu, m, o);
             m = d > m ? d : m;
         }
-        E = mx_exp_f64(m, mx.mode);
+        E = mx_exp_f64(m, mode);
     }
     const float sc = inv_pow2(E);
+    float2 u[4];
     uint32_t key = 0xFFFFFFFFu;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) key = min(key, border_key(f[e] * sc));
-    if (on && (key <= kNear << 13 || low)) {
+    for (int e = 0; e < 8; e += 2) {
+        u[e / 2] = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(sc, sc));
+        key = min(key, min(border_key(u[e / 2].x), border_key(u[e / 2].y)));
+    }
+    if (on && (key <= kNear << 13 || far)) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (border_key(f[e] * sc) <= kNear << 13 || a[e] < kGateMin) {
+            float &w = e & 1 ? u[e / 2].y : u[e / 2].x;
+            if (border_key(w) <= kNear << 13 || gate_far(a[e])) {
                 // the fp64 value, with whatever fp32 drops of it kept as a sticky last bit, rounds to the same code
                 const double d = silu_mul_f64(a[e], b[e]);
                 float h = __double2float_rz(d);
                 if ((double)h != d) h = __uint_as_float(__float_as_uint(h) | 1u);
-                f[e] = fabs(d) > 3.4028234663852886e38 ? (float)d : h;  // past fp32's range: infinite, the largest code
+                w = (fabs(d) > 3.4028234663852886e38 ? (float)d : h) * sc;  // past fp32's range: infinite, the largest code
             }
         }
     }
-    mx_store<kBlockLanes>(f, E, on, t, v, F, mx);
+    mx_store<kBlockLanes>(u, E, on, q, scale, v, F);
 }
 
-// A thread takes one vector at a time (two, with four loads in flight, were no faster: the registers cost as many warps);
-// rows are padded to whole groups of 16 lanes (128 values: a word of scales).
-constexpr int kSwigluNT = 256;
-template <int kBlockLanes>
-__global__ void __launch_bounds__(kSwigluNT, 4)
+// A thread takes one vector at a time, the next one's loads in flight; rows are padded to whole groups of 16 lanes (128
+// values: a word of scales).  16384 x 2048 (169 MB): 40 us with one CTA of 768 threads an SM, 44-46 with 256-thread CTAs (or
+// without the loads ahead); a call that does not fill one round of the large CTAs takes the small ones (48 x 2048: 2.8 us
+// against 3.3).  What is left above the bytes (25 us) is issue: about 27 instructions a value, two of them for the test of
+// the borders.
+template <int kNT, int kBlockLanes>
+__global__ void __launch_bounds__(kNT)
 swiglu_kernel(const uint16_t *__restrict__ gu, int64_t T, int F, int lanes_row, MxOut mx) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int64_t step = (int64_t)gridDim.x * kSwigluNT, first = (int64_t)blockIdx.x * kSwigluNT + threadIdx.x;
+    const int64_t step = (int64_t)gridDim.x * kNT, first = (int64_t)blockIdx.x * kNT + threadIdx.x;
     const int64_t dt = step / lanes_row;
     const int dv = (int)(step - dt * lanes_row);
     int64_t t = first / lanes_row;
     int v = (int)(first - t * lanes_row);
-    for (int64_t n = (int64_t)blockIdx.x * kSwigluNT; n < T * lanes_row; n += step) {  // the same for the whole block
-        const bool on = t < T && v * kVec < F;
+    uint4 g, u;
+    bool on;
+    auto load = [&]() {
+        on = t < T && v * kVec < F;
         const uint16_t *src = gu + t * 2 * (int64_t)F + (int64_t)v * kVec;
-        const uint4 g = on ? ld_stream(src) : make_uint4(0u, 0u, 0u, 0u);
-        const uint4 u = on ? ld_stream(src + F) : make_uint4(0u, 0u, 0u, 0u);
-        swiglu_vec<kBlockLanes>(g, u, on, t, v, F, mx);
+        g = on ? ld_stream(src) : make_uint4(0u, 0u, 0u, 0u);
+        u = on ? ld_stream(src + F) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    load();
+    for (int64_t n = (int64_t)blockIdx.x * kNT; n < T * lanes_row; n += step) {  // the same for the whole block
+        const uint4 g0 = g, u0 = u;
+        const bool on0 = on;
+        const int64_t t0 = t;
+        const int v0 = v;
         t += dt;
         v += dv;
         if (v >= lanes_row) {
             v -= lanes_row;
             ++t;
         }
+        load();
+        swiglu_vec<kBlockLanes>(g0, u0, on0, mx.q + t0 * F + (int64_t)v0 * kVec, mx.scale + mx_scale_row(t0, F), v0, F, mx.mode);
     }
 }
 
@@ -342,9 +367,13 @@ cudaError_t launch_add_rmsnorm(const uint16_t *x, const uint16_t *residual, cons
 cudaError_t launch_swiglu(const uint16_t *gate_up, int64_t T, int F, const MxOut &mx, int block, int num_sms,
                           cudaStream_t stream) {
     const int lanes_row = (F / kVec + 15) / 16 * 16;
-    const int64_t want = (T * lanes_row + kSwigluNT - 1) / kSwigluNT, cap = (int64_t)num_sms * 8;
-    auto kern = block == 128 ? swiglu_kernel<16> : swiglu_kernel<4>;
-    return launch_pdl(kern, (unsigned)std::min(want, cap), kSwigluNT, stream, gate_up, T, F, lanes_row, mx);
+    const int64_t n = T * lanes_row;
+    if (n >= (int64_t)num_sms * 768) {
+        auto kern = block == 128 ? swiglu_kernel<768, 16> : swiglu_kernel<768, 4>;
+        return launch_pdl(kern, (unsigned)num_sms, 768, stream, gate_up, T, F, lanes_row, mx);
+    }
+    auto kern = block == 128 ? swiglu_kernel<256, 16> : swiglu_kernel<256, 4>;
+    return launch_pdl(kern, (unsigned)((n + 255) / 256), 256, stream, gate_up, T, F, lanes_row, mx);
 }
 
 }  // namespace mhc
