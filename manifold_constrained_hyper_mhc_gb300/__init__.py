@@ -490,7 +490,7 @@ def add_rmsnorm_mxfp8(x, residual, rmsnorm_weight, *, rmsnorm_eps, scale_mode=MX
          None if ro is None else _arg(ro, "residual_out", bf16, shape, dev),
          None if li is None else _arg(li, "layer_in", bf16, shape, dev),
          None if q is None else _arg(q, "layer_in_fp8", fp8, shape, dev),
-         None if sc is None else _arg(sc, "layer_in_scales", e8m0, tiles, dev), scale_mode, scale_block)
+         None if sc is None else _arg(sc, "layer_in_scales", e8m0, tiles, dev), int(scale_mode), int(scale_block))
     return o
 
 
@@ -509,7 +509,7 @@ def swiglu_mxfp8(gate_up, *, scale_mode=MX_SCALE_FLOOR, scale_block=32, out=None
         o["act_scales"] = torch.empty(tiles, dtype=torch.uint8, device=dev)
     _run("mhc_swiglu_mxfp8", dev, stream, _arg(gate_up, "gate_up", bf16, (T, 2 * F), dev), T, F,
          _arg(o["act_fp8"], "act_fp8", fp8, (T, F), dev),
-         _arg(o["act_scales"], "act_scales", e8m0, tiles, dev), scale_mode, scale_block)
+         _arg(o["act_scales"], "act_scales", e8m0, tiles, dev), int(scale_mode), int(scale_block))
     return o
 
 

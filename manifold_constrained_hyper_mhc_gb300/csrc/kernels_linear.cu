@@ -90,7 +90,7 @@ struct Cfg {
 };
 
 struct LinearMaps {
-    CUtensorMap w, x;
+    CUtensorMap w, x, x16;  // x in boxes of a CTA's rows (one row for gathered rows), and of 16 rows
 };
 
 struct LinearParams {
@@ -448,8 +448,9 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
     if (CG == 2) cluster_sync_all();  // the peer's barriers exist before anything arrives on them
     tmem_fence_after();
     const uint32_t tbase = *sTmem;
-    const int64_t ntiles = (p.offsets != nullptr ? (int64_t)sCum[p.E] : nT) * nN;
     const int64_t first = blockIdx.x / (S * CG), step = gridDim.x / (S * CG);
+    int64_t ntiles = (p.offsets != nullptr ? (int64_t)sCum[p.E] : nT) * nN;
+    if (S > 1) ntiles = min(ntiles, step);  // a split cluster takes one tile (only overlapping groups make more tiles)
     // this CTA's share of the stages, and of their k blocks
     const int nKS = (nKB + kSB - 1) / kSB;
     const int ks0 = (int)((int64_t)nKS * rank / S), ks1 = (int)((int64_t)nKS * (rank + 1) / S);
@@ -466,7 +467,9 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
         uint32_t last_ph = 0;
         for (int64_t i = first; i < ntiles && !dead; i += step) {
             const Tile t = tile_at<TN, CG>(i, p, sCum, nN, nT, pair);
-            const int q0 = CG == 1 ? 0 : pair * (t.width<CG>() / 2);  // this CTA's part of the tile's rows
+            // this CTA's part of the tile's rows: a multiple of 16, all that is copied (a group's last tile is half empty
+            // on average, and the copies are what bounds a tile)
+            const int rows = t.width<CG>() / CG, q0 = CG == 1 ? 0 : pair * rows;
             int r[kRows4Part][4];  // this warp's rows, the same in every lane
             if (kGather) {
                 int mine[4] = {0, 0, 0, 0};
@@ -497,14 +500,27 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
                     unsigned char *da = sA + st.s * C::A_BYTES + h * C::A_BLOCK, *db = sB + st.s * C::B_BYTES + h * C::B_BLOCK;
                     if (part == 0 && elect_one()) {
                         // the leader expects the pair's bytes (the peer's may land before: the phase waits for this arrival)
-                        if (pair == 0) mbar_arrive_expect_tx(&full[at], CG * (C::A_BLOCK + C::B_BLOCK));
+                        if (pair == 0) mbar_arrive_expect_tx(&full[at], CG * (C::A_BLOCK + rows * kBK));
                         load_w<CG>(da, &maps.w, x, t.n0, t.e, bar);
-                        if (!kGather) load_x<CG>(db, &maps.x, x, (int)t.m0 + q0, bar);
+                        if (!kGather) {
+                            if (rows == C::TNC) {
+                                load_x<CG>(db, &maps.x, x, (int)t.m0 + q0, bar);
+                            } else {
+                                for (int g = 0; g < rows; g += 16) load_x<CG>(db + g * kBK, &maps.x16, x, (int)t.m0 + q0 + g, bar);
+                            }
+                        }
                     }
                     if (kGather && elect_one()) {
+                        // (the whole tile apart: a test for every four rows costs the full tiles a fifth)
+                        if (rows == C::TNC) {
 #pragma unroll
-                        for (int g = 0; g < kRows4Part; ++g)
-                            if (part + g * kParts < kRows4) load_x_rows<CG>(db + (part + g * kParts) * 512, &maps.x, x, r[g], bar);
+                            for (int g = 0; g < kRows4Part; ++g)
+                                if (part + g * kParts < kRows4) load_x_rows<CG>(db + (part + g * kParts) * 512, &maps.x, x, r[g], bar);
+                        } else {
+#pragma unroll
+                            for (int g = 0; g < kRows4Part; ++g)
+                                if (4 * (part + g * kParts) < rows) load_x_rows<CG>(db + (part + g * kParts) * 512, &maps.x, x, r[g], bar);
+                        }
                     }
                     last_st = at;
                     last_ph = st.ph;
@@ -804,6 +820,8 @@ cudaError_t launch_one(const LinearArgs &a, int num_sms, cudaStream_t stream) {
         const cuuint64_t dx[2] = {K, (cuuint64_t)a.R}, sx[1] = {K};
         const cuuint32_t bx[2] = {kBK, kGather ? 1u : (cuuint32_t)C::TNC};
         if ((e = encode_u8(fn, &maps.x, 2, a.x, dx, sx, bx)) != cudaSuccess) return e;
+        const cuuint32_t b16[2] = {kBK, 16};
+        if (!kGather && C::TNC > 16 && (e = encode_u8(fn, &maps.x16, 2, a.x, dx, sx, b16)) != cudaSuccess) return e;
     }
     auto kern = linear_kernel<TN, CG, kWF32, kGather>;
     constexpr int smem = C::SMEM > kSmemMin ? C::SMEM : kSmemMin;
@@ -884,7 +902,8 @@ double rounds(const LinearArgs &a, int tn, int cg, int num_sms) {
 
 template <bool kWF32>
 cudaError_t launch_scaled(const LinearArgs &a, int num_sms, cudaStream_t stream) {
-    const int64_t per = a.offsets != nullptr ? (a.M + a.E - 1) / a.E : a.M;  // tokens a weight meets
+    // tokens a weight meets (experts' groups differ: half as many again as their mean)
+    const int64_t per = a.offsets != nullptr ? (3 * a.M + 2 * a.E - 1) / (2 * a.E) : a.M;
     if (per <= 16) return launch_tn<16, 1, kWF32>(a, num_sms, stream);
     if (per <= 32) return launch_tn<32, 1, kWF32>(a, num_sms, stream);
     if (per <= 64) return launch_tn<64, 1, kWF32>(a, num_sms, stream);

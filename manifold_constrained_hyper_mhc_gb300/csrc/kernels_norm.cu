@@ -86,7 +86,7 @@ __device__ __forceinline__ void mx_store(const float2 (&u)[4], int E, bool on, u
 // (413 MB): 75 us, 5.5 TB/s, with 448 threads of two vectors, four CTAs an SM; 224 threads of four 83-98 us, 896 of one
 // 162 us (a CTA waits for its row's sum, so what counts is how many rows an SM has in flight).
 template <int kNT, int kV, int kBlockLanes>
-__global__ void __launch_bounds__(kNT, 2048 / kNT > 4 ? 4 : 2048 / kNT)
+__global__ void __launch_bounds__(kNT, kNT >= 448 ? 4 : 1)
 add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, const uint16_t *__restrict__ gamma, int H,
                    float eps, uint16_t *R_out, uint16_t *__restrict__ X_out, MxOut mx) {
     __shared__ float sWarp[kNT / 32];
@@ -131,7 +131,7 @@ add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, con
     float hi = (tid & 31) < kNT / 32 ? sWarp[tid & 31] : 0.f;
     hi = warp_sum(hi);
     // 1 / sqrt(v), v = sum / H + eps, as rh + rl: an approximation and one Newton step whose residual 1 - v rh^2 is taken
-    // with exact products (fp64 here took 1.25 TFLOP/s' worth of the prefill: 151 us against 79)
+    // with exact products (fp64 here was what the prefill's time went to: 151 us)
     const float inv = 1.f / (float)H, inv_lo = fmaf(-inv, (float)H, 1.f) * inv;
     const float mh = hi * inv, ml = fmaf(hi, inv, -mh) + hi * inv_lo;
     const float vh = mh + eps, vz = vh - mh, vl = ((mh - (vh - vz)) + (eps - vz)) + ml;
@@ -357,8 +357,13 @@ cudaError_t launch_add_rmsnorm(const uint16_t *x, const uint16_t *residual, cons
                                cudaStream_t stream) {
     (void)num_sms;
     const int nvec = H / kVec;
+    // The fewest threads that hold the row with one vector each, from 513 vectors with two (us at 8192 rows with the
+    // residual: H = 512: 64 x 1 8.9, 256 x 1 15; 2048: 256 x 1 24.5, 128 x 2 24.1, 64 x 4 28.0; 4096: 512 x 1 45.3, 256 x 2
+    // 47.8; 7168: 448 x 2 75, 512 threads reading the row twice 84.8; 8192: 512 x 2 85.6, 256 x 4 97, twice 89.5).
+    if (nvec <= 64) return launch_norm_nv<64, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
+    if (nvec <= 128) return launch_norm_nv<128, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
     if (nvec <= 256) return launch_norm_nv<256, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
-    if (nvec <= 512) return launch_norm_nv<256, 2>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
+    if (nvec <= 512) return launch_norm_nv<512, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
     if (nvec <= 896) return launch_norm_nv<448, 2>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
     if (nvec <= 1024) return launch_norm_nv<512, 2>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
     return launch_norm_nv<512, 0>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
