@@ -38,7 +38,8 @@ def check(got, x, w, label=""):
 
 SIZES = [(1, 32, 8), (1, 128, 128), (3, 96, 136), (6, 7168, 1024), (16, 256, 384), (17, 1056, 264), (32, 512, 1000),
          (33, 544, 520), (64, 2048, 256), (65, 288, 136), (128, 1024, 1032), (129, 4064, 328), (300, 1056, 520),
-         (513, 2080, 776), (1000, 160, 2056), (2049, 320, 1160)]
+         (513, 2080, 776), (1000, 160, 2056), (2049, 320, 1160),
+         (3000, 1056, 7176), (4100, 544, 4104), (5000, 96, 4096)]  # the last ones: pairs of CTAs
 
 
 @pytest.mark.parametrize("wide", [False, True], ids=["ue8m0", "f32scale"])
@@ -69,7 +70,8 @@ def group(M, E, seed, lo=0, hi=None, empty=()):
 EXPERTS = [  # M, E, K, N, rows of x (None: no gather)
     (1, 1, 32, 8, None), (1, 8, 128, 128, 3), (12, 8, 512, 264, 6), (48, 64, 1024, 256, 6), (100, 3, 96, 136, None),
     (130, 5, 288, 520, 50), (700, 8, 544, 264, 200), (1500, 16, 416, 392, None), (2000, 2, 1056, 136, 700),
-    (77, 1024, 64, 72, 20), (4000, 40, 256, 128, None)]
+    (77, 1024, 64, 72, 20), (4000, 40, 256, 128, None),
+    (6000, 8, 288, 4104, 900), (9000, 40, 160, 2056, None), (3000, 24, 1056, 4096, 700)]  # pairs of CTAs
 
 
 @pytest.mark.parametrize("wide", [False, True], ids=["ue8m0", "f32scale"])
@@ -111,9 +113,36 @@ def test_one_expert_equals_the_plain_product(mhc, ws):
     assert torch.equal(b, c)
 
 
-def test_offsets_outside_the_rows_are_clamped(mhc, ws):
+def test_one_expert_equals_the_plain_product_in_pairs(mhc, ws):
+    M, K, N = 4100, 288, 4104
+    xq, xs = ref.activations(M, K, 1)
+    wq, wsc = ref.weights((), N, K, 2, True)
+    a = mhc.linear_mxfp8(xq, xs, wq, wsc, workspace=ws)
+    off = torch.tensor([0, 0, M, M], dtype=torch.int32, device="cuda")
+    w3, s3 = torch.stack([wq * 0, wq, wq * 0]), torch.stack([wsc, wsc, wsc])
+    b = mhc.expert_linear_mxfp8(xq, xs, w3, s3, off, workspace=ws)
+    c = mhc.expert_linear_mxfp8(xq, xs, w3, s3, off, rows=torch.arange(M, dtype=torch.int32, device="cuda"), workspace=ws)
+    check(a, ref.dequant_x(xq, xs), ref.dequant_w(wq, wsc))
+    assert torch.equal(a, b) and torch.equal(b, c)
+
+
+def test_overlapping_groups_stay_inside_the_output(mhc, ws):
+    """Offsets that go back and forth (not allowed: groups overlap) make more tiles than the rows do; the call still ends,
+    and writes nothing outside out."""
+    M, K, N, E = 40, 2048, 136, 16
+    xq, xs = ref.activations(M, K, 5)
+    wq, wsc = ref.weights((E,), N, K, 6, False)
+    buf = torch.full((M + 100, N), -7.0, dtype=torch.float32, device="cuda")
+    off = torch.tensor([0, M] * 8 + [0], dtype=torch.int32, device="cuda")
+    mhc.expert_linear_mxfp8(xq, xs, wq, wsc, off, out=buf[:M], workspace=ws)
+    mhc.check_status(ws)
+    assert bool((buf[M:] == -7.0).all())
+
+
+@pytest.mark.parametrize("K", [128, 2048])
+def test_offsets_outside_the_rows_are_clamped(mhc, ws, K):
     """A bound outside [0, M] is clamped, a group that ends before it begins is empty; nothing outside out is written."""
-    M, K, N, E = 70, 128, 136, 4
+    M, N, E = 70, 136, 4
     xq, xs = ref.activations(M, K, 5)
     wq, wsc = ref.weights((E,), N, K, 6, False)
     x = ref.dequant_x(xq, xs)
@@ -132,9 +161,9 @@ def test_offsets_outside_the_rows_are_clamped(mhc, ws):
     assert bool((buf == -7.0).all())  # every group empty
 
 
-@pytest.mark.parametrize("M", [9, 200])
-def test_a_row_index_outside_x_gives_a_row_of_nan(mhc, ws, M):
-    R, K, N, E = 10, 256, 136, 3
+@pytest.mark.parametrize("M,N", [(9, 136), (200, 136), (6000, 4104)])
+def test_a_row_index_outside_x_gives_a_row_of_nan(mhc, ws, M, N):
+    R, K, E = 10, 256, 3
     xq, xs = ref.activations(R, K, 5)
     wq, wsc = ref.weights((E,), N, K, 6, False)
     rows = torch.randint(0, R, (M,), generator=torch.Generator().manual_seed(1)).int().cuda()
@@ -147,7 +176,7 @@ def test_a_row_index_outside_x_gives_a_row_of_nan(mhc, ws, M):
     assert bool(out[bad].isnan().all()) and bool(out[~bad].isfinite().all())
 
 
-@pytest.mark.parametrize("T,N", [(5, 136), (200, 264)])
+@pytest.mark.parametrize("T,N", [(5, 136), (200, 264), (4100, 4104)])
 @pytest.mark.parametrize("wide", [False, True], ids=["ue8m0", "f32scale"])
 def test_nan_stays_in_its_row_and_column(mhc, ws, T, N, wide):
     K = 416
@@ -185,6 +214,9 @@ def test_results_repeat_and_workspaces_stay_clear(mhc, ws):
     wq, wsc = ref.weights((), 1024, 4096, 2, True)   # split over k in clusters
     eq, es = ref.weights((8,), 264, 4096, 3, False)
     off = group(6, 8, 1)
+    yq, ys = ref.activations(4100, 288, 1)
+    vq, vs = ref.weights((), 4104, 288, 2, False)    # pairs of CTAs
+    three = mhc.linear_mxfp8(yq, ys, vq, vs, workspace=ws)
     one = mhc.linear_mxfp8(xq, xs, wq, wsc, workspace=ws)
     two = mhc.expert_linear_mxfp8(xq, xs, eq, es, off, workspace=ws)
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
@@ -192,8 +224,10 @@ def test_results_repeat_and_workspaces_stay_clear(mhc, ws):
     outs = [torch.empty_like(one) for _ in range(20)], [torch.empty_like(two) for _ in range(20)]
     for a, b in zip(*outs):  # both streams at once
         mhc.linear_mxfp8(xq, xs, wq, wsc, out=a, workspace=ws, stream=s1)
+        c = mhc.linear_mxfp8(yq, ys, vq, vs, workspace=ws, stream=s2)
         mhc.expert_linear_mxfp8(xq, xs, eq, es, off, out=b, workspace=ws, stream=s2)
     torch.cuda.synchronize()
+    assert torch.equal(c, three)
     assert all(torch.equal(a, one) for a in outs[0]) and all(torch.equal(b, two) for b in outs[1])
     ga, gb = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
     a, b = torch.empty_like(one), torch.empty_like(two)
