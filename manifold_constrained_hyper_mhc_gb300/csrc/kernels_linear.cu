@@ -127,6 +127,15 @@ __device__ __forceinline__ void wwait(uint64_t *bar, uint32_t parity, bool &dead
     }
     dead = __any_sync(0xffffffffu, dead);
 }
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
 // The waits for a stage's blocks, all tested before any is waited for.
 __device__ __forceinline__ void wwait_blocks(uint64_t *blocks, uint32_t parity, bool &dead) {
     bool ok = true;
@@ -694,12 +703,13 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
         const uint32_t tq = tbase + ((uint32_t)(32 * q) << 16);
         Ring<C::NA> ac;
         float *red = reinterpret_cast<float *>(sA);  // split: this CTA's sums [token][128], in the stages (free by then)
-        auto release = [&](uint64_t *bar) {
+        const uint32_t free_bar = lead<CG>(acc_empty);
+        auto release = [&](int acc) {  // accumulator `acc` has been read: its loads are back in every lane
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (pair == 0) mbar_arrive(bar);
-                else arrive_relaxed_at(lead<CG>(bar));
+                if (pair == 0) mbar_arrive(&acc_empty[acc]);
+                else arrive_relaxed_at(free_bar + 8 * acc);
             }
         };
         for (int64_t i = first; i < ntiles && !dead; i += step) {
@@ -721,23 +731,28 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
 #pragma unroll
                     for (int j = 0; j < C::CC / 2; ++j) acc[c][j] = make_float2(0.f, 0.f);
                 const float *ws = reinterpret_cast<const float *>(p.w_scales) + ((int64_t)t.e * nNB + min(t.n0 / kBM, nNB - 1)) * nKB;
-                float mine = 0.f;
-                for (int kb = kb0; kb < kb1; ++kb, ac.next()) {
-                    if (((kb - kb0) & 31) == 0) mine = kb + lane < kb1 ? __ldg(ws + kb + lane) : 0.f;
-                    const float sc = __shfl_sync(0xffffffffu, mine, (kb - kb0) & 31);
-                    const float2 s2 = make_float2(sc, sc);
-                    wwait<false>(&acc_full[ac.s], ac.ph, dead);
+                float next = __ldg(ws + kb0);
+                bool seen = false;  // the next accumulator's barrier was seen complete
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    const float2 s2 = make_float2(next, next);
+                    next = __ldg(ws + min(kb + 1, kb1 - 1));
+                    if (!__all_sync(0xffffffffu, seen)) wwait<false>(&acc_full[ac.s], ac.ph, dead);
                     if (dead) break;
                     tmem_fence_after();
+                    const uint32_t at = tq + (uint32_t)(ac.s * TN);
 #pragma unroll
                     for (int c = 0; c < kLoads; ++c) {
                         const int col = (c * C::SH + share) * C::CC;
                         uint32_t v[C::CC];
                         if (col < t.valid) {
-                            tmem_load(tq + (uint32_t)(ac.s * TN + col), v);
+                            tmem_load(at + (uint32_t)col, v);
                             tmem_wait_ld();
                         }
-                        if (c == kLoads - 1) release(&acc_empty[ac.s]);  // all loads are back
+                        if (c == kLoads - 1) {  // all loads are back
+                            release(ac.s);
+                            ac.next();
+                            seen = mbar_test(&acc_full[ac.s], ac.ph);
+                        }
                         if (col < t.valid) {
 #pragma unroll
                             for (int j = 0; j < C::CC / 2; ++j)
@@ -768,7 +783,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
                     for (int j = 0; j < C::CC; ++j) v[j] = __uint_as_float(u[j]);
                     emit(c, v);
                 }
-                release(&acc_empty[ac.s]);
+                release(ac.s);
                 ac.next();
             }
         }
