@@ -13,9 +13,18 @@
 //   - fp32 weight scales (kWF32) are not representable there: the operand's scales are 1, every k block
 //     gets its own accumulator, and the epilogue warps add it to fp32 registers times the block's scale.
 //
-// Roles of a CTA: warp 0 copies operands, warp 1 issues the MMAs, warp 2 (and 3) loads scales and owns the
-// tensor memory, the others are the epilogue (and copy gathered rows).  They hand work over through mbarriers: a ring of stages (one
-// k block each) and two accumulators, so one tile's epilogue overlaps the next tile's products.
+// Roles of a CTA: warp 0 copies operands, warp 1 issues the MMAs, warp 2 (and 3) loads scales (2 also owns the
+// tensor memory), the others are the epilogue (and copy gathered rows).  They hand work over through mbarriers: a
+// ring of stages (two k blocks each), a ring of scale chunks, and two accumulators, so one tile's epilogue overlaps
+// the next tile's products.
+//
+// Tiles.  A k block of a 128 x TN tile takes TN * 2 tensor cycles, and 16 KB + TN * 128 bytes of copies.  From L2 an SM
+// gets about 50 bytes a cycle, so large calls are bound by copies: a pair of CTAs (cta_group::2) shares the token rows
+// of a 256 x 224 tile, 31 KB an SM and k block.  Measured (UE8M0 scales): 8192 x 7168 x 7168 in 237-245 us, 3.4-3.5
+// PFLOP/s, 90-93 % of twice the measured bf16 rate, the clock at 1.65 GHz under the power limit; without the copies it
+// would be 196 us, without the MMAs 211.  Few tokens are bound by the weight's bytes: 6 x 7168 x 7168 in 13.2 us, 48 rows
+// over 64 experts (1.0 GB of touched weights) in 137 us, 7.3 TB/s.  fp32 scales: 2048 x 7168 x 4096 in 84 us, bound by
+// the hand-over of one accumulator per k block (about 850 cycles in the epilogue warps).
 //
 // Few tiles (decode) are split over k in a cluster: each CTA of the cluster sums its range, then the ranges
 // are added in rank order through distributed shared memory, so the result is the same in every run.
