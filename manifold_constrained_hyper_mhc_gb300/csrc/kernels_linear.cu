@@ -58,6 +58,8 @@ constexpr int kSB = 2;         // k blocks per stage: each has its own barriers,
 constexpr int kSF = 4;         // k blocks per chunk of scales, and the chunks of their ring (a chunk takes a memory latency, a
 constexpr int kSfSlots = 3;    // fence and an arrival at the pair's leader, about 2,000 cycles, whatever its size)
 constexpr int kMaxSplit = 8;   // CTAs a tile's k range is split among (a portable cluster)
+constexpr int kSplitStages = 4;  // and only beyond so many stages: a stage takes a CTA 0.41 us, the join 1.2 (one token) to
+                                 // 2.6 us (128): K = 512 3.8 us whole, 4.6 in two; 1024 4.65 and 4.8; 2048 6.3 and 5.7
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s per wait
 constexpr int kSmemMax = 227 * 1024;
 // More than half of an SM's shared memory, always: two CTAs that allocate tensor memory then never share an
@@ -879,7 +881,7 @@ cudaError_t launch_one(const LinearArgs &a, int num_sms, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const int64_t nN = (a.N + kBM * CG - 1) / (kBM * CG), nKB = (a.K + kBK - 1) / kBK;
+    const int64_t nN = (a.N + kBM * CG - 1) / (kBM * CG), nKS = (a.K + kSB * kBK - 1) / (kSB * kBK);
     const int64_t bound = token_tiles(a, TN) * nN;
     // Few tiles: each is split over k among the S CTAs of a cluster, as many as keep every cluster resident at once (a
     // second wave of clusters costs more than the larger share: 256 x 7168 x 1024, 16 clusters of 8: 26 us, of 4: 15).
@@ -890,9 +892,11 @@ cudaError_t launch_one(const LinearArgs &a, int num_sms, cudaStream_t stream) {
         if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
         static int fits[64][kMaxSplit + 1];  // clusters of CG * S CTAs resident at once
         std::lock_guard<std::mutex> lock(g_mu);
-        if (fits[dev][1] == 0 && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
-            return e;
-        const int64_t most = CG == 2 ? 1 : std::min<int64_t>(std::min<int64_t>(num_sms / bound, kMaxSplit), (nKB + kSB - 1) / kSB);
+        if (fits[dev][0] == 0) {  // once per device
+            if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+            fits[dev][0] = 1;
+        }
+        const int64_t most = CG == 2 || nKS <= kSplitStages ? 1 : std::min<int64_t>(std::min<int64_t>(num_sms / bound, kMaxSplit), nKS);
         for (S = most < 1 ? 1 : (int)most;; --S) {
             int &n = fits[dev][S];
             if (n == 0) {
@@ -937,7 +941,7 @@ double rounds(const LinearArgs &a, int tn, int cg, int num_sms) {
     const double nt = a.offsets == nullptr ? (double)((a.M + tn - 1) / tn) : std::min((double)a.M, (double)a.M / tn + 0.5 * a.E);
     const double tiles = nt * (double)((a.N + kBM * cg - 1) / (kBM * cg)), units = num_sms / cg;
     if (tiles > units) return std::ceil(tiles / units);
-    return cg == 2 ? 1.0 : 1.0 / std::min<double>(std::floor(units / tiles), kMaxSplit);
+    return cg == 2 || a.K <= kSplitStages * kSB * kBK ? 1.0 : 1.0 / std::min<double>(std::floor(units / tiles), kMaxSplit);
 }
 
 template <bool kWF32>
