@@ -457,6 +457,17 @@ def _run(name, dev, stream, *args):
         raise MhcError(rc, name)
 
 
+def _new(shape, dtype, dev, stream, zero=False):
+    """A new tensor for a call on `stream`, allocated (and zeroed) on that stream, so that it is ready there and its
+    memory is not handed to another stream's work before that stream is done with it."""
+    torch = _torch()
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=dev)
+
+
 def _scale_shape(rows, cols):
     """The shape of the scale tiles (mhc_mxfp8_scale_bytes)."""
     return ((rows + 127) // 128 * 128 * ((cols // 32 + 3) // 4 * 4),) if cols % 32 == 0 else (0,)
@@ -475,14 +486,14 @@ def add_rmsnorm_mxfp8(x, residual, rmsnorm_weight, *, rmsnorm_eps, scale_mode=MX
     o = dict(out) if out else {}
     shape, tiles = (T, H), _scale_shape(T, H)
     if residual is not None and "residual_out" not in o:
-        o["residual_out"] = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        o["residual_out"] = _new(shape, torch.bfloat16, dev, stream)
     if want_bf16 and "layer_in" not in o:
-        o["layer_in"] = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        o["layer_in"] = _new(shape, torch.bfloat16, dev, stream)
     if want_mxfp8:
         if "layer_in_fp8" not in o:
-            o["layer_in_fp8"] = torch.empty((T, H), dtype=torch.uint8, device=dev)
+            o["layer_in_fp8"] = _new(shape, torch.uint8, dev, stream)
         if "layer_in_scales" not in o:
-            o["layer_in_scales"] = torch.empty(tiles, dtype=torch.uint8, device=dev)
+            o["layer_in_scales"] = _new(tiles, torch.uint8, dev, stream)
     ro, li, q, sc = o.get("residual_out"), o.get("layer_in"), o.get("layer_in_fp8"), o.get("layer_in_scales")
     _run("mhc_add_rmsnorm_mxfp8", dev, stream, _arg(x, "x", bf16, shape, dev),
          None if residual is None else _arg(residual, "residual", bf16, shape, dev),
@@ -504,9 +515,9 @@ def swiglu_mxfp8(gate_up, *, scale_mode=MX_SCALE_FLOOR, scale_block=32, out=None
     o = dict(out) if out else {}
     tiles = _scale_shape(T, F)
     if "act_fp8" not in o:
-        o["act_fp8"] = torch.empty((T, F), dtype=torch.uint8, device=dev)
+        o["act_fp8"] = _new((T, F), torch.uint8, dev, stream)
     if "act_scales" not in o:
-        o["act_scales"] = torch.empty(tiles, dtype=torch.uint8, device=dev)
+        o["act_scales"] = _new(tiles, torch.uint8, dev, stream)
     _run("mhc_swiglu_mxfp8", dev, stream, _arg(gate_up, "gate_up", bf16, (T, 2 * F), dev), T, F,
          _arg(o["act_fp8"], "act_fp8", fp8, (T, F), dev),
          _arg(o["act_scales"], "act_scales", e8m0, tiles, dev), int(scale_mode), int(scale_block))
@@ -517,7 +528,7 @@ def linear_workspace_size() -> int:
     return int(lib().mhc_linear_workspace_size())
 
 
-def _linear_args(x_fp8, x_scales, w_fp8, w_scales, M, E, out_dtype, out, workspace):
+def _linear_args(x_fp8, x_scales, w_fp8, w_scales, M, E, out_dtype, out, workspace, stream):
     """What the two products share: the checked addresses, the weight scales' and the result's types."""
     torch = _torch()
     dev = _cuda(x_fp8, "x_fp8")
@@ -526,11 +537,11 @@ def _linear_args(x_fp8, x_scales, w_fp8, w_scales, M, E, out_dtype, out, workspa
     lead = () if E is None else (E,)
     N = w_fp8.shape[-2]
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
+        out = _new((M, N), out_dtype or torch.bfloat16, dev, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out must be {str(out_dtype).removeprefix('torch.')}, got {out.dtype}")
     if workspace is None:
-        workspace = torch.zeros(linear_workspace_size(), dtype=torch.uint8, device=dev)
+        workspace = _new((linear_workspace_size(),), torch.uint8, dev, stream, zero=True)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     wide = w_scales.dtype == torch.float32
@@ -547,7 +558,7 @@ def linear_mxfp8(x_fp8, x_scales, w_fp8, w_scales, *, out_dtype=None, out=None, 
     128 x 128 block: w_scales [ceil(N/128), ceil(K/128)], uint8 or float8_e8m0fnu (exponents) or float32.
     Returns out [T,N], bfloat16 (the default) or float32."""
     dev, T, K, N, x, w, out, o = _linear_args(x_fp8, x_scales, w_fp8, w_scales, x_fp8.shape[0], None, out_dtype, out,
-                                              workspace)
+                                              workspace, stream)
     _run("mhc_linear_mxfp8", dev, stream, *x, *w, T, K, N, *o)
     return out
 
@@ -559,7 +570,7 @@ def expert_linear_mxfp8(x_fp8, x_scales, w_fp8, w_scales, expert_offsets, *, row
     linear_mxfp8.  Rows of out outside every group are left as they were."""
     M = x_fp8.shape[0] if rows is None else rows.shape[0]
     E = w_fp8.shape[0]
-    dev, R, K, N, x, w, out, o = _linear_args(x_fp8, x_scales, w_fp8, w_scales, M, E, out_dtype, out, workspace)
+    dev, R, K, N, x, w, out, o = _linear_args(x_fp8, x_scales, w_fp8, w_scales, M, E, out_dtype, out, workspace, stream)
     i32 = _dtypes()[4]
     _run("mhc_expert_linear_mxfp8", dev, stream, *x, R, None if rows is None else _arg(rows, "rows", i32, (M,), dev), M,
          _arg(expert_offsets, "expert_offsets", i32, (E + 1,), dev), E, *w, K, N, *o)

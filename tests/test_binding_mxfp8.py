@@ -85,3 +85,20 @@ def test_argument_checks_name_the_argument():
 def test_scale_shape_is_the_librarys(mhc_lib, rows, cols):
     assert mhc._scale_shape(rows, cols) == (mhc.mxfp8_scale_bytes(rows, cols),)
     assert mhc._scale_shape(rows, cols + 8) == (0,)
+
+
+@pytest.mark.parametrize("zero", [False, True])
+def test_new_tensors_belong_to_the_calls_stream(monkeypatch, zero):
+    on = []
+
+    @contextlib.contextmanager
+    def use(stream):
+        on.append(stream)
+        yield
+
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    s = Stream()
+    t = mhc._new((2, 3), torch.uint8, torch.device("cpu"), s, zero=zero)
+    assert on == [s] and t.shape == (2, 3) and t.dtype == torch.uint8
+    mhc._new((2, 3), torch.uint8, torch.device("cpu"), None)
+    assert on == [s]
