@@ -56,9 +56,22 @@ __device__ __forceinline__ uint2 e4m3_codes(const float2 (&u)[4]) {
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
+// The scale bytes w of the row's 128-value group k, by a lane that is `on` (a row's last group may be incomplete: then
+// byte by byte, the padding is not written).
+__device__ __forceinline__ void mx_store_scales(uint32_t w, bool on, uint8_t *scale, int k, int H) {
+    if (on) {
+        uint8_t *dst = scale + k * 512;  // mx_scale_col(4 k)
+        const int left = H / 32 - 4 * k;
+        if (left >= 4) {
+            *reinterpret_cast<uint32_t *>(dst) = w;
+        } else {
+            for (int b = 0; b < left; ++b) dst[b] = (uint8_t)(w >> (8 * b));
+        }
+    }
+}
+
 // Stores vector v (8 scaled values of exponent E) of a row: its codes at `q`, and the scale bytes of 128 values as one
-// word from the first of their 16 lanes, at `scale` + mx_scale_col (a row's last word may be incomplete: then byte by
-// byte, the padding is not written).  Every lane of the warp calls it.
+// word from the first of their 16 lanes.  Every lane of the warp calls it.
 template <int kBlockLanes>
 __device__ __forceinline__ void mx_store(const float2 (&u)[4], int E, bool on, uint8_t *q, uint8_t *scale, int v, int H) {
     if (on) __stcs(reinterpret_cast<uint2 *>(q), e4m3_codes(u));
@@ -69,15 +82,7 @@ __device__ __forceinline__ void mx_store(const float2 (&u)[4], int E, bool on, u
         w |= __shfl_down_sync(0xffffffffu, w, 4) << 8;   // blocks k, k + 1
         w |= __shfl_down_sync(0xffffffffu, w, 8) << 16;  // and k + 2, k + 3
     }
-    if (on && (v & 15) == 0) {
-        uint8_t *dst = scale + (v >> 4) * 512;  // mx_scale_col(v / 4)
-        const int left = H / 32 - (v >> 2);
-        if (left >= 4) {
-            *reinterpret_cast<uint32_t *>(dst) = w;
-        } else {
-            for (int b = 0; b < left; ++b) dst[b] = (uint8_t)(w >> (8 * b));
-        }
-    }
+    mx_store_scales(w, on && (v & 15) == 0, scale, v >> 4, H);
 }
 
 // ---- residual addition + RMSNorm ---------------------------------------------------------------------
@@ -223,23 +228,36 @@ __device__ __noinline__ int mx_exp_f64(double amax, int mode) {
     return E < -127 ? -127 : (E > 127 ? 127 : E);
 }
 
-// One vector of 8 output values of a lane (consecutive lanes hold consecutive vectors of a row; `on`: inside the row):
-// its codes go to `q`, the row's scales are at `scale`.
+// 16 output values of a lane (consecutive lanes hold consecutive ones of a row; `on`: inside the row): their codes go to
+// `q`, the row's scales are at `scale`.  kBlockLanes lanes share an exponent.
+constexpr int kLaneVals = 16;
 template <int kBlockLanes>
-__device__ __forceinline__ void swiglu_vec(uint4 ga, uint4 ub, bool on, uint8_t *q, uint8_t *scale, int v, int F, int mode) {
-    float a[8], b[8], f[8];
-    unpack8(ga, a);
-    unpack8(ub, b);
+__device__ __forceinline__ void swiglu_vals(const uint4 (&ga)[2], const uint4 (&ub)[2], bool on, uint8_t *q, uint8_t *scale, int v,
+                                            int F, int mode) {
+    float a[kLaneVals], b[kLaneVals], f[kLaneVals];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        unpack8(ga[h], *reinterpret_cast<float (*)[8]>(&a[8 * h]));
+        unpack8(ub[h], *reinterpret_cast<float (*)[8]>(&b[8 * h]));
+    }
     float amax = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
+    for (int e = 0; e < kLaneVals; e += 2) {
         const float2 y = silu_mul2(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
         f[e] = y.x;
         f[e + 1] = y.y;
         amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
     }
-    const __nv_bfloat162 lo2 = __hmin2(__hmin2(as_bf162(ga.x), as_bf162(ga.y)), __hmin2(as_bf162(ga.z), as_bf162(ga.w))),
-                         hi2 = __hmax2(__hmax2(as_bf162(ga.x), as_bf162(ga.y)), __hmax2(as_bf162(ga.z), as_bf162(ga.w)));
+    __nv_bfloat162 lo2 = as_bf162(ga[0].x), hi2 = lo2;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t w[4] = {ga[h].x, ga[h].y, ga[h].z, ga[h].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            lo2 = __hmin2(lo2, as_bf162(w[k]));
+            hi2 = __hmax2(hi2, as_bf162(w[k]));
+        }
+    }
     const bool far = on && (gate_far(fminf(__low2float(lo2), __high2float(lo2))) || gate_far(fmaxf(__low2float(hi2), __high2float(hi2))));
     amax = group_max<kBlockLanes>(amax);
     int E = mx_exp(amax, mode);
@@ -248,7 +266,7 @@ __device__ __forceinline__ void swiglu_vec(uint4 ga, uint4 ub, bool on, uint8_t 
         double m = 0.0;
         const float cut = amax * 0.99999f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < kLaneVals; ++e) {
             if (on && (gate_far(a[e]) || !(fabsf(f[e]) < cut))) {
                 const double d = fabs(silu_mul_f64(a[e], b[e]));
                 m = d > m ? d : m;
@@ -262,16 +280,16 @@ __device__ __forceinline__ void swiglu_vec(uint4 ga, uint4 ub, bool on, uint8_t 
         E = mx_exp_f64(m, mode);
     }
     const float sc = inv_pow2(E);
-    float2 u[4];
+    float2 u[kLaneVals / 2];
     uint32_t key = 0xFFFFFFFFu;
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
+    for (int e = 0; e < kLaneVals; e += 2) {
         u[e / 2] = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(sc, sc));
         key = min(key, min(border_key(u[e / 2].x), border_key(u[e / 2].y)));
     }
     if (on && (key <= kNear << 13 || far)) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < kLaneVals; ++e) {
             float &w = e & 1 ? u[e / 2].y : u[e / 2].x;
             if (border_key(w) <= kNear << 13 || gate_far(a[e])) {
                 // the fp64 value, with whatever fp32 drops of it kept as a sticky last bit, rounds to the same code
@@ -282,14 +300,25 @@ __device__ __forceinline__ void swiglu_vec(uint4 ga, uint4 ub, bool on, uint8_t 
             }
         }
     }
-    mx_store<kBlockLanes>(u, E, on, q, scale, v, F);
+    const uint2 c0 = e4m3_codes(*reinterpret_cast<const float2 (*)[4]>(&u[0])), c1 = e4m3_codes(*reinterpret_cast<const float2 (*)[4]>(&u[4]));
+    if (on) __stcs(reinterpret_cast<uint4 *>(q), make_uint4(c0.x, c0.y, c1.x, c1.y));
+    // the scale bytes of 128 values (8 lanes) as one word
+    uint32_t w = (uint32_t)(E + 127);
+    if (kBlockLanes == 8) {
+        w *= 0x01010101u;
+    } else {
+        w |= __shfl_down_sync(0xffffffffu, w, 2) << 8;   // blocks k, k + 1
+        w |= __shfl_down_sync(0xffffffffu, w, 4) << 16;  // and k + 2, k + 3
+    }
+    mx_store_scales(w, on && (v & 7) == 0, scale, v >> 3, F);
 }
 
-// A thread takes one vector at a time, the next one's loads in flight; rows are padded to whole groups of 16 lanes (128
-// values: a word of scales).  16384 x 2048 (169 MB): 40 us with one CTA of 768 threads an SM, 44-46 with 256-thread CTAs (or
-// without the loads ahead); a call that does not fill one round of the large CTAs takes the small ones (48 x 2048: 2.8 us
-// against 3.3).  What is left above the bytes (25 us) is issue: about 27 instructions a value, two of them for the test of
-// the borders.
+// A thread takes 16 values at a time (two vectors of gate, two of up: four loads of 16 bytes), the next ones' loads in
+// flight; rows are padded to whole groups of 8 lanes (128 values: a word of scales).  16384 x 2048 (169 MB): 33.6 us with one
+// CTA of 512 threads an SM, that is 5.0 TB/s; 39.8 with 8 values at a time and 768 threads (twice the votes, shuffles and
+// scale stores a value, half the bytes in flight a thread); 34.0 with two CTAs of 256 threads, 39 with 384 threads, 41.6 with
+// 768 (registers spill; 640 threads spill a little and take 33.0).  A call that does not fill one round of the large CTAs
+// takes the small ones (48 x 2048: 3.2 us against 3.7; 2048 x 2048: 10.1 against 8.5).
 template <int kNT, int kBlockLanes>
 __global__ void __launch_bounds__(kNT)
 swiglu_kernel(const uint16_t *__restrict__ gu, int64_t T, int F, int lanes_row, MxOut mx) {
@@ -300,17 +329,20 @@ swiglu_kernel(const uint16_t *__restrict__ gu, int64_t T, int F, int lanes_row, 
     const int dv = (int)(step - dt * lanes_row);
     int64_t t = first / lanes_row;
     int v = (int)(first - t * lanes_row);
-    uint4 g, u;
+    uint4 g[2], u[2];
     bool on;
     auto load = [&]() {
-        on = t < T && v * kVec < F;
-        const uint16_t *src = gu + t * 2 * (int64_t)F + (int64_t)v * kVec;
-        g = on ? ld_stream(src) : make_uint4(0u, 0u, 0u, 0u);
-        u = on ? ld_stream(src + F) : make_uint4(0u, 0u, 0u, 0u);
+        on = t < T && v * kLaneVals < F;
+        const uint16_t *src = gu + t * 2 * (int64_t)F + (int64_t)v * kLaneVals;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            g[h] = on ? ld_stream(src + 8 * h) : make_uint4(0u, 0u, 0u, 0u);
+            u[h] = on ? ld_stream(src + F + 8 * h) : make_uint4(0u, 0u, 0u, 0u);
+        }
     };
     load();
     for (int64_t n = (int64_t)blockIdx.x * kNT; n < T * lanes_row; n += step) {  // the same for the whole block
-        const uint4 g0 = g, u0 = u;
+        const uint4 g0[2] = {g[0], g[1]}, u0[2] = {u[0], u[1]};
         const bool on0 = on;
         const int64_t t0 = t;
         const int v0 = v;
@@ -321,7 +353,7 @@ swiglu_kernel(const uint16_t *__restrict__ gu, int64_t T, int F, int lanes_row, 
             ++t;
         }
         load();
-        swiglu_vec<kBlockLanes>(g0, u0, on0, mx.q + t0 * F + (int64_t)v0 * kVec, mx.scale + mx_scale_row(t0, F), v0, F, mx.mode);
+        swiglu_vals<kBlockLanes>(g0, u0, on0, mx.q + t0 * F + (int64_t)v0 * kLaneVals, mx.scale + mx_scale_row(t0, F), v0, F, mx.mode);
     }
 }
 
@@ -371,14 +403,14 @@ cudaError_t launch_add_rmsnorm(const uint16_t *x, const uint16_t *residual, cons
 
 cudaError_t launch_swiglu(const uint16_t *gate_up, int64_t T, int F, const MxOut &mx, int block, int num_sms,
                           cudaStream_t stream) {
-    const int lanes_row = (F / kVec + 15) / 16 * 16;
+    const int lanes_row = (F / kLaneVals + 7) / 8 * 8;
     const int64_t n = T * lanes_row;
-    if (n >= (int64_t)num_sms * 768) {
-        auto kern = block == 128 ? swiglu_kernel<768, 16> : swiglu_kernel<768, 4>;
-        return launch_pdl(kern, (unsigned)num_sms, 768, stream, gate_up, T, F, lanes_row, mx);
+    if (n >= (int64_t)num_sms * 512) {
+        auto kern = block == 128 ? swiglu_kernel<512, 8> : swiglu_kernel<512, 2>;
+        return launch_pdl(kern, (unsigned)num_sms, 512, stream, gate_up, T, F, lanes_row, mx);
     }
-    auto kern = block == 128 ? swiglu_kernel<256, 16> : swiglu_kernel<256, 4>;
-    return launch_pdl(kern, (unsigned)((n + 255) / 256), 256, stream, gate_up, T, F, lanes_row, mx);
+    auto kern = block == 128 ? swiglu_kernel<128, 8> : swiglu_kernel<128, 2>;
+    return launch_pdl(kern, (unsigned)((n + 127) / 128), 128, stream, gate_up, T, F, lanes_row, mx);
 }
 
 }  // namespace mhc
