@@ -39,7 +39,8 @@ def check(got, x, w, label=""):
 SIZES = [(1, 32, 8), (1, 128, 128), (3, 96, 136), (6, 7168, 1024), (16, 256, 384), (17, 1056, 264), (32, 512, 1000),
          (33, 544, 520), (64, 2048, 256), (65, 288, 136), (128, 1024, 1032), (129, 4064, 328), (300, 1056, 520),
          (513, 2080, 776), (1000, 160, 2056), (2049, 320, 1160),
-         (3000, 1056, 7176), (4100, 544, 4104), (5000, 96, 4096)]  # the last ones: pairs of CTAs
+         (3000, 1056, 7176), (4100, 544, 4104), (5000, 96, 4096),  # the last ones: pairs of CTAs
+         (700, 416, 7168), (697, 2080, 7176), (1500, 544, 4096), (1531, 256, 4104)]  # on narrower tiles
 
 
 @pytest.mark.parametrize("wide", [False, True], ids=["ue8m0", "f32scale"])
