@@ -86,30 +86,34 @@ __device__ __forceinline__ void mx_store(const float2 (&u)[4], int E, bool on, u
 }
 
 // ---- residual addition + RMSNorm ---------------------------------------------------------------------
-// One CTA per token.  Rows of at most kNT * kV vectors stay in registers (kV loads of each input in flight
-// per thread); longer ones (kV == 0) are read again after the square sum, from L2.  8192 x 7168 with the residual
-// (413 MB): 75 us, 5.5 TB/s, with 448 threads of two vectors, four CTAs an SM; 224 threads of four 83-98 us, 896 of one
-// 162 us (a CTA waits for its row's sum, so what counts is how many rows an SM has in flight).
+// A CTA takes rows in turn.  Rows of at most kNT * kV vectors stay in registers, and the next row's loads are in flight while
+// a row's sum is awaited and its results are stored; longer ones (kV == 0: a CTA a row) are read again after the square sum,
+// from L2.  8192 x 7168 with the residual (413 MB): 67.3 us, 6.1 TB/s, with 448 threads of two vectors, two CTAs an SM;
+// without the loads ahead, four CTAs an SM, 75.5; three CTAs with the loads ahead spill: 86.
+// CTAs an SM (8192 rows of 512 to 4096 with one vector a thread: 6.6 to 41.5 us with 1536 threads an SM, 7.9 to 42.1 with
+// 1024, 7.4 to 40.9 with 2048, where 333 rows of 4096 take 4.2 us for 3.4).
+constexpr int norm_ctas(int nt, int v) { return v == 0 ? 4 : v == 2 ? 2 : 1536 / nt; }
 template <int kNT, int kV, int kBlockLanes>
-__global__ void __launch_bounds__(kNT, kNT >= 448 ? 4 : 1)
-add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, const uint16_t *__restrict__ gamma, int H,
+__global__ void __launch_bounds__(kNT, norm_ctas(kNT, kV))
+add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, const uint16_t *__restrict__ gamma, int64_t T, int H,
                    float eps, uint16_t *R_out, uint16_t *__restrict__ X_out, MxOut mx) {
-    __shared__ float sWarp[kNT / 32];
+    __shared__ float sWarp[2][kNT / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int64_t t = blockIdx.x, at = t * (int64_t)H + (int64_t)threadIdx.x * kVec;  // this thread's first vector
     const int tid = threadIdx.x, nvec = H / kVec;
     constexpr int kRegs = kV > 0 ? kV : 1;
-    uint4 s[kRegs];
-    const uint16_t *const xr = x + at, *const rr = residual != nullptr ? residual + at : nullptr;
-    auto load = [&](int off) {  // bf16(x + residual) of one vector, `off` values after the first
-        uint4 a = ld_stream(xr + off);
-        if (rr != nullptr) {
-            const uint4 b = __ldcs(reinterpret_cast<const uint4 *>(rr + off));
-            a = make_uint4(add2(a.x, b.x), add2(a.y, b.y), add2(a.z, b.z), add2(a.w, b.w));
+    uint4 a[kRegs], b[kRegs];
+    // this thread's vectors of row t, of both inputs
+    auto fetch = [&](int64_t t) {
+        const int64_t at = t * (int64_t)H + tid * kVec;
+#pragma unroll
+        for (int k = 0; k < kRegs; ++k) {
+            const bool on = tid + k * kNT < nvec;
+            a[k] = on ? ld_stream(x + at + k * kNT * kVec) : make_uint4(0u, 0u, 0u, 0u);
+            b[k] = on && residual != nullptr ? __ldcs(reinterpret_cast<const uint4 *>(residual + at + k * kNT * kVec)) : make_uint4(0u, 0u, 0u, 0u);
         }
-        return a;
     };
+    auto added = [&](uint4 p, uint4 q) { return residual != nullptr ? make_uint4(add2(p.x, q.x), add2(p.y, q.y), add2(p.z, q.z), add2(p.w, q.w)) : p; };
     auto squares = [&](uint4 a) {
         float f[8];
         unpack8(a, f);
@@ -118,68 +122,76 @@ add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, con
         for (int e = 2; e < 8; e += 2) q = __ffma2_rn(make_float2(f[e], f[e + 1]), make_float2(f[e], f[e + 1]), q);
         return q.x + q.y;
     };
-    float sum = 0.f;
-    if constexpr (kV > 0) {
+    if (kV > 0) fetch(blockIdx.x);
+    int odd = 0;
+    for (int64_t t = blockIdx.x; t < T; t += gridDim.x, odd ^= 1) {
+        const int64_t at = t * (int64_t)H + (int64_t)tid * kVec;
+        auto again = [&](int off) {  // (rows that do not stay in registers)
+            const uint4 p = ld_stream(x + at + off);
+            return added(p, residual != nullptr ? __ldcs(reinterpret_cast<const uint4 *>(residual + at + off)) : p);
+        };
+        uint4 s[kRegs];
+        float sum = 0.f;
+        if constexpr (kV > 0) {
 #pragma unroll
-        for (int k = 0; k < kV; ++k) {
-            const int v = tid + k * kNT;
-            s[k] = v < nvec ? load(k * kNT * kVec) : make_uint4(0u, 0u, 0u, 0u);
+            for (int k = 0; k < kV; ++k) s[k] = added(a[k], b[k]);
+            if (t + gridDim.x < T) fetch(t + gridDim.x);
+#pragma unroll
+            for (int k = 0; k < kV; ++k) sum += squares(s[k]);
+        } else {
+            for (int v = tid; v < nvec; v += kNT) sum += squares(again((v - tid) * kVec));
         }
+        sum = warp_sum(sum);
+        if ((tid & 31) == 0) sWarp[odd][tid >> 5] = sum;
+        __syncthreads();
+        float hi = (tid & 31) < kNT / 32 ? sWarp[odd][tid & 31] : 0.f;
+        hi = warp_sum(hi);
+        // 1 / sqrt(v), v = sum / H + eps, as rh + rl: an approximation and one Newton step whose residual 1 - v rh^2 is taken
+        // with exact products (fp64 here was what the prefill's time went to: 151 us)
+        const float inv = 1.f / (float)H, inv_lo = fmaf(-inv, (float)H, 1.f) * inv;
+        const float mh = hi * inv, ml = fmaf(hi, inv, -mh) + hi * inv_lo;
+        const float vh = mh + eps, vz = vh - mh, vl = ((mh - (vh - vz)) + (eps - vz)) + ml;
+        const float rh = rsqrtf(vh);
+        const float ph = rh * rh, pl = fmaf(rh, rh, -ph);
+        const float res = fmaf(-vh, ph, 1.f) - fmaf(vh, pl, vl * ph);
+        const float rl = vh > 0.f && vh < __int_as_float(0x7f800000) ? 0.5f * rh * res : 0.f;
+        uint8_t *const scale = mx.q != nullptr ? mx.scale + mx_scale_row(t, H) : nullptr;
+        const float2 rh2 = make_float2(rh, rh), rl2 = make_float2(rl, rl);
+        auto finish = [&](uint4 a, int off) {
+            const int v = tid + off / kVec;
+            const bool on = v < nvec;
+            float f[8], g[8];
+            unpack8(a, f);
+            unpack8(on ? ld_ro(gamma + tid * kVec + off) : make_uint4(0u, 0u, 0u, 0u), g);
+            if (on && R_out != nullptr) st_stream(R_out + at + off, a);
 #pragma unroll
-        for (int k = 0; k < kV; ++k) sum += squares(s[k]);
-    } else {
-        for (int v = tid; v < nvec; v += kNT) sum += squares(load((v - tid) * kVec));
-    }
-    sum = warp_sum(sum);
-    if ((tid & 31) == 0) sWarp[tid >> 5] = sum;
-    __syncthreads();
-    float hi = (tid & 31) < kNT / 32 ? sWarp[tid & 31] : 0.f;
-    hi = warp_sum(hi);
-    // 1 / sqrt(v), v = sum / H + eps, as rh + rl: an approximation and one Newton step whose residual 1 - v rh^2 is taken
-    // with exact products (fp64 here was what the prefill's time went to: 151 us)
-    const float inv = 1.f / (float)H, inv_lo = fmaf(-inv, (float)H, 1.f) * inv;
-    const float mh = hi * inv, ml = fmaf(hi, inv, -mh) + hi * inv_lo;
-    const float vh = mh + eps, vz = vh - mh, vl = ((mh - (vh - vz)) + (eps - vz)) + ml;
-    const float rh = rsqrtf(vh);
-    const float ph = rh * rh, pl = fmaf(rh, rh, -ph);
-    const float res = fmaf(-vh, ph, 1.f) - fmaf(vh, pl, vl * ph);
-    const float rl = vh > 0.f && vh < __int_as_float(0x7f800000) ? 0.5f * rh * res : 0.f;
-    uint8_t *const scale = mx.q != nullptr ? mx.scale + mx_scale_row(t, H) : nullptr;
-    const float2 rh2 = make_float2(rh, rh), rl2 = make_float2(rl, rl);
-    auto finish = [&](uint4 a, int off) {
-        const int v = tid + off / kVec;
-        const bool on = v < nvec;
-        float f[8], g[8];
-        unpack8(a, f);
-        unpack8(on ? ld_ro(gamma + tid * kVec + off) : make_uint4(0u, 0u, 0u, 0u), g);
-        if (on && R_out != nullptr) st_stream(R_out + at + off, a);
+            for (int e = 0; e < 8; e += 2) {
+                const float2 q = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(g[e], g[e + 1]));  // exact
+                const float2 o = __ffma2_rn(q, rh2, __fmul2_rn(q, rl2));
+                f[e] = o.x;
+                f[e + 1] = o.y;
+            }
+            const uint4 y = pack8_rn(f);
+            if (on && X_out != nullptr) st_stream(X_out + at + off, y);
+            if (mx.q != nullptr) {
+                unpack8(y, f);
+                const float amax = group_max<kBlockLanes>(on ? absmax8(y) : 0.f);
+                const int E = mx_exp(amax, mx.mode);
+                const float sc = inv_pow2(E);
+                float2 u[4];
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            const float2 q = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(g[e], g[e + 1]));  // exact
-            const float2 o = __ffma2_rn(q, rh2, __fmul2_rn(q, rl2));
-            f[e] = o.x;
-            f[e + 1] = o.y;
+                for (int e = 0; e < 8; e += 2) u[e / 2] = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(sc, sc));
+                mx_store<kBlockLanes>(u, E, on, mx.q + at + off, scale, v, H);
+            }
+        };
+        if constexpr (kV > 0) {
+#pragma unroll
+            for (int k = 0; k < kV; ++k)
+                if (k == 0 || k * kNT < nvec) finish(s[k], k * kNT * kVec);
+        } else {
+            for (int v0 = 0; v0 < nvec; v0 += kNT)  // whole groups of lanes: the maxima are exchanged
+                finish(v0 + tid < nvec ? again(v0 * kVec) : make_uint4(0u, 0u, 0u, 0u), v0 * kVec);
         }
-        const uint4 y = pack8_rn(f);
-        if (on && X_out != nullptr) st_stream(X_out + at + off, y);
-        if (mx.q != nullptr) {
-            unpack8(y, f);
-            const float amax = group_max<kBlockLanes>(on ? absmax8(y) : 0.f);
-            const int E = mx_exp(amax, mx.mode);
-            const float sc = inv_pow2(E);
-            float2 u[4];
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) u[e / 2] = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(sc, sc));
-            mx_store<kBlockLanes>(u, E, on, mx.q + at + off, scale, v, H);
-        }
-    };
-    if constexpr (kV > 0) {
-#pragma unroll
-        for (int k = 0; k < kV; ++k)
-            if (k == 0 || k * kNT < nvec) finish(s[k], k * kNT * kVec);
-    } else {
-        for (int v0 = 0; v0 < nvec; v0 += kNT)  // whole groups of lanes: the maxima are exchanged
-            finish(v0 + tid < nvec ? load(v0 * kVec) : make_uint4(0u, 0u, 0u, 0u), v0 * kVec);
     }
 }
 
@@ -377,9 +389,9 @@ cudaError_t launch_pdl(void (*kern)(P...), unsigned grid, unsigned block, cudaSt
 
 template <int kNT, int kV>
 cudaError_t launch_norm_nv(const uint16_t *x, const uint16_t *residual, const uint16_t *gamma, int64_t T, int H, float eps,
-                           uint16_t *R_out, uint16_t *X_out, const MxOut &mx, int block, cudaStream_t stream) {
+                           uint16_t *R_out, uint16_t *X_out, const MxOut &mx, int block, int num_sms, cudaStream_t stream) {
     auto kern = block == 128 ? add_rmsnorm_kernel<kNT, kV, 16> : add_rmsnorm_kernel<kNT, kV, 4>;
-    return launch_pdl(kern, (unsigned)T, kNT, stream, x, residual, gamma, H, eps, R_out, X_out, mx);
+    return launch_pdl(kern, (unsigned)std::min<int64_t>(T, kV == 0 ? T : (int64_t)num_sms * norm_ctas(kNT, kV)), kNT, stream, x, residual, gamma, T, H, eps, R_out, X_out, mx);
 }
 
 }  // namespace
@@ -387,18 +399,18 @@ cudaError_t launch_norm_nv(const uint16_t *x, const uint16_t *residual, const ui
 cudaError_t launch_add_rmsnorm(const uint16_t *x, const uint16_t *residual, const uint16_t *gamma, int64_t T, int H,
                                float eps, uint16_t *R_out, uint16_t *X_out, const MxOut &mx, int block, int num_sms,
                                cudaStream_t stream) {
-    (void)num_sms;
     const int nvec = H / kVec;
     // The fewest threads that hold the row with one vector each, from 513 vectors with two (us at 8192 rows with the
-    // residual: H = 512: 64 x 1 8.9, 256 x 1 15; 2048: 256 x 1 24.5, 128 x 2 24.1, 64 x 4 28.0; 4096: 512 x 1 45.3, 256 x 2
-    // 47.8; 7168: 448 x 2 75, 512 threads reading the row twice 84.8; 8192: 512 x 2 85.6, 256 x 4 97, twice 89.5).
-    if (nvec <= 64) return launch_norm_nv<64, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
-    if (nvec <= 128) return launch_norm_nv<128, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
-    if (nvec <= 256) return launch_norm_nv<256, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
-    if (nvec <= 512) return launch_norm_nv<512, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
-    if (nvec <= 896) return launch_norm_nv<448, 2>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
-    if (nvec <= 1024) return launch_norm_nv<512, 2>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
-    return launch_norm_nv<512, 0>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, stream);
+    // residual, a CTA a row: H = 512: 64 x 1 8.9, 256 x 1 15; 2048: 256 x 1 24.5, 128 x 2 24.1, 64 x 4 28.0; 4096: 512 x 1
+    // 45.3, 256 x 2 47.8; 7168: 448 x 2 75, 512 threads reading the row twice 84.8; 8192: 512 x 2 85.6, 256 x 4 97, twice
+    // 89.5.  With rows in turn 6.6, 21.7, 41.5, 66.8 and 73.9).
+    if (nvec <= 64) return launch_norm_nv<64, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, num_sms, stream);
+    if (nvec <= 128) return launch_norm_nv<128, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, num_sms, stream);
+    if (nvec <= 256) return launch_norm_nv<256, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, num_sms, stream);
+    if (nvec <= 512) return launch_norm_nv<512, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, num_sms, stream);
+    if (nvec <= 896) return launch_norm_nv<448, 2>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, num_sms, stream);
+    if (nvec <= 1024) return launch_norm_nv<512, 2>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, num_sms, stream);
+    return launch_norm_nv<512, 0>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, num_sms, stream);
 }
 
 cudaError_t launch_swiglu(const uint16_t *gate_up, int64_t T, int F, const MxOut &mx, int block, int num_sms,

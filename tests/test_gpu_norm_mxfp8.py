@@ -111,8 +111,35 @@ def test_residual_in_place_padding_untouched_and_special_rows(mhc, H):
     assert bool(v[[0, 4, 5]].isfinite().all())
 
 
+@pytest.mark.parametrize("T,H", [(9001, 512), (5003, 992), (3001, 2048), (1501, 4096), (1003, 7168), (1201, 8192), (700, 8224)])
+def test_rows_in_turn(mhc, T, H):
+    """More rows than run at once: those of the formula, and the bits of calls of a few rows, the residual in place or not;
+    NaN and infinity stay in their rows."""
+    x, r, w = norm_inputs(T, H, T)
+    x[T // 2, 3] = float("nan")
+    x[T // 3, H - 1] = float("inf")
+    o = mhc.add_rmsnorm_mxfp8(x, r, w, rmsnorm_eps=2e-6, want_bf16=True)
+    mild = torch.ones(T, dtype=torch.bool, device="cuda")
+    mild[[T // 2, T // 3]] = False
+    y = norm_ref(o["residual_out"][mild], w, 2e-6)
+    assert bool(((o["layer_in"][mild].double() - y).abs() <= (2.0 ** -8 + 2.0 ** -19) * y.abs() + 2.0 ** -133).all())
+    assert bool(o["layer_in"][T // 2].isnan().all()) and not bool(o["layer_in"][mild].isnan().any())
+    idx = ref.scale_index(T, H, "cuda")
+    for lo in (0, T // 2 - 50, T - 100):
+        few = mhc.add_rmsnorm_mxfp8(x[lo:lo + 100].clone(), r[lo:lo + 100].clone(), w, rmsnorm_eps=2e-6, want_bf16=True)
+        for k in ("residual_out", "layer_in"):
+            assert torch.equal(few[k].view(torch.int16), o[k][lo:lo + 100].view(torch.int16))
+        assert torch.equal(few["layer_in_fp8"], o["layer_in_fp8"][lo:lo + 100])
+        assert torch.equal(few["layer_in_scales"][ref.scale_index(100, H, "cuda")], o["layer_in_scales"][idx[lo:lo + 100]])
+    again = mhc.add_rmsnorm_mxfp8(x, r, w, rmsnorm_eps=2e-6, out={"residual_out": r})
+    assert torch.equal(r.view(torch.int16), o["residual_out"].view(torch.int16))
+    assert torch.equal(again["layer_in_fp8"], o["layer_in_fp8"])
+    assert torch.equal(again["layer_in_scales"][idx], o["layer_in_scales"][idx])
+
+
 @pytest.mark.parametrize("block,mode", [(32, 0), (32, 1), (128, 0), (128, 1)])
-@pytest.mark.parametrize("T,F", [(1, 32), (1, 2048), (3, 96), (48, 2048), (130, 160), (77, 1056), (1000, 512), (2, 65536)])
+@pytest.mark.parametrize("T,F", [(1, 32), (1, 2048), (3, 96), (48, 2048), (130, 160), (77, 1056), (1000, 512), (2, 65536),
+                                 (5000, 544), (4097, 2048)])  # several rounds
 def test_swiglu_against_64_bits(mhc, T, F, block, mode):
     g = torch.Generator(device="cuda").manual_seed(T + F)
     gu = (torch.randn(T, 2 * F, generator=g, device="cuda") * 10.0 ** (2 * torch.rand(T, 1, generator=g, device="cuda") - 1)).bfloat16()
