@@ -718,17 +718,14 @@ mhc_status mhc_pre_prepacked(const mhc_bf16 *residual, const float *phi, const v
 
 namespace {
 
-mhc_status check_mx(const uint8_t *codes, const uint8_t *scales, const char *codes_name, int64_t cols, int scale_mode,
-                    int scale_block) {
-    mhc_status st;
+mhc_status check_mx(const uint8_t *codes, const uint8_t *scales, const char *codes_name, const char *scales_name, int64_t cols,
+                    int scale_mode, int scale_block) {
     if (cols % 32 != 0) return fail(MHC_ERR_INVALID_ARG, "the MXFP8 output needs a row of a multiple of 32 values (%lld)", (long long)cols);
     if (scale_mode != MHC_MX_SCALE_FLOOR && scale_mode != MHC_MX_SCALE_CEIL)
         return fail(MHC_ERR_INVALID_ARG, "unknown MXFP8 scale mode %d", scale_mode);
     if (scale_block != MHC_MX_BLOCK_32 && scale_block != MHC_MX_BLOCK_128)
         return fail(MHC_ERR_INVALID_ARG, "scale_block must be 32 or 128, not %d", scale_block);
-    if ((st = check_ptrs({{codes, codes_name}})) != MHC_OK) return st;
-    if (scales == nullptr) return fail(MHC_ERR_INVALID_ARG, "the scales of %s are NULL", codes_name);
-    return MHC_OK;
+    return check_ptrs({{codes, codes_name}, {scales, scales_name}});  // (the scales are stored as words of four)
 }
 
 mhc_status check_overlaps(std::initializer_list<std::pair<Span, const char *>> outs, std::initializer_list<Span> ins) {
@@ -810,7 +807,7 @@ mhc_status mhc_add_rmsnorm_mxfp8(const mhc_bf16 *x, const mhc_bf16 *residual, co
     const bool mx = layer_in_fp8 != nullptr || layer_in_scales != nullptr;
     if (layer_in_out != nullptr && (st = check_ptrs({{layer_in_out, "layer_in_out"}})) != MHC_OK) return st;
     if (!mx && layer_in_out == nullptr) return fail(MHC_ERR_INVALID_ARG, "layer_in_out and layer_in_fp8 are NULL");
-    if (mx && (st = check_mx(layer_in_fp8, layer_in_scales, "layer_in_fp8", H, scale_mode, scale_block)) != MHC_OK) return st;
+    if (mx && (st = check_mx(layer_in_fp8, layer_in_scales, "layer_in_fp8", "layer_in_scales", H, scale_mode, scale_block)) != MHC_OK) return st;
     const size_t n = (size_t)T * (size_t)H;
     const bool in_place = residual_out != nullptr && residual_out == residual;
     if ((st = check_overlaps({{{residual_out, n * 2}, "residual_out"}, {{layer_in_out, n * 2}, "layer_in_out"},
@@ -834,7 +831,7 @@ mhc_status mhc_swiglu_mxfp8(const mhc_bf16 *gate_up, int64_t T, int64_t F, uint8
     if ((st = check_sizes(T, F)) != MHC_OK) return st;
     if (T == 0) return MHC_OK;
     if ((st = check_ptrs({{gate_up, "gate_up"}})) != MHC_OK) return st;
-    if ((st = check_mx(act_fp8, act_scales, "act_fp8", F, scale_mode, scale_block)) != MHC_OK) return st;
+    if ((st = check_mx(act_fp8, act_scales, "act_fp8", "act_scales", F, scale_mode, scale_block)) != MHC_OK) return st;
     const size_t n = (size_t)T * (size_t)F;
     if ((st = check_overlaps({{{act_fp8, n}, "act_fp8"}, {{act_scales, mx_scale_bytes(T, F)}, "act_scales"}}, {{gate_up, n * 4}})) != MHC_OK)
         return st;

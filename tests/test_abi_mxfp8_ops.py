@@ -107,3 +107,10 @@ def test_binding_refuses_host_tensors(mhc_lib):
         mhc_lib.linear_mxfp8(q, torch.zeros(512, dtype=torch.uint8), q, torch.zeros((1, 1)), workspace=q)
     with pytest.raises((ValueError, RuntimeError)):
         mhc_lib.expert_linear_mxfp8(q, torch.zeros(512, dtype=torch.uint8), q[None], torch.zeros((1, 1, 1)), torch.zeros(2, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("off", [1, 2, 4, 8])
+def test_misaligned_scale_outputs_are_refused(L, off):
+    """The producers store four scale bytes as a word, so their scales are 16-byte aligned like every other pointer."""
+    refused(L, norm(L, s=fake(6, off)), "layer_in_scales is not 16-byte aligned")
+    refused(L, swiglu(L, s=fake(2, off)), "act_scales is not 16-byte aligned")
