@@ -373,7 +373,8 @@ typedef enum mhc_mx_scale_block { MHC_MX_BLOCK_32 = 32, MHC_MX_BLOCK_128 = 128 }
  *   layer_in_fp8, layer_in_scales   MXFP8 of the bf16 y as in mhc_shifted_post_pre_mxfp8 (H % 32 == 0),
  *                                   or both NULL; one of y's two forms is required
  *   scale_mode       mhc_mx_scale_mode;  scale_block  mhc_mx_scale_block
- * One launch, no workspace. */
+ * Rows of any magnitude: those whose mean s^2 + rmsnorm_eps is outside [2^-40, 2^60] are computed in fp64, which
+ * takes longer.  A row of zeros with rmsnorm_eps 0 is NaN (0 / 0).  One launch, no workspace. */
 MHC_API mhc_status mhc_add_rmsnorm_mxfp8(const mhc_bf16 *x, const mhc_bf16 *residual, const mhc_bf16 *rmsnorm_weight,
                                          int64_t T, int64_t H, float rmsnorm_eps, mhc_bf16 *residual_out,
                                          mhc_bf16 *layer_in_out, uint8_t *layer_in_fp8, uint8_t *layer_in_scales,

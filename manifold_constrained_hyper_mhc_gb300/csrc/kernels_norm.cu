@@ -86,9 +86,84 @@ __device__ __forceinline__ void mx_store(const float2 (&u)[4], int E, bool on, u
 }
 
 // ---- residual addition + RMSNorm ---------------------------------------------------------------------
+// fp32 holds a row's squares, its root and the products s * gamma where v = mean s^2 + eps is in [2^-40, 2^60] (eps 1e-12 is;
+// a product below fp32's range is off by 2^-150, times a root of at most 2^20).  A CTA that met a row beyond ("far": zeros, or
+// next to nothing, with a smaller eps; magnitudes past 2^30; infinities, NaN) looks its rows over again at its end and computes
+// the far ones in fp64, each thread over its own results.  The borders there lie a little outside those that send it there, so
+// a row's result does not depend on the rows beside it.
+// Kept out of the loop over the rows, without loops unrolled and without fp64's division and root (they are calls), this costs
+// the other rows nothing up to 8192 values a row; longer ones, in 32 registers, 6 % (4096 x 16384 83.4 -> 88.9 us).  The same
+// row taken again in the loop, in fp64 or scaled, cost every row up to 25 %.
+constexpr uint32_t kMeanMinBits = (127u - 40u) << 23, kMeanMaxBits = (127u + 60u) << 23;
+template <int kNT, int kBlockLanes>
+__device__ __forceinline__ void norm_far_rows(const uint16_t *x, const uint16_t *residual, const uint16_t *gamma, int64_t T, int H,
+                                              float eps, uint16_t *R_out, uint16_t *X_out, const MxOut &mx, double *parts) {
+    const int tid = threadIdx.x, nvec = H / kVec;
+    const double inv_0 = (double)(1.f / (float)H), inv_h = inv_0 * fma(-inv_0, (double)H, 2.0);
+    const double inf = __hiloint2double(0x7FF00000, 0);
+    auto two_to = [](int e) { return __hiloint2double((int)((uint32_t)(1023 + e) << 20), 0); };
+#pragma unroll 1
+    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+        const int64_t at = t * (int64_t)H;
+        const uint16_t *p = (R_out != nullptr ? R_out : x) + at;  // s: R_out may have replaced the residual
+        const uint16_t *q = R_out != nullptr || residual == nullptr ? nullptr : residual + at;
+        auto row = [&](int v) {
+            const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p) + v);
+            if (q == nullptr) return a;
+            const uint4 b = __ldcs(reinterpret_cast<const uint4 *>(q) + v);
+            return make_uint4(add2(a.x, b.x), add2(a.y, b.y), add2(a.z, b.z), add2(a.w, b.w));
+        };
+        double sum = 0.0;
+#pragma unroll 1
+        for (int v = tid; v < nvec; v += kNT) {
+            float f[8];
+            unpack8(row(v), f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = fma((double)f[e], (double)f[e], sum);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        __syncthreads();  // `parts` has been read
+        if ((tid & 31) == 0) parts[tid >> 5] = sum;
+        __syncthreads();
+        sum = 0.0;
+#pragma unroll 1
+        for (int w = 0; w < kNT / 32; ++w) sum += parts[w];
+        const double v = fma(sum, inv_h, (double)eps);
+        if (v > 0.99 * 9.094947017729282e-13 && v < 1.01 * 1.152921504606847e18) continue;
+        // 1 / sqrt(v): v = m 4^k with m in [1, 4), an fp32 estimate of m's and one Newton step
+        const int k = ((int)((uint32_t)__double2hiint(v) >> 20) - 1023) >> 1;
+        const double m = v * two_to(-2 * k), r0 = (double)rsqrtf((float)m);
+        double r = r0 * fma(-0.5 * m, r0 * r0, 1.5) * two_to(-k);
+        if (!(v > 0.0 && v < inf)) r = v == 0.0 ? inf : v > 0.0 ? 0.0 : v;
+        uint8_t *const scale = mx.q != nullptr ? mx.scale + mx_scale_row(t, H) : nullptr;
+#pragma unroll 1
+        for (int v0 = 0; v0 < nvec; v0 += kNT) {  // whole groups of lanes: the maxima are exchanged
+            const int v = v0 + tid;
+            const bool on = v < nvec;
+            float f[8], g[8];
+            unpack8(on ? row(v) : make_uint4(0u, 0u, 0u, 0u), f);
+            unpack8(on ? ld_ro(gamma + v * kVec) : make_uint4(0u, 0u, 0u, 0u), g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = (float)((double)f[e] * (double)g[e] * r);
+            const uint4 y = pack8_rn(f);
+            if (on && X_out != nullptr) st_stream(X_out + at + v * kVec, y);
+            if (mx.q != nullptr) {
+                unpack8(y, f);
+                const int E = mx_exp(group_max<kBlockLanes>(on ? absmax8(y) : 0.f), mx.mode);
+                const float sc = inv_pow2(E);
+                float2 u[4];
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) u[e / 2] = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(sc, sc));
+                mx_store<kBlockLanes>(u, E, on, mx.q + at + v * kVec, scale, v, H);
+            }
+        }
+    }
+}
+
 // A CTA takes rows in turn.  Rows of at most kNT * kV vectors stay in registers, and the next row's loads are in flight while
 // a row's sum is awaited and its results are stored; longer ones (kV == 0: a CTA a row) are read again after the square sum,
-// from L2.  8192 x 7168 with the residual (413 MB): 67.3 us, 6.1 TB/s, with 448 threads of two vectors, two CTAs an SM;
+// from L2.  8192 x 7168 with the residual (413 MB): 64.3 us, 6.4 TB/s, with 448 threads of two vectors, two CTAs an SM;
 // without the loads ahead, four CTAs an SM, 75.5; three CTAs with the loads ahead spill: 86.
 // CTAs an SM (8192 rows of 512 to 4096 with one vector a thread: 6.6 to 41.5 us with 1536 threads an SM, 7.9 to 42.1 with
 // 1024, 7.4 to 40.9 with 2048, where 333 rows of 4096 take 4.2 us for 3.4).
@@ -98,6 +173,7 @@ __global__ void __launch_bounds__(kNT, norm_ctas(kNT, kV))
 add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, const uint16_t *__restrict__ gamma, int64_t T, int H,
                    float eps, uint16_t *R_out, uint16_t *__restrict__ X_out, MxOut mx) {
     __shared__ float sWarp[2][kNT / 32];
+    __shared__ double sParts[kNT / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, nvec = H / kVec;
@@ -122,6 +198,7 @@ add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, con
         for (int e = 2; e < 8; e += 2) q = __ffma2_rn(make_float2(f[e], f[e + 1]), make_float2(f[e], f[e + 1]), q);
         return q.x + q.y;
     };
+    bool any_far = false;  // the same in the whole CTA
     if (kV > 0) fetch(blockIdx.x);
     int odd = 0;
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x, odd ^= 1) {
@@ -151,10 +228,11 @@ add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, con
         const float inv = 1.f / (float)H, inv_lo = fmaf(-inv, (float)H, 1.f) * inv;
         const float mh = hi * inv, ml = fmaf(hi, inv, -mh) + hi * inv_lo;
         const float vh = mh + eps, vz = vh - mh, vl = ((mh - (vh - vz)) + (eps - vz)) + ml;
+        any_far |= __float_as_uint(vh) - kMeanMinBits > kMeanMaxBits - kMeanMinBits;  // (NaN too)
         const float rh = rsqrtf(vh);
         const float ph = rh * rh, pl = fmaf(rh, rh, -ph);
         const float res = fmaf(-vh, ph, 1.f) - fmaf(vh, pl, vl * ph);
-        const float rl = vh > 0.f && vh < __int_as_float(0x7f800000) ? 0.5f * rh * res : 0.f;
+        const float rl = 0.5f * rh * res;
         uint8_t *const scale = mx.q != nullptr ? mx.scale + mx_scale_row(t, H) : nullptr;
         const float2 rh2 = make_float2(rh, rh), rl2 = make_float2(rl, rl);
         auto finish = [&](uint4 a, int off) {
@@ -192,6 +270,13 @@ add_rmsnorm_kernel(const uint16_t *__restrict__ x, const uint16_t *residual, con
             for (int v0 = 0; v0 < nvec; v0 += kNT)  // whole groups of lanes: the maxima are exchanged
                 finish(v0 + tid < nvec ? again(v0 * kVec) : make_uint4(0u, 0u, 0u, 0u), v0 * kVec);
         }
+    }
+    if (any_far) {
+        // (what is known of these pointers is for the loop above, whose loads do not wait for its stores)
+        const uint16_t *x_again = x, *gamma_again = gamma;
+        uint16_t *X_again = X_out;
+        asm volatile("" : "+l"(x_again), "+l"(gamma_again), "+l"(X_again)::"memory");
+        norm_far_rows<kNT, kBlockLanes>(x_again, residual, gamma_again, T, H, eps, R_out, X_again, mx, sParts);
     }
 }
 
@@ -403,7 +488,7 @@ cudaError_t launch_add_rmsnorm(const uint16_t *x, const uint16_t *residual, cons
     // The fewest threads that hold the row with one vector each, from 513 vectors with two (us at 8192 rows with the
     // residual, a CTA a row: H = 512: 64 x 1 8.9, 256 x 1 15; 2048: 256 x 1 24.5, 128 x 2 24.1, 64 x 4 28.0; 4096: 512 x 1
     // 45.3, 256 x 2 47.8; 7168: 448 x 2 75, 512 threads reading the row twice 84.8; 8192: 512 x 2 85.6, 256 x 4 97, twice
-    // 89.5.  With rows in turn 6.6, 21.7, 41.5, 66.8 and 73.9).
+    // 89.5.  With rows in turn 6.3, 21.9, 40.9, 64.3 and 75.9).
     if (nvec <= 64) return launch_norm_nv<64, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, num_sms, stream);
     if (nvec <= 128) return launch_norm_nv<128, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, num_sms, stream);
     if (nvec <= 256) return launch_norm_nv<256, 1>(x, residual, gamma, T, H, eps, R_out, X_out, mx, block, num_sms, stream);
