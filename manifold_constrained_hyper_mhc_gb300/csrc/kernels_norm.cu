@@ -311,7 +311,7 @@ __device__ __noinline__ double silu_mul_f64(float a, float b) { return (double)a
 __device__ __forceinline__ uint32_t border_key(float u) { return (__float_as_uint(u) << 12) + ((0x80000u + kNear) << 12); }
 // The same for a maximum: near a power of two (or past fp32's range), or near 1.75 times one (mode 1).
 __device__ __forceinline__ bool near_exponent(float a, int mode) {
-    if (a < 7.7e-34f) return false;  // 2^-110: the exponent is the smallest one on either side (rows of zeros)
+    if (a < 1.5046328e-36f) return false;  // 2^-119: up to 2^-118 (mode 1: 1.75 2^-119) the exponent is the smallest one
     const uint32_t m = __float_as_uint(a) & 0x7FFFFFu;
     return m + kNear > 0x7FFFFFu || m < kNear || (mode == 1 && m - (0x600000u - kNear) <= 2 * kNear);
 }
