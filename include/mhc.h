@@ -383,7 +383,8 @@ MHC_API mhc_status mhc_add_rmsnorm_mxfp8(const mhc_bf16 *x, const mhc_bf16 *resi
 /* The SwiGLU between a gate/up and a down product: MXFP8 of silu(gate) * up.
  *   gate_up     [T,2F] bf16: columns 0..F-1 gate, F..2F-1 up
  *   act_fp8     [T,F] codes, act_scales  mhc_mxfp8_scale_bytes(T, F) bytes;  F % 32 == 0
- * The value is quantized from fp32 or better in one rounding (no bf16 in between).  One launch, no workspace. */
+ * The value is quantized from fp32 or better in one rounding (no bf16 in between), products past fp32's range too; an
+ * infinite one gives its block E = 120.  One launch, no workspace. */
 MHC_API mhc_status mhc_swiglu_mxfp8(const mhc_bf16 *gate_up, int64_t T, int64_t F, uint8_t *act_fp8, uint8_t *act_scales,
                                     int scale_mode, int scale_block, void *stream);
 

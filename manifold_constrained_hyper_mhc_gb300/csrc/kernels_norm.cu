@@ -384,16 +384,16 @@ __device__ __forceinline__ void swiglu_vals(const uint4 (&ga)[2], const uint4 (&
         u[e / 2] = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(sc, sc));
         key = min(key, min(border_key(u[e / 2].x), border_key(u[e / 2].y)));
     }
-    if (on && (key <= kNear << 13 || far)) {
+    const bool past = amax > 3.4028234663852886e38f;  // products past fp32's range: infinite here, their codes are not
+    if (on && (key <= kNear << 13 || far || past)) {
 #pragma unroll
         for (int e = 0; e < kLaneVals; ++e) {
             float &w = e & 1 ? u[e / 2].y : u[e / 2].x;
-            if (border_key(w) <= kNear << 13 || gate_far(a[e])) {
-                // the fp64 value, with whatever fp32 drops of it kept as a sticky last bit, rounds to the same code
-                const double d = silu_mul_f64(a[e], b[e]);
-                float h = __double2float_rz(d);
-                if ((double)h != d) h = __uint_as_float(__float_as_uint(h) | 1u);
-                w = (fabs(d) > 3.4028234663852886e38 ? (float)d : h) * sc;  // past fp32's range: infinite, the largest code
+            if (border_key(w) <= kNear << 13 || gate_far(a[e]) || (past && isinf(w))) {
+                // the fp64 value over 2^E, with whatever fp32 drops of it kept as a sticky last bit, rounds to the same code
+                const double d = silu_mul_f64(a[e], b[e]) * (double)sc;
+                w = __double2float_rz(d);
+                if ((double)w != d) w = __uint_as_float(__float_as_uint(w) | 1u);
             }
         }
     }
