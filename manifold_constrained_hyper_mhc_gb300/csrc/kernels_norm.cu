@@ -355,7 +355,7 @@ __device__ __forceinline__ void swiglu_vals(const uint4 (&ga)[2], const uint4 (&
             hi2 = __hmax2(hi2, as_bf162(w[k]));
         }
     }
-    const bool far = on && (gate_far(fminf(__low2float(lo2), __high2float(lo2))) || gate_far(fmaxf(__low2float(hi2), __high2float(hi2))));
+    bool far = on && (gate_far(fminf(__low2float(lo2), __high2float(lo2))) || gate_far(fmaxf(__low2float(hi2), __high2float(hi2))));
     amax = group_max<kBlockLanes>(amax);
     int E = mx_exp(amax, mode);
     if (__any_sync(0xffffffffu, far || (on && near_exponent(amax, mode)))) {
@@ -375,6 +375,7 @@ __device__ __forceinline__ void swiglu_vals(const uint4 (&ga)[2], const uint4 (&
             m = d > m ? d : m;
         }
         E = mx_exp_f64(m, mode);
+        far |= isinf(amax);  // products past fp32's range: infinite here, their codes are not
     }
     const float sc = inv_pow2(E);
     float2 u[kLaneVals / 2];
@@ -384,12 +385,11 @@ __device__ __forceinline__ void swiglu_vals(const uint4 (&ga)[2], const uint4 (&
         u[e / 2] = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(sc, sc));
         key = min(key, min(border_key(u[e / 2].x), border_key(u[e / 2].y)));
     }
-    const bool past = amax > 3.4028234663852886e38f;  // products past fp32's range: infinite here, their codes are not
-    if (on && (key <= kNear << 13 || far || past)) {
+    if (on && (key <= kNear << 13 || far)) {
 #pragma unroll
         for (int e = 0; e < kLaneVals; ++e) {
             float &w = e & 1 ? u[e / 2].y : u[e / 2].x;
-            if (border_key(w) <= kNear << 13 || gate_far(a[e]) || (past && isinf(w))) {
+            if (border_key(w) <= kNear << 13 || gate_far(a[e]) || isinf(w)) {
                 // the fp64 value over 2^E, with whatever fp32 drops of it kept as a sticky last bit, rounds to the same code
                 const double d = silu_mul_f64(a[e], b[e]) * (double)sc;
                 w = __double2float_rz(d);
