@@ -373,8 +373,9 @@ typedef enum mhc_mx_scale_block { MHC_MX_BLOCK_32 = 32, MHC_MX_BLOCK_128 = 128 }
  *   layer_in_fp8, layer_in_scales   MXFP8 of the bf16 y as in mhc_shifted_post_pre_mxfp8 (H % 32 == 0),
  *                                   or both NULL; one of y's two forms is required
  *   scale_mode       mhc_mx_scale_mode;  scale_block  mhc_mx_scale_block
- * Rows of any magnitude: those whose mean s^2 + rmsnorm_eps is outside [2^-40, 2^60] are computed in fp64, which
- * takes longer.  A row of zeros with rmsnorm_eps 0 is NaN (0 / 0).  One launch, no workspace. */
+ * gamma's magnitudes are below 2^80 (s * gamma is a product in fp32).  Rows of any magnitude: those whose
+ * mean s^2 + rmsnorm_eps is outside [2^-40, 2^60] are computed in fp64, which takes longer.  A row of zeros
+ * with rmsnorm_eps 0 is NaN (0 / 0).  One launch, no workspace. */
 MHC_API mhc_status mhc_add_rmsnorm_mxfp8(const mhc_bf16 *x, const mhc_bf16 *residual, const mhc_bf16 *rmsnorm_weight,
                                          int64_t T, int64_t H, float rmsnorm_eps, mhc_bf16 *residual_out,
                                          mhc_bf16 *layer_in_out, uint8_t *layer_in_fp8, uint8_t *layer_in_scales,
@@ -397,7 +398,8 @@ typedef enum mhc_out_type { MHC_OUT_BF16 = 0, MHC_OUT_F32 = 1 } mhc_out_type;
 
 /* Bytes of workspace of the two products below, whatever their sizes (the device status word that
  * mhc_check_status reads; zero-filled before the first use, like the other workspaces).  They keep
- * nothing else in it, so calls in any order and on any streams may share one. */
+ * nothing else in it, so calls in any order and on any streams may share one; a wait that gave up is
+ * noted nowhere else. */
 MHC_API size_t mhc_linear_workspace_size(void);
 
 /* The 8-bit matrix product: out[t][n] = sum_k x[t][k] w[n][k], accumulated in fp32, with
@@ -422,7 +424,9 @@ MHC_API mhc_status mhc_linear_mxfp8(const uint8_t *x_fp8, const uint8_t *x_scale
  *                   [0, R) reads nothing and gives a row of NaN
  *   expert_offsets  [E+1] int32, non-decreasing, on the device (never read by the host).  Rows before the
  *                   first and behind the last group are left as they were; a bound outside [0, M] is
- *                   clamped, a group that ends before it begins is empty
+ *                   clamped, a group that ends before it begins is empty.  With offsets that do decrease
+ *                   nothing outside out is written, but rows of out may be left as they were, and rows
+ *                   of two groups get either one's product
  *   w_fp8           [E,N,K] codes, w_scales [E][ceil(N/128)][ceil(K/128)]
  *   out             [M,N]
  * 1 <= E <= MHC_MAX_EXPERTS, M and R at most MHC_MAX_TOKENS.  One launch. */

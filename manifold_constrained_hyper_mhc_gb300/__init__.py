@@ -556,7 +556,9 @@ def _linear_args(x_fp8, x_scales, w_fp8, w_scales, M, E, out_dtype, out, workspa
 def linear_mxfp8(x_fp8, x_scales, w_fp8, w_scales, *, out_dtype=None, out=None, workspace=None, stream=None):
     """mhc_linear_mxfp8: x [T,K] (MXFP8 codes and scale tiles) times w [N,K] transposed, w with one scale per
     128 x 128 block: w_scales [ceil(N/128), ceil(K/128)], uint8 or float8_e8m0fnu (exponents) or float32.
-    Returns out [T,N], bfloat16 (the default) or float32."""
+    Returns out [T,N], bfloat16 (the default) or float32.  A wait in the kernel that gave up is noted in the
+    workspace alone: pass one (linear_workspace_size() zeroed bytes, or new_workspace's) to ask check_status;
+    without one the call also fills a new one with zeros, a launch more."""
     dev, T, K, N, x, w, out, o = _linear_args(x_fp8, x_scales, w_fp8, w_scales, x_fp8.shape[0], None, out_dtype, out,
                                               workspace, stream)
     _run("mhc_linear_mxfp8", dev, stream, *x, *w, T, K, N, *o)
@@ -566,8 +568,8 @@ def linear_mxfp8(x_fp8, x_scales, w_fp8, w_scales, *, out_dtype=None, out=None, 
 def expert_linear_mxfp8(x_fp8, x_scales, w_fp8, w_scales, expert_offsets, *, rows=None, out_dtype=None, out=None,
                         workspace=None, stream=None):
     """mhc_expert_linear_mxfp8: out[m] = x[rows[m]] w[e]^T for expert_offsets[e] <= m < expert_offsets[e+1]
-    (int32 on the device; rows None: row m).  w [E,N,K], w_scales [E, ceil(N/128), ceil(K/128)] as in
-    linear_mxfp8.  Rows of out outside every group are left as they were."""
+    (int32 on the device; rows None: row m).  w [E,N,K], w_scales [E, ceil(N/128), ceil(K/128)] and workspace as
+    in linear_mxfp8.  Rows of out outside every group are left as they were."""
     M = x_fp8.shape[0] if rows is None else rows.shape[0]
     E = w_fp8.shape[0]
     dev, R, K, N, x, w, out, o = _linear_args(x_fp8, x_scales, w_fp8, w_scales, M, E, out_dtype, out, workspace, stream)

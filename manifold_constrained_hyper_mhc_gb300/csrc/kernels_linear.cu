@@ -21,9 +21,10 @@
 // Tiles.  A k block of a 128 x TN tile takes TN * 2 tensor cycles, and 16 KB + TN * 128 bytes of copies.  From L2 an SM
 // gets about 50 bytes a cycle, so large calls are bound by copies: a pair of CTAs (cta_group::2) shares the token rows
 // of a 256 x 224 tile, 31 KB an SM and k block.  Measured (UE8M0 scales): 8192 x 7168 x 7168 in 237-245 us, 3.4-3.5
-// PFLOP/s, 90-93 % of twice the measured bf16 rate, the clock at 1.65 GHz under the power limit; without the copies it
-// would be 196 us, without the MMAs 211.  Few tokens are bound by the weight's bytes: 6 x 7168 x 7168 in 13.0 us, 48 rows
-// over 64 experts (1.0 GB of touched weights) in 137 us, 7.3 TB/s.  fp32 scales: 2048 x 7168 x 4096 in 69 us, bound by
+// PFLOP/s, 90-93 % of twice the measured bf16 rate, the clock at 1.65 GHz under the power limit (275-280 us in runs of
+// seconds, where it falls further); without the copies it would be 196 us, without the MMAs 211.  Few tokens are bound by the
+// weight's bytes: 6 x 7168 x 7168 in 13.0 us; 48 rows over 64 experts, of which 25 to 35 get one (0.886 GB in the mean of
+// six sets in turn), in 138 us, 6.4 TB/s.  fp32 scales: 2048 x 7168 x 4096 in 69 us, bound by
 // the hand-over of one accumulator per k block (its load, sum and release are a chain of 700-800 cycles in the epilogue
 // warps; the MMAs would take 320-400).
 //

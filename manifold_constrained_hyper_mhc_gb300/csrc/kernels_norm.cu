@@ -411,7 +411,7 @@ __device__ __forceinline__ void swiglu_vals(const uint4 (&ga)[2], const uint4 (&
 }
 
 // A thread takes 16 values at a time (two vectors of gate, two of up: four loads of 16 bytes), the next ones' loads in
-// flight; rows are padded to whole groups of 8 lanes (128 values: a word of scales).  16384 x 2048 (169 MB): 33.6 us with one
+// flight; rows are padded to whole groups of 8 lanes (128 values: a word of scales).  16384 x 2048 (169 MB): 33.4 us with one
 // CTA of 512 threads an SM, that is 5.0 TB/s; 39.8 with 8 values at a time and 768 threads (twice the votes, shuffles and
 // scale stores a value, half the bytes in flight a thread); 34.0 with two CTAs of 256 threads, 39 with 384 threads, 41.6 with
 // 768 (registers spill; 640 threads spill a little and take 33.0).  A call that does not fill one round of the large CTAs

@@ -2,9 +2,10 @@
 
 Tolerances, from the arithmetic:
   * residual_out = bf16(x + residual): one fp32 addition, then the bf16 rounding: 2^-8 (1 + 2^-16) of the value.
-  * layer_in: one bf16 rounding (2^-8) of a value whose relative error before it is at most 2^-23: the square sum of H
-    values (fp32 sums of at most 32 squares, then fp64; 32 2^-24, halved by the root, under 2^-20), two fp32
-    roundings.  Asked: 2^-8 + 2^-19.
+  * layer_in: one bf16 rounding (2^-8) of a value that is off by less than 2^-20 before it.  The square sum, of terms of
+    one sign: 5 roundings within a vector of 8 (product, three fused additions, the two halves), one addition per
+    vector of a thread (at most 16, H = 65536), twice 5 in the sums over lanes: 31 of 2^-24, halved by the root; the
+    root as a pair, and two roundings.  Asked: 2^-8 + 2^-19.
   * codes and scale bytes of the norm: those of the kernel's own bf16 layer input, bit for bit.
   * codes of the SwiGLU: the correctly rounded code of the exact value wherever that is a normal E4M3 number; below
     (|value| < 2^-6 after scaling) fp32's error may move a value across a border: one step, 2^-9, at most; the scale
