@@ -92,8 +92,8 @@ __device__ __forceinline__ void mx_store(const float2 (&u)[4], int E, bool on, u
 // the far ones in fp64, each thread over its own results.  The borders there lie a little outside those that send it there, so
 // a row's result does not depend on the rows beside it.
 // Kept out of the loop over the rows, without loops unrolled and without fp64's division and root (they are calls), this costs
-// the other rows nothing up to 8192 values a row; longer ones, in 32 registers, 6 % (4096 x 16384 83.4 -> 88.9 us).  The same
-// row taken again in the loop, in fp64 or scaled, cost every row up to 25 %.
+// the other rows nothing up to 8192 values a row; longer ones, in 32 registers, up to 7 % (4096 x 8224 52.9 -> 55.7 us, 16384
+// 86.5 -> 92.7; 1024 x 65536 nothing).  The same row taken again in the loop, in fp64 or scaled, cost every row up to 25 %.
 constexpr uint32_t kMeanMinBits = (127u - 40u) << 23, kMeanMaxBits = (127u + 60u) << 23;
 template <int kNT, int kBlockLanes>
 __device__ __forceinline__ void norm_far_rows(const uint16_t *x, const uint16_t *residual, const uint16_t *gamma, int64_t T, int H,
