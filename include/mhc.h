@@ -435,6 +435,83 @@ MHC_API mhc_status mhc_expert_linear_mxfp8(const uint8_t *x_fp8, const uint8_t *
                                            const void *w_scales, int w_scale_type, int64_t K, int64_t N, void *out,
                                            int out_type, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- attention between the 8-bit products --------------------------------------------------------
+ * A decoder layer's attention from the product that makes q, k and v to the product that reads its result: a paged cache
+ * of keys and values held in 4 bits, the attention of a sequence's last tokens over it, and causal attention over whole
+ * prompts.
+ *
+ * A batch is packed: sequence b's tokens are the rows offsets[b] .. offsets[b + 1] - 1 of q, k, v and the outputs, and
+ * they are the LAST tokens of the sequence.  offsets [B + 1], seq_lens [B] (tokens of the sequence in the cache, the
+ * packed ones among them), page_table [B][table_width] and k_offsets [B + 1] are int32 on the device, never read by the
+ * host.  Row i of the n of sequence b is at position seq_lens[b] - n + i and sees the positions 0 .. its own.
+ *   - Rows outside every sequence (before the first, behind the last) are left as they were.  A bound outside [0, T] is
+ *     clamped, a sequence that ends before it begins is empty; with offsets that do decrease nothing outside the outputs
+ *     is touched, but which sequence a row belongs to is not defined.
+ *   - A row that sees nothing (a position below 0) gives zeros and a log-sum of -inf.
+ *   - Positions beyond table_width pages, and pages outside [0, pages), are no place: writes to them are dropped, reads
+ *     from them (positions below 0 too) give NaN, and a row that sees one is NaN.
+ *   - What a row does not see (later tokens, other sequences, the rest of a page) is never part of its result, NaN and
+ *     infinities there included.
+ * q, k and v may be parts of wider rows: a token every q_stride, k_stride, v_stride values (at least heads * head_dim, a
+ * multiple of 8), its heads next to each other.  head_dim is 64 or 128; q_heads is a multiple of kv_heads (q head h reads
+ * kv head h / (q_heads / kv_heads)), at most MHC_MAX_HEADS_PER_KV times it, q_heads * head_dim <= MHC_MAX_HIDDEN.
+ *
+ * The cache: [pages][kv_heads][page_size / 16] groups of 16 tokens, 17 * head_dim bytes each: of K, 16 rows of
+ * head_dim / 2 bytes of E2M1 codes (two a byte, the even value in the low half; row r's 16-byte chunk c stored as chunk
+ * c ^ (r / 2 % 4) for head_dim 128, c ^ (r / 4 % 2) for 64), then 16 rows of head_dim / 32 UE8M0 scale bytes; then of V
+ * the same.  Code * 2^(byte - 127) is the value, and the byte 255 is NaN.  page_size is 16, 32, 64, 128 or 256. */
+#define MHC_MAX_SEQUENCES (1 << 16)
+#define MHC_MAX_HEADS_PER_KV 64
+#define MHC_MAX_CACHE_TOKENS (1 << 30) /* table_width * page_size */
+
+/* Bytes of a cache (0 for sizes that are refused). */
+MHC_API size_t mhc_kv_cache_bytes(int64_t pages, int64_t kv_heads, int64_t page_size, int64_t head_dim);
+
+/* Quantizes k and v [T][kv_heads][head_dim] (bf16, or fp32 with MHC_OUT_F32: a product's result types) into the cache.
+ * Per 32 values: E = floor(log2 amax) - 2 (MHC_MX_SCALE_FLOOR) or the smallest E with amax <= 6 * 2^E
+ * (MHC_MX_SCALE_CEIL), in [-127, 127]; codes are nearest, ties to even, at most 6.  A block with a NaN reads as NaN; an
+ * infinite amax gives E = 126.  Nothing of the cache but the tokens' own bytes is touched.  A place that two rows of the
+ * call share (a page twice in the table) holds, piece by piece, one of them.  One launch. */
+MHC_API mhc_status mhc_kv_write_mxfp4(const void *k, const void *v, int value_type, int64_t k_stride, int64_t v_stride,
+                                      int64_t T, const int32_t *offsets, const int32_t *seq_lens, const int32_t *page_table,
+                                      int64_t B, int64_t table_width, uint8_t *cache, int64_t pages, int64_t kv_heads,
+                                      int64_t page_size, int64_t head_dim, int scale_mode, void *stream);
+
+/* Reads tokens back: k_out and v_out [T][kv_heads][head_dim] bf16 (contiguous) of the last offsets[b + 1] - offsets[b]
+ * tokens of each sequence (all of them: offsets the sums of seq_lens).  One launch. */
+MHC_API mhc_status mhc_kv_read_mxfp4(const uint8_t *cache, int64_t pages, int64_t kv_heads, int64_t page_size, int64_t head_dim,
+                                     const int32_t *offsets, const int32_t *seq_lens, const int32_t *page_table, int64_t B,
+                                     int64_t table_width, int64_t T, mhc_bf16 *k_out, mhc_bf16 *v_out, void *stream);
+
+/* Workspace bytes of the two attentions, whatever their sizes (zero-filled before the first use; every call that
+ * completes leaves it ready).  Calls that share a decode workspace must be ordered; a prompt workspace (the status word
+ * alone, as the products') may be shared by any calls. */
+MHC_API size_t mhc_decode_workspace_size(void);
+MHC_API size_t mhc_prompt_workspace_size(void);
+
+/* Attention of each sequence's last tokens (one, or a verify block's few; their k and v already written) over the cache:
+ *   out[i][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(s_j - max s),  s_j = sm_scale * <q[i][h], k_j>, over the j it sees
+ *   q            [T][q_heads][head_dim] bf16
+ *   attn_out     [T][q_heads][head_dim] bf16, or NULL
+ *   attn_fp8, attn_scales   the result as MXFP8 [T][q_heads * head_dim] (scale tiles as above, one scale per 32 values,
+ *                scale_mode), quantized from fp32 in one rounding, or both NULL; one form of the result is required
+ *   lse          [T][q_heads] fp32 max s + ln sum_j p_j, for a join with other keys, or NULL
+ * Deterministic. */
+MHC_API mhc_status mhc_decode_attention_mxfp4(const mhc_bf16 *q, int64_t q_stride, int64_t T, int64_t q_heads,
+                                              const int32_t *offsets, const int32_t *seq_lens, const int32_t *page_table,
+                                              int64_t B, int64_t table_width, const uint8_t *cache, int64_t pages,
+                                              int64_t kv_heads, int64_t page_size, int64_t head_dim, float sm_scale,
+                                              mhc_bf16 *attn_out, uint8_t *attn_fp8, uint8_t *attn_scales, int scale_mode,
+                                              float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The same over packed bf16 keys and values: the rows q_offsets[b] .. of q are the last of the keys k_offsets[b] .. of k
+ * and v (with as many of both: a whole prompt; with more keys: a later chunk of it after its prefix). */
+MHC_API mhc_status mhc_prompt_attention(const mhc_bf16 *q, int64_t q_stride, const mhc_bf16 *k, int64_t k_stride,
+                                        const mhc_bf16 *v, int64_t v_stride, int64_t Tq, int64_t Tk, int64_t q_heads,
+                                        int64_t kv_heads, int64_t head_dim, const int32_t *q_offsets, const int32_t *k_offsets,
+                                        int64_t B, float sm_scale, mhc_bf16 *attn_out, uint8_t *attn_fp8, uint8_t *attn_scales,
+                                        int scale_mode, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Forces a schedule for every following call of this process (a test hook; the
  * default is MHC_SCHEDULE_AUTO).  Returns MHC_ERR_INVALID_ARG for an unknown value. */
 MHC_API mhc_status mhc_set_schedule(int schedule);

@@ -22,6 +22,7 @@ __all__ = [
     "post_int8", "post_sqrsum", "pre_broadcast", "shifted_post_pre_split", "shifted_post_pre_mxfp8", "mxfp8_scale_bytes", "MX_SCALE_FLOOR", "MX_SCALE_CEIL", "set_main_kernel_events",
     "packed_phi_bytes", "pack_phi",
     "add_rmsnorm_mxfp8", "swiglu_mxfp8", "linear_mxfp8", "expert_linear_mxfp8", "linear_workspace_size",
+    "kv_cache_shape", "kv_write_mxfp4", "kv_read_mxfp4", "decode_attention_mxfp4", "prompt_attention", "decode_workspace_size", "prompt_workspace_size",
 ]
 MX_SCALE_FLOOR, MX_SCALE_CEIL = 0, 1
 
@@ -97,6 +98,21 @@ def lib():
             L.mhc_linear_mxfp8.restype = I
             L.mhc_expert_linear_mxfp8.argtypes = [P, P, I64, P, I64, P, I64, P, P, I, I64, I64, P, I, P, Z, P]
             L.mhc_expert_linear_mxfp8.restype = I
+            L.mhc_kv_cache_bytes.argtypes = [I64, I64, I64, I64]
+            L.mhc_kv_cache_bytes.restype = Z
+            L.mhc_kv_write_mxfp4.argtypes = [P, P, I, I64, I64, I64, P, P, P, I64, I64, P, I64, I64, I64, I64, I, P]
+            L.mhc_kv_write_mxfp4.restype = I
+            L.mhc_kv_read_mxfp4.argtypes = [P, I64, I64, I64, I64, P, P, P, I64, I64, I64, P, P, P]
+            L.mhc_kv_read_mxfp4.restype = I
+            L.mhc_decode_workspace_size.argtypes = []
+            L.mhc_decode_workspace_size.restype = Z
+            L.mhc_prompt_workspace_size.argtypes = []
+            L.mhc_prompt_workspace_size.restype = Z
+            L.mhc_decode_attention_mxfp4.argtypes = [P, I64, I64, I64, P, P, P, I64, I64, P, I64, I64, I64, I64, F, P, P, P, I, P,
+                                                     P, Z, P]
+            L.mhc_decode_attention_mxfp4.restype = I
+            L.mhc_prompt_attention.argtypes = [P, I64, P, I64, P, I64, I64, I64, I64, I64, I64, P, P, I64, F, P, P, P, I, P, P, Z, P]
+            L.mhc_prompt_attention.restype = I
             L.mhc_set_schedule.argtypes = [I]
             L.mhc_set_schedule.restype = I
             L.mhc_auto_schedule.argtypes = [I64, I64]
@@ -577,6 +593,154 @@ def expert_linear_mxfp8(x_fp8, x_scales, w_fp8, w_scales, expert_offsets, *, row
     _run("mhc_expert_linear_mxfp8", dev, stream, *x, R, None if rows is None else _arg(rows, "rows", i32, (M,), dev), M,
          _arg(expert_offsets, "expert_offsets", i32, (E + 1,), dev), E, *w, K, N, *o)
     return out
+
+
+# ---- attention between the 8-bit products
+def kv_cache_shape(pages: int, kv_heads: int, page_size: int, head_dim: int):
+    """The shape of a uint8 cache tensor of that many pages of page_size (16, 32, 64, 128 or 256) tokens."""
+    if page_size not in (16, 32, 64, 128, 256) or head_dim not in (64, 128) or pages < 1 or kv_heads < 1:
+        raise ValueError("page_size must be 16, 32, 64, 128 or 256, head_dim 64 or 128, pages and kv_heads positive")
+    return (pages, kv_heads, page_size // 16, 17 * head_dim)
+
+
+def _strided(t, name, dtypes, dev):
+    """A [T, heads, D] argument that may be part of wider rows: its address and a token's distance in values."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d).removeprefix('torch.') for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens, heads, head_dim]")
+    T, heads, D = t.shape
+    st, sh, sd = t.stride()
+    if t.device != dev or (T > 0 and ((sd != 1 and D > 1) or (sh != D and heads > 1))):
+        raise ValueError(f"{name} must be a tensor on {dev} whose heads lie next to each other")
+    return t.data_ptr(), (st if T > 1 else heads * D)
+
+
+def _cache(cache, page_table, seq_lens, offsets, dev):
+    """The checked cache: its address and sizes, and the addresses of its index tensors."""
+    _, fp8, _, _, i32 = _dtypes()
+    if cache.dim() != 4 or cache.shape[3] not in (17 * 64, 17 * 128):
+        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected that of kv_cache_shape()")
+    pages, heads, groups, width = cache.shape
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [sequences, pages]")
+    B, W = page_table.shape
+    return (_arg(cache, "cache", fp8[:1], cache.shape, dev), (pages, heads, groups * 16, width // 17),
+            (_arg(offsets, "offsets", i32, (B + 1,), dev), _arg(seq_lens, "seq_lens", i32, (B,), dev),
+             _arg(page_table, "page_table", i32, (B, W), dev)), (B, W))
+
+
+def _attn_out(T, heads, D, dev, out, want_bf16, want_mxfp8, want_lse, workspace, size, stream):
+    """The output dict of an attention, the addresses of its forms, and the workspace's."""
+    torch = _torch()
+    bf16, fp8, e8m0, f32, _ = _dtypes()
+    o = dict(out) if out else {}
+    K = heads * D
+    tiles = _scale_shape(T, K)
+    if want_bf16 and "attn_out" not in o:
+        o["attn_out"] = _new((T, heads, D), torch.bfloat16, dev, stream)
+    if want_mxfp8:
+        if "attn_fp8" not in o:
+            o["attn_fp8"] = _new((T, K), torch.uint8, dev, stream)
+        if "attn_scales" not in o:
+            o["attn_scales"] = _new(tiles, torch.uint8, dev, stream)
+    if want_lse and "lse" not in o:
+        o["lse"] = _new((T, heads), torch.float32, dev, stream)
+    if workspace is None:
+        workspace = _new((size(),), torch.uint8, dev, stream, zero=True)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    b, q, s, e = o.get("attn_out"), o.get("attn_fp8"), o.get("attn_scales"), o.get("lse")
+    return (o, None if b is None else _arg(b, "attn_out", bf16, (T, heads, D), dev), None if q is None else _arg(q, "attn_fp8", fp8, (T, K), dev),
+            None if s is None else _arg(s, "attn_scales", e8m0, tiles, dev), None if e is None else _arg(e, "lse", f32, (T, heads), dev),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace)
+
+
+def kv_write_mxfp4(k, v, cache, page_table, seq_lens, offsets, *, scale_mode=MX_SCALE_FLOOR, stream=None):
+    """mhc_kv_write_mxfp4: quantizes k and v [T, kv_heads, head_dim] (bfloat16 or float32, both the same; parts of a
+    wider row are fine) into the cache.  offsets [B+1] are the packed rows of each sequence, the last of its
+    seq_lens [B] tokens; page_table [B, W].  Returns the cache."""
+    dev = _cuda(cache, "cache")
+    bf16, _, _, f32, _ = _dtypes()
+    wide = k.dtype == f32[0]
+    (kp, ks), (vp, vs) = _strided(k, "k", bf16 + f32, dev), _strided(v, "v", f32 if wide else bf16, dev)
+    address, sizes, index, (B, W) = _cache(cache, page_table, seq_lens, offsets, dev)
+    T = k.shape[0]
+    for t, name in ((k, "k"), (v, "v")):
+        if t.shape != (T, sizes[1], sizes[3]):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, sizes[1], sizes[3])}")
+    _run("mhc_kv_write_mxfp4", dev, stream, kp, vp, int(wide), ks, vs, T, *index, B, W, address, *sizes, int(scale_mode))
+    return cache
+
+
+def kv_read_mxfp4(cache, page_table, seq_lens, offsets, *, rows=None, out=None, stream=None):
+    """mhc_kv_read_mxfp4: the last offsets[b+1] - offsets[b] tokens of each sequence as bfloat16.  Returns a dict with k
+    and v [rows, kv_heads, head_dim]; ``out`` may supply them (both), otherwise ``rows`` says how many packed rows
+    there are."""
+    torch = _torch()
+    dev = _cuda(cache, "cache")
+    address, sizes, index, (B, W) = _cache(cache, page_table, seq_lens, offsets, dev)
+    o = dict(out) if out else {}
+    if rows is None:
+        if "k" not in o:
+            raise ValueError("rows or out is required")
+        rows = o["k"].shape[0]
+    shape = (rows, sizes[1], sizes[3])
+    for n in ("k", "v"):
+        if n not in o:
+            o[n] = _new(shape, torch.bfloat16, dev, stream)
+    bf16 = _dtypes()[0]
+    _run("mhc_kv_read_mxfp4", dev, stream, address, *sizes, *index, B, W, rows, _arg(o["k"], "k", bf16, shape, dev),
+         _arg(o["v"], "v", bf16, shape, dev))
+    return o
+
+
+def decode_workspace_size() -> int:
+    return int(lib().mhc_decode_workspace_size())
+
+
+def prompt_workspace_size() -> int:
+    return int(lib().mhc_prompt_workspace_size())
+
+
+def decode_attention_mxfp4(q, cache, page_table, seq_lens, offsets, *, sm_scale=None, want_bf16=True, want_mxfp8=False,
+                           want_lse=False, scale_mode=MX_SCALE_FLOOR, out=None, workspace=None, stream=None):
+    """mhc_decode_attention_mxfp4: attention of q [T, q_heads, head_dim] bf16, each sequence's last tokens, over the
+    cache (the tokens' own k and v already written).  sm_scale: head_dim ** -0.5 unless given.  Returns a dict with
+    attn_out [T, q_heads, head_dim] bf16, attn_fp8 [T, q_heads * head_dim] and attn_scales (the MXFP8 form that
+    linear_mxfp8 reads) and lse [T, q_heads], those that are wanted or given in ``out``.  workspace:
+    decode_workspace_size() zeroed bytes, for calls in order; without one the call fills a new one with zeros."""
+    dev = _cuda(cache, "cache")
+    qp, qs = _strided(q, "q", _dtypes()[0], dev)
+    T, heads, D = q.shape
+    address, sizes, index, (B, W) = _cache(cache, page_table, seq_lens, offsets, dev)
+    if D != sizes[3]:
+        raise ValueError(f"q has shape {tuple(q.shape)}, but the cache's head_dim is {sizes[3]}")
+    o, b, f, s, e, ws, n, keep = _attn_out(T, heads, D, dev, out, want_bf16, want_mxfp8, want_lse, workspace, decode_workspace_size, stream)
+    _run("mhc_decode_attention_mxfp4", dev, stream, qp, qs, T, heads, *index, B, W, address, *sizes,
+         D ** -0.5 if sm_scale is None else float(sm_scale), b, f, s, int(scale_mode), e, ws, n)
+    return o
+
+
+def prompt_attention(q, k, v, q_offsets, k_offsets, *, sm_scale=None, want_bf16=True, want_mxfp8=False, want_lse=False,
+                     scale_mode=MX_SCALE_FLOOR, out=None, workspace=None, stream=None):
+    """mhc_prompt_attention: causal attention of packed prompts.  q [Tq, q_heads, head_dim], k and v [Tk, kv_heads,
+    head_dim] bf16 (parts of a wider row are fine); the rows q_offsets[b] .. are the last of the keys k_offsets[b] ...
+    Options and result as decode_attention_mxfp4's; workspace: prompt_workspace_size() zeroed bytes, which any calls
+    may share (a wait in the kernel that gave up is noted there: check_status)."""
+    dev = _cuda(q, "q")
+    bf16, _, _, _, i32 = _dtypes()
+    (qp, qs), (kp, ks), (vp, vs) = (_strided(t, n, bf16, dev) for t, n in ((q, "q"), (k, "k"), (v, "v")))
+    Tq, heads, D = q.shape
+    Tk, kv_heads = k.shape[:2]
+    for t, name in ((k, "k"), (v, "v")):
+        if t.shape != (Tk, kv_heads, D):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(Tk, kv_heads, D)}")
+    B = q_offsets.shape[0] - 1
+    o, b, f, s, e, ws, n, keep = _attn_out(Tq, heads, D, dev, out, want_bf16, want_mxfp8, want_lse, workspace, prompt_workspace_size, stream)
+    _run("mhc_prompt_attention", dev, stream, qp, qs, kp, ks, vp, vs, Tq, Tk, heads, kv_heads, D, _arg(q_offsets, "q_offsets", i32, (B + 1,), dev),
+         _arg(k_offsets, "k_offsets", i32, (B + 1,), dev), B, D ** -0.5 if sm_scale is None else float(sm_scale), b, f, s, int(scale_mode), e, ws, n)
+    return o
 
 
 def set_schedule(name_or_id):

@@ -863,6 +863,218 @@ mhc_status mhc_expert_linear_mxfp8(const uint8_t *x_fp8, const uint8_t *x_scales
                       workspace, workspace_bytes, stream, true);
 }
 
+namespace {
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+mhc_status check_index(std::initializer_list<std::pair<const int32_t *, const char *>> arrays) {
+    for (auto &a : arrays) {
+        if (a.first == nullptr) return fail(MHC_ERR_INVALID_ARG, "%s is NULL", a.second);
+        if (!aligned4(a.first)) return fail(MHC_ERR_INVALID_ARG, "%s is not 4-byte aligned", a.second);
+    }
+    return MHC_OK;
+}
+
+mhc_status check_rows(const char *name, int64_t rows) {
+    if (rows < 0 || rows > MHC_MAX_TOKENS) return fail(MHC_ERR_INVALID_ARG, "%s=%lld outside [0, %d]", name, (long long)rows, MHC_MAX_TOKENS);
+    return MHC_OK;
+}
+
+mhc_status check_heads(int64_t q_heads, int64_t kv_heads, int64_t D) {
+    if (D != 64 && D != 128) return fail(MHC_ERR_INVALID_ARG, "head_dim must be 64 or 128, not %lld", (long long)D);
+    if (kv_heads < 1 || kv_heads > MHC_MAX_HIDDEN / D)
+        return fail(MHC_ERR_INVALID_ARG, "kv_heads=%lld outside [1, %lld]", (long long)kv_heads, (long long)(MHC_MAX_HIDDEN / D));
+    if (q_heads < kv_heads || q_heads > MHC_MAX_HIDDEN / D || q_heads % kv_heads != 0 || q_heads / kv_heads > MHC_MAX_HEADS_PER_KV)
+        return fail(MHC_ERR_INVALID_ARG, "q_heads=%lld must be a multiple of kv_heads=%lld, at most %d times it and %lld", (long long)q_heads,
+                    (long long)kv_heads, MHC_MAX_HEADS_PER_KV, (long long)(MHC_MAX_HIDDEN / D));
+    return MHC_OK;
+}
+
+constexpr int64_t kMaxStride = int64_t(1) << 30;
+
+mhc_status check_stride(const char *name, int64_t stride, int64_t row) {
+    if (stride < row || stride % 8 != 0 || stride > kMaxStride)
+        return fail(MHC_ERR_INVALID_ARG, "%s=%lld must be a multiple of 8 in [%lld, 2^30]", name, (long long)stride, (long long)row);
+    return MHC_OK;
+}
+
+size_t strided_bytes(int64_t rows, int64_t stride, int64_t row, size_t each) {
+    return rows == 0 ? 0 : ((size_t)(rows - 1) * (size_t)stride + (size_t)row) * each;
+}
+
+size_t cache_bytes(int64_t pages, int64_t heads, int64_t page, int64_t D) {
+    return (size_t)pages * (size_t)heads * (size_t)(page / 16) * 17 * (size_t)D;
+}
+
+mhc_status check_batch(int64_t B) {
+    if (B < 0 || B > MHC_MAX_SEQUENCES) return fail(MHC_ERR_INVALID_ARG, "B=%lld outside [0, %d]", (long long)B, MHC_MAX_SEQUENCES);
+    return MHC_OK;
+}
+
+// The sizes of a cache and of the table that points into it.
+mhc_status check_cache(int64_t B, int64_t width, int64_t pages, int64_t heads, int64_t page, int64_t D) {
+    mhc_status st;
+    if ((st = check_heads(heads, heads, D)) != MHC_OK || (st = check_batch(B)) != MHC_OK) return st;
+    if (page != 16 && page != 32 && page != 64 && page != 128 && page != 256)
+        return fail(MHC_ERR_INVALID_ARG, "page_size must be 16, 32, 64, 128 or 256, not %lld", (long long)page);
+    if (pages < 1 || pages > INT32_MAX) return fail(MHC_ERR_INVALID_ARG, "pages=%lld outside [1, 2^31)", (long long)pages);
+    if (width < 1 || width > MHC_MAX_CACHE_TOKENS / page)
+        return fail(MHC_ERR_INVALID_ARG, "table_width=%lld outside [1, %lld]", (long long)width, (long long)(MHC_MAX_CACHE_TOKENS / page));
+    return MHC_OK;
+}
+
+mhc::CacheArgs cache_args(const uint8_t *cache, int64_t pages, int64_t heads, int64_t page, const int32_t *page_table,
+                          const int32_t *seq_lens, const int32_t *offsets, int64_t B, int64_t width) {
+    int log2 = 4;
+    while ((int64_t(1) << log2) < page) ++log2;
+    return {const_cast<uint8_t *>(cache), pages, (int)heads, (int)page, log2, page_table, seq_lens, offsets, (int)B, (int)width};
+}
+
+// The forms of an attention's result, and their spans against the inputs'.
+mhc_status check_attn_out(int64_t T, int64_t q_heads, int64_t D, const mhc_bf16 *out, const uint8_t *fp8, const uint8_t *scales,
+                          int scale_mode, const float *lse, const void *workspace, size_t workspace_bytes, size_t need,
+                          std::initializer_list<Span> ins) {
+    mhc_status st;
+    const bool mx = fp8 != nullptr || scales != nullptr;
+    if (out == nullptr && !mx) return fail(MHC_ERR_INVALID_ARG, "attn_out and attn_fp8 are NULL");
+    if (out != nullptr && (st = check_ptrs({{out, "attn_out"}})) != MHC_OK) return st;
+    if (mx && (st = check_mx(fp8, scales, "attn_fp8", "attn_scales", q_heads * D, scale_mode, MHC_MX_BLOCK_32)) != MHC_OK) return st;
+    if (lse != nullptr && !aligned4(lse)) return fail(MHC_ERR_INVALID_ARG, "lse is not 4-byte aligned");
+    if (workspace == nullptr) return fail(MHC_ERR_WORKSPACE, "workspace is NULL");
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(MHC_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    if (workspace_bytes < need) return fail(MHC_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    const size_t n = (size_t)T * (size_t)q_heads * (size_t)D;
+    return check_overlaps({{{out, n * 2}, "attn_out"}, {{fp8, n}, "attn_fp8"}, {{scales, mx ? mx_scale_bytes(T, q_heads * D) : 0}, "attn_scales"},
+                           {{lse, (size_t)T * (size_t)q_heads * 4}, "lse"}, {{workspace, need}, "workspace"}}, ins);
+}
+
+}  // namespace
+
+size_t mhc_kv_cache_bytes(int64_t pages, int64_t kv_heads, int64_t page_size, int64_t head_dim) {
+    return check_cache(0, 1, pages, kv_heads, page_size, head_dim) == MHC_OK ? cache_bytes(pages, kv_heads, page_size, head_dim) : 0;
+}
+
+mhc_status mhc_kv_write_mxfp4(const void *k, const void *v, int value_type, int64_t k_stride, int64_t v_stride, int64_t T,
+                              const int32_t *offsets, const int32_t *seq_lens, const int32_t *page_table, int64_t B,
+                              int64_t table_width, uint8_t *cache, int64_t pages, int64_t kv_heads, int64_t page_size,
+                              int64_t head_dim, int scale_mode, void *stream) {
+    mhc_status st;
+    g_launches = 0;
+    if ((st = check_rows("T", T)) != MHC_OK || (st = check_cache(B, table_width, pages, kv_heads, page_size, head_dim)) != MHC_OK) return st;
+    if (value_type != MHC_OUT_BF16 && value_type != MHC_OUT_F32) return fail(MHC_ERR_INVALID_ARG, "unknown value type %d", value_type);
+    if (scale_mode != MHC_MX_SCALE_FLOOR && scale_mode != MHC_MX_SCALE_CEIL) return fail(MHC_ERR_INVALID_ARG, "unknown scale mode %d", scale_mode);
+    const int64_t row = kv_heads * head_dim;
+    if ((st = check_stride("k_stride", k_stride, row)) != MHC_OK || (st = check_stride("v_stride", v_stride, row)) != MHC_OK) return st;
+    if (T == 0 || B == 0) return MHC_OK;
+    if ((st = check_ptrs({{k, "k"}, {v, "v"}, {cache, "cache"}})) != MHC_OK) return st;
+    if ((st = check_index({{offsets, "offsets"}, {seq_lens, "seq_lens"}, {page_table, "page_table"}})) != MHC_OK) return st;
+    const size_t each = value_type == MHC_OUT_F32 ? 4 : 2;
+    if ((st = check_overlaps({{{cache, cache_bytes(pages, kv_heads, page_size, head_dim)}, "cache"}},
+                             {{k, strided_bytes(T, k_stride, row, each)}, {v, strided_bytes(T, v_stride, row, each)},
+                              {offsets, (size_t)(B + 1) * 4}, {seq_lens, (size_t)B * 4}, {page_table, (size_t)B * table_width * 4}})) != MHC_OK)
+        return st;
+    Device dev;
+    if ((st = current_device(dev)) != MHC_OK) return st;
+    const cudaError_t e = mhc::launch_kv_write(cache_args(cache, pages, kv_heads, page_size, page_table, seq_lens, offsets, B, table_width),
+                                               {k, v, k_stride, v_stride, value_type == MHC_OUT_F32, scale_mode}, T, (int)head_dim, dev.sms,
+                                               static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
+    g_launches = 1;
+    return MHC_OK;
+}
+
+mhc_status mhc_kv_read_mxfp4(const uint8_t *cache, int64_t pages, int64_t kv_heads, int64_t page_size, int64_t head_dim,
+                             const int32_t *offsets, const int32_t *seq_lens, const int32_t *page_table, int64_t B, int64_t table_width,
+                             int64_t T, mhc_bf16 *k_out, mhc_bf16 *v_out, void *stream) {
+    mhc_status st;
+    g_launches = 0;
+    if ((st = check_rows("T", T)) != MHC_OK || (st = check_cache(B, table_width, pages, kv_heads, page_size, head_dim)) != MHC_OK) return st;
+    if (T == 0 || B == 0) return MHC_OK;
+    if ((st = check_ptrs({{cache, "cache"}, {k_out, "k_out"}, {v_out, "v_out"}})) != MHC_OK) return st;
+    if ((st = check_index({{offsets, "offsets"}, {seq_lens, "seq_lens"}, {page_table, "page_table"}})) != MHC_OK) return st;
+    const size_t n = (size_t)T * (size_t)(kv_heads * head_dim) * 2;
+    if ((st = check_overlaps({{{k_out, n}, "k_out"}, {{v_out, n}, "v_out"}},
+                             {{cache, cache_bytes(pages, kv_heads, page_size, head_dim)}, {offsets, (size_t)(B + 1) * 4}, {seq_lens, (size_t)B * 4},
+                              {page_table, (size_t)B * table_width * 4}})) != MHC_OK)
+        return st;
+    Device dev;
+    if ((st = current_device(dev)) != MHC_OK) return st;
+    const cudaError_t e = mhc::launch_kv_read(cache_args(cache, pages, kv_heads, page_size, page_table, seq_lens, offsets, B, table_width), k_out,
+                                              v_out, T, (int)head_dim, dev.sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
+    g_launches = 1;
+    return MHC_OK;
+}
+
+size_t mhc_decode_workspace_size(void) { return mhc::decode_workspace_bytes(); }
+size_t mhc_prompt_workspace_size(void) { return mhc::kControlBytes; }
+
+mhc_status mhc_decode_attention_mxfp4(const mhc_bf16 *q, int64_t q_stride, int64_t T, int64_t q_heads, const int32_t *offsets,
+                                      const int32_t *seq_lens, const int32_t *page_table, int64_t B, int64_t table_width,
+                                      const uint8_t *cache, int64_t pages, int64_t kv_heads, int64_t page_size, int64_t head_dim,
+                                      float sm_scale, mhc_bf16 *attn_out, uint8_t *attn_fp8, uint8_t *attn_scales, int scale_mode,
+                                      float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    mhc_status st;
+    g_launches = 0;
+    if ((st = check_rows("T", T)) != MHC_OK || (st = check_cache(B, table_width, pages, kv_heads, page_size, head_dim)) != MHC_OK ||
+        (st = check_heads(q_heads, kv_heads, head_dim)) != MHC_OK)
+        return st;
+    const int64_t row = q_heads * head_dim;
+    if ((st = check_stride("q_stride", q_stride, row)) != MHC_OK) return st;
+    if (!std::isfinite(sm_scale)) return fail(MHC_ERR_INVALID_ARG, "sm_scale must be finite");
+    if (T == 0 || B == 0) return MHC_OK;
+    if ((st = check_ptrs({{q, "q"}, {cache, "cache"}})) != MHC_OK) return st;
+    if ((st = check_index({{offsets, "offsets"}, {seq_lens, "seq_lens"}, {page_table, "page_table"}})) != MHC_OK) return st;
+    const size_t need = mhc::decode_workspace_bytes();
+    if ((st = check_attn_out(T, q_heads, head_dim, attn_out, attn_fp8, attn_scales, scale_mode, lse, workspace, workspace_bytes, need,
+                             {{q, strided_bytes(T, q_stride, row, 2)}, {cache, cache_bytes(pages, kv_heads, page_size, head_dim)},
+                              {offsets, (size_t)(B + 1) * 4}, {seq_lens, (size_t)B * 4}, {page_table, (size_t)B * table_width * 4}})) != MHC_OK)
+        return st;
+    Device dev;
+    if ((st = current_device(dev)) != MHC_OK) return st;
+    mhc::DecodeArgs a{cache_args(cache, pages, kv_heads, page_size, page_table, seq_lens, offsets, B, table_width), q, q_stride, T, (int)q_heads,
+                      (int)head_dim, sm_scale, {attn_out, {attn_fp8, attn_scales, scale_mode}, lse, (int)q_heads},
+                      static_cast<unsigned int *>(workspace)};
+    const cudaError_t e = mhc::launch_decode(a, dev.sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
+    g_launches = 1;
+    return MHC_OK;
+}
+
+mhc_status mhc_prompt_attention(const mhc_bf16 *q, int64_t q_stride, const mhc_bf16 *k, int64_t k_stride, const mhc_bf16 *v,
+                                int64_t v_stride, int64_t Tq, int64_t Tk, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                const int32_t *q_offsets, const int32_t *k_offsets, int64_t B, float sm_scale, mhc_bf16 *attn_out,
+                                uint8_t *attn_fp8, uint8_t *attn_scales, int scale_mode, float *lse, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    mhc_status st;
+    g_launches = 0;
+    if ((st = check_rows("Tq", Tq)) != MHC_OK || (st = check_rows("Tk", Tk)) != MHC_OK || (st = check_batch(B)) != MHC_OK ||
+        (st = check_heads(kv_heads, kv_heads, head_dim)) != MHC_OK || (st = check_heads(q_heads, kv_heads, head_dim)) != MHC_OK)
+        return st;
+    const int64_t row = q_heads * head_dim, kv_row = kv_heads * head_dim;
+    if ((st = check_stride("q_stride", q_stride, row)) != MHC_OK || (st = check_stride("k_stride", k_stride, kv_row)) != MHC_OK ||
+        (st = check_stride("v_stride", v_stride, kv_row)) != MHC_OK)
+        return st;
+    if (!std::isfinite(sm_scale)) return fail(MHC_ERR_INVALID_ARG, "sm_scale must be finite");
+    if (Tq == 0 || B == 0) return MHC_OK;
+    if ((st = check_ptrs({{q, "q"}})) != MHC_OK) return st;
+    if (Tk > 0 && (st = check_ptrs({{k, "k"}, {v, "v"}})) != MHC_OK) return st;
+    if ((st = check_index({{q_offsets, "q_offsets"}, {k_offsets, "k_offsets"}})) != MHC_OK) return st;
+    if ((st = check_attn_out(Tq, q_heads, head_dim, attn_out, attn_fp8, attn_scales, scale_mode, lse, workspace, workspace_bytes,
+                             mhc::kControlBytes,
+                             {{q, strided_bytes(Tq, q_stride, row, 2)}, {k, strided_bytes(Tk, k_stride, kv_row, 2)},
+                              {v, strided_bytes(Tk, v_stride, kv_row, 2)}, {q_offsets, (size_t)(B + 1) * 4}, {k_offsets, (size_t)(B + 1) * 4}})) != MHC_OK)
+        return st;
+    Device dev;
+    if ((st = current_device(dev)) != MHC_OK) return st;
+    mhc::PromptArgs a{q, k, v, q_stride, k_stride, v_stride, Tq, Tk, (int)q_heads, (int)kv_heads, (int)head_dim, (int)B, q_offsets, k_offsets,
+                      sm_scale, {attn_out, {attn_fp8, attn_scales, scale_mode}, lse, (int)q_heads}, static_cast<unsigned int *>(workspace)};
+    const cudaError_t e = mhc::launch_prompt(a, dev.sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
+    g_launches = 1;
+    return MHC_OK;
+}
+
 mhc_status mhc_set_schedule(int schedule) {
     if (schedule != MHC_SCHEDULE_AUTO && schedule != MHC_SCHEDULE_SPLIT && schedule != MHC_SCHEDULE_WS &&
         schedule != MHC_SCHEDULE_SMALL && schedule != MHC_SCHEDULE_BCAST && schedule != MHC_SCHEDULE_TILE)

@@ -171,6 +171,58 @@ struct LinearArgs {
 };
 cudaError_t launch_linear(const LinearArgs &a, int num_sms, cudaStream_t stream);
 
+// The 4-bit cache (kernels_cache.cu): its bytes, and where the tokens of a packed batch lie in it.
+struct CacheArgs {
+    uint8_t *data;               // [pages][heads][page / 16][17 * D]
+    int64_t pages;
+    int heads, page, page_log2;  // kv heads; tokens of a page, and their log2
+    const int32_t *page_table;   // [B][width]
+    const int32_t *seq_lens;     // [B] tokens in the cache, the packed rows the last of them
+    const int32_t *offsets;      // [B + 1] first packed row of each sequence
+    int B, width;
+};
+struct CacheWriteArgs {
+    const void *k, *v;           // [T][heads][D] bf16, or fp32 (f32); a token every k_stride, v_stride values
+    int64_t k_stride, v_stride;
+    bool f32;
+    int mode;                    // mhc_mx_scale_mode
+};
+cudaError_t launch_kv_write(const CacheArgs &c, const CacheWriteArgs &a, int64_t T, int D, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_read(const CacheArgs &c, uint16_t *k, uint16_t *v, int64_t T, int D, int num_sms, cudaStream_t stream);
+
+// Where an attention's result goes: any of out [T][heads][D] bf16, mx [T][heads * D] and lse [T][heads] fp32.
+struct AttnOut {
+    uint16_t *out;
+    MxOut mx;
+    float *lse;
+    int heads;
+};
+
+// Attention over the cache (kernels_decode.cu).
+struct DecodeArgs {
+    CacheArgs c;
+    const uint16_t *q;           // [T][q_heads][D], a token every q_stride values
+    int64_t q_stride, T;
+    int q_heads, D;
+    float sm_scale;
+    AttnOut o;
+    unsigned int *ctrl;          // the workspace
+};
+size_t decode_workspace_bytes();
+cudaError_t launch_decode(const DecodeArgs &a, int num_sms, cudaStream_t stream);
+
+// Attention over packed prompts (kernels_prompt.cu).
+struct PromptArgs {
+    const uint16_t *q, *k, *v;   // [Tq][q_heads][D], [Tk][kv_heads][D], a token every q_stride, k_stride, v_stride values
+    int64_t q_stride, k_stride, v_stride, Tq, Tk;
+    int q_heads, kv_heads, D, B;
+    const int32_t *q_offsets, *k_offsets;  // [B + 1]
+    float sm_scale;
+    AttnOut o;
+    unsigned int *status;        // bit 0 is set when a bounded wait gives up
+};
+cudaError_t launch_prompt(const PromptArgs &a, int num_sms, cudaStream_t stream);
+
 cudaError_t launch_post(const uint16_t *R, const uint16_t *Y, const float *prev_post,
                         const float *prev_comb, int64_t T, int H, uint16_t *R_out, int num_sms,
                         cudaStream_t stream);
