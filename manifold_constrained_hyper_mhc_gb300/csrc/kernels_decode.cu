@@ -1,64 +1,688 @@
 // Attention of a sequence's last tokens (one, or the few of a speculative-verify block) over its 4-bit cache.
+//
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(s_j - m),  s_j = sm_scale log2(e) <q, k_j>,  m the largest s so far
+//
+// The cache is read once (17/32 byte a value): that is the floor, and what must not be in its way are the conversions,
+// about three instructions for every four codes.  One CTA an SM; the keys of all (sequence, kv head) pairs are one long
+// line of slices of 32 tokens, cut into equal shares whatever the lengths (the host knows none of them).  A CTA's warps
+// take the slices of its share in turn, each with its own running maximum, sum and accumulators, copied ahead into its
+// own ring in shared memory, and are joined at the end of each pair; a pair that is cut leaves its parts in the
+// workspace, and the CTA that arrives last joins them, in order.
+//
+// The rows of a pair are the tokens times the heads of the group.  For NR = 8 or 16 rows a warp computes, on the legacy
+// tensor path (operands from registers: the codes are converted there and never written back),
+//   S [rows x 32 tokens] = Q K^T   m16n8k16, fp16: E2M1 codes are exact there, and a row of q scaled by a power of two
+//                                  has all its 8 bits; each 32 values' sum is multiplied by its scale in fp32
+//   O^T [D x rows] += V^T P^T      with V's codes and P' = p * 2^(scale - largest scale so far) in fp16 (2^-11 of p; the
+//                                  values that get lost are below 2^-35 of the largest), so V's scales cost nothing on V
+// The k order of a product is free: a lane takes 8 neighbouring codes of K (ldmatrix), and 4 of V for two tokens
+// (ldmatrix.trans), as they lie; q and the output follow that order.
+//
+// An ALU instruction takes 1/2 clock a warp and SM here, m16n8k16 2 clocks, so 32 tokens of D = 128 cost about 190 clocks
+// of the ALU and 100 of the tensor pipe for 8 rows, against 190 of memory.
 #include "attention.cuh"
+#include "sm100_ptx.cuh"
 
 namespace mhc {
 namespace {
 
-constexpr int kThreads = 128;
+using namespace ptx;
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) decode_rows_kernel(DecodeArgs a) {
-    using L = CacheLayout<D>;
-    constexpr int N = D / 32;
+constexpr int kMaxCtas = 192;     // partial results and counters in the workspace
+constexpr int kMaxRows = 64;      // rows of a CTA
+constexpr int kSlice = 32;        // tokens
+constexpr float kLazy = 4.f;      // a maximum is raised when a score is above it by more than this (log2): few rescales
+constexpr int kGain = 11;         // P' is p * 2^kGain, at most 2^(kGain + kLazy) (fp16 ends at 2^16)
+
+struct Partial {                  // of a CTA's share of a pair
+    float o[kMaxRows][128];
+    float m[kMaxRows], l[kMaxRows];
+};
+constexpr size_t kCounterBytes = 1024;  // kMaxCtas counters
+static_assert(kMaxCtas * 4 <= kCounterBytes, "");
+
+template <int D, int NR_, int WR_, int NW_, int ST_>
+struct Cfg {
+    static constexpr int NR = NR_, WR = WR_, NW = NW_, ST = ST_;   // rows a warp, warps over rows, warps, ring stages
+    static constexpr int WT = NW / WR, ROWS = NR * WR, NT = NW * 32, NB = D / 32, NTILE = NR / 8;
+    static constexpr int kSliceBytes = 2 * CacheLayout<D>::kGroupBytes;
+    static constexpr int kRing = WT * ST * kSliceBytes;
+    static constexpr int kScale = NW * 2 * kSlice * NB * 4;        // K's and V's scales of a slice in fp32, a warp's own
+    static constexpr int kJoin = NW * NR * 32 * 4;                 // 32 values of every warp's rows; weights of parts
+    static_assert(kJoin >= NW * kMaxCtas * 4, "");
+    static constexpr int kQ = NR == 16 ? WR * (D / 16) * 32 * 16 : 0;
+    static constexpr int kStats = 3 * NW * NR * 4 + WT * ST * 4 + 256;
+    static constexpr int kSmem = kRing + kScale + kJoin + kQ + kStats;
+    static_assert(kSmem <= 232448, "");
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ float quad_max(float v) {
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// What is to be done: a sequence's geometry, and a CTA's place on the line.
+struct Seq {
+    int64_t begin;      // first packed row
+    int n, len;         // packed rows; tokens in the cache (at most one past what the table holds for each packed row)
+    int tiles, slices;  // row tiles of a kv head; slices of a pair
+};
+
+__device__ __forceinline__ Seq sequence(const DecodeArgs &a, int rows, int b) {
+    Seq s;
+    const int64_t lo = clamp_row(__ldg(a.c.offsets + b), a.T), hi = clamp_row(__ldg(a.c.offsets + b + 1), a.T);
+    s.begin = lo;
+    s.n = hi > lo ? (int)(hi - lo) : 0;
+    // lengths beyond the table: positions from its end on are NaN, so no more of them are needed than rows
+    const int64_t room = (int64_t)a.c.width << a.c.page_log2;
+    s.len = (int)max((int64_t)0, min((int64_t)__ldg(a.c.seq_lens + b), room + s.n));
+    s.tiles = (int)(((int64_t)s.n * (a.q_heads / a.c.heads) + rows - 1) / rows);
+    s.slices = max(1, (s.len + kSlice - 1) / kSlice);
+    return s;
+}
+__device__ __forceinline__ int64_t cost(const DecodeArgs &a, const Seq &s) { return (int64_t)a.c.heads * s.tiles * s.slices; }
+
+// A block's exclusive sum; `total` the whole.  Two syncs; `scratch` 33 words.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t &total, int64_t *scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+        const int64_t y = scratch[w];
+        if (w < warp) before += y;
+        all += y;
+    }
+    __syncthreads();
+    total = all;
+    return before + x - v;
+}
+
+// 32 values of one head's row, one a lane (block `blk` of the head).
+__device__ __forceinline__ void write_block(const AttnOut &o, int D, int64_t t, int head, int blk, float v) {
     const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t t = item / a.q_heads;
-    if (t >= a.T) return;
-    const int hq = (int)(item % a.q_heads), head = hq / (a.q_heads / a.c.heads);
-    const SeqOfRow s = find_sequence(a.c.offsets, a.c.B, t, a.T);
-    if (s.b < 0) return;
-    // a length beyond the table's: positions from the table's end on are NaN, and one of them is enough
-    const int64_t n = s.end - s.begin, room = (int64_t)a.c.width << a.c.page_log2;
-    const int64_t len = min((int64_t)__ldg(a.c.seq_lens + s.b), room + n);
-    const int64_t sees = max((int64_t)0, len - n + (t - s.begin) + 1);
-    float q[N], o[N];
-    const uint16_t *qp = a.q + t * a.q_stride + hq * D + lane * N;
+    const int64_t at = (t * o.heads + head) * (int64_t)D + blk * 32 + lane;
+    if (o.out != nullptr) o.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    if (o.mx.q != nullptr) {
+        float amax = fabsf(v);
 #pragma unroll
-    for (int i = 0; i < N; ++i) q[i] = __uint_as_float((uint32_t)qp[i] << 16);
-    auto fetch = [&](int64_t j, int part_v, float (&x)[N]) {
-        const int page = cache_page(a.c, s.b, j);
-        const int at = (int)(j & (a.c.page - 1)), row = at & 15, blk = lane * N / 32;
-        if (page < 0) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = __uint_as_float(0x7fffffffu);
-            return;
+        for (int m = 1; m < 32; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+        const int E = mx_exp(amax, o.mx.mode);
+        o.mx.q[at] = (uint8_t)__nv_cvt_float_to_fp8(v * __uint_as_float((uint32_t)(127 - E) << 23), __NV_SATFINITE, __NV_E4M3);
+        if (lane == 0) o.mx.scale[mx_scale_offset(t, head * (D / 32) + blk, o.heads * D)] = (uint8_t)(E + 127);
+    }
+}
+// The row's result from its sums: what sees nothing gives zeros and -inf.
+__device__ __forceinline__ void finish_block(const DecodeArgs &a, const Seq &q, int head, int r, int blk, float o, float m, float l) {
+    const int G = a.q_heads / a.c.heads, i = r / G;
+    const bool sees = q.len - q.n + i >= 0;
+    const int64_t t = q.begin + i;
+    const int hq = head * G + r % G;
+    write_block(a.o, a.D, t, hq, blk, sees ? o / l : 0.f);
+    if (blk == 0 && a.o.lse != nullptr && (threadIdx.x & 31) == 0) a.o.lse[t * a.o.heads + hq] = sees ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+template <int D, class C>
+struct Warp {                              // a warp's running state
+    float o[C::NB][2][C::NTILE][4];        // O^T: per 32 values two tiles of 16, per 8 rows
+    float m[C::NTILE], l[C::NTILE];        // row lane / 4 (+ 8): reference maximum, sum of the lane's own tokens
+    uint32_t top;                          // V's largest scale byte so far: o is in units of 2^(top - 127 - kGain)
+};
+
+// A slice of 32 tokens from shared memory.  tok0: its first token; vis: tokens that the lane's rows see.
+template <int D, class C, bool kMask>
+__device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32_t (&q)[C::NB][2][C::NTILE * 2], const uint4 *sq,
+                                      float *sk, float *sv, int tok0, int len, uint32_t bad, const float (&f)[C::NTILE], const int (&vis)[C::NTILE]) {
+    using L = CacheLayout<D>;
+    constexpr int NB = C::NB, NTL = C::NTILE;
+    const int lane = threadIdx.x & 31, t4 = lane & 3;
+    // ---- scales, a token a lane
+    uint32_t vtop;
+    {
+        const uint32_t at = base + (lane >> 4) * L::kGroupBytes + L::kScales + (lane & 15) * NB;
+        uint32_t kw, vw;
+        if constexpr (NB == 4) {
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(at));
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw) : "r"(at + L::kPart));
+        } else {
+            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(kw) : "r"(at));
+            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(vw) : "r"(at + L::kPart));
         }
-        const uint8_t *part = a.c.data + cache_group<D>(a.c, page, head, at >> 4) + part_v * L::kPart;
-        const uint8_t *codes = part + row * L::kRow + (blk ^ L::swizzle(row)) * 16 + (lane * N % 32) / 2;
-        const float m = ue8m0(part[L::kScales + row * L::kBlocks + blk]);
+        if ((bad >> (lane >> 4)) & 1u) kw = vw = 0xffffffffu;   // no such page: NaN
+        const bool there = tok0 + lane < len;
+        uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const float2 f = half2_to_float2(e2m1x2<0>(codes[i / 2]));
-            x[i] = f.x * m;
-            x[i + 1] = f.y * m;
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t e = (vw >> (8 * b)) & 255u;
+            top = max(top, there && e != 255u ? e : 0u);
+        }
+        vtop = max(w.top, __reduce_max_sync(0xffffffffu, top));
+        float ks[NB], vs[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t ke = (kw >> (8 * b)) & 255u, ve = (vw >> (8 * b)) & 255u;
+            ks[b] = there ? ue8m0(ke) : 0.f;
+            const int d = (int)ve - (int)vtop + 127 + kGain;
+            vs[b] = !there || d < 0 ? 0.f : ve == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)d << 23);
+        }
+        if constexpr (NB == 4) {
+            *reinterpret_cast<float4 *>(sk + lane * 4) = make_float4(ks[0], ks[1], ks[2], ks[3]);
+            *reinterpret_cast<float4 *>(sv + lane * 4) = make_float4(vs[0], vs[1], vs[2], vs[3]);
+        } else {
+            *reinterpret_cast<float2 *>(sk + lane * 2) = make_float2(ks[0], ks[1]);
+            *reinterpret_cast<float2 *>(sv + lane * 2) = make_float2(vs[0], vs[1]);
+        }
+        __syncwarp();
+    }
+    // the lane's tokens 8n + 2 t4 and the next: [token][block]
+    auto scales = [&](const float *s, int n, float (&x)[2][NB]) {
+        const float4 *p = reinterpret_cast<const float4 *>(s + (8 * n + 2 * t4) * NB);
+        if constexpr (NB == 4) {
+            const float4 u = p[0], v = p[1];
+            x[0][0] = u.x; x[0][1] = u.y; x[0][2] = u.z; x[0][3] = u.w;
+            x[1][0] = v.x; x[1][1] = v.y; x[1][2] = v.z; x[1][3] = v.w;
+        } else {
+            const float4 u = p[0];
+            x[0][0] = u.x; x[0][1] = u.y; x[1][0] = u.z; x[1][1] = u.w;
         }
     };
-    const float lse = attend_row<D>(
-        q, a.sm_scale * kLog2e, sees, [&](int64_t j, float (&x)[N]) { fetch(j, 0, x); }, [&](int64_t j, float (&x)[N]) { fetch(j, 1, x); }, o);
-    write_head_row<D>(a.o, t, hq, o, lse);
+    // the codes of 8 tokens (n) and all blocks, or of 16 tokens (2 n') and both blocks for D = 64
+    auto codes_at = [&](int part, int i) {
+        const int mi = lane >> 3;
+        const int n = NB == 4 ? i : 2 * i + (mi >> 1), blk = NB == 4 ? mi : mi & 1;
+        const int row = (n & 1) * 8 + (lane & 7);
+        return base + (n >> 1) * L::kGroupBytes + part * L::kPart + row * L::kRow + ((blk ^ L::swizzle(row)) * 16);
+    };
+    // ---- scores
+    float s[4][2 * NTL];
+#pragma unroll
+    for (int i = 0; i < (NB == 4 ? 4 : 2); ++i) {
+        uint32_t kc[4];
+        ldsm4(kc, codes_at(0, i));
+#pragma unroll
+        for (int nn = 0; nn < (NB == 4 ? 1 : 2); ++nn) {
+            const int n = NB == 4 ? i : 2 * i + nn;
+            float sc[2][NB];
+            scales(sk, n, sc);
+#pragma unroll
+            for (int e = 0; e < 2 * NTL; ++e) s[n][e] = 0.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const uint32_t c = kc[NB == 4 ? b : nn * 2 + b];
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (NTL == 1) {
+                    const uint32_t a0[4] = {q[b][0][0], 0u, q[b][0][1], 0u}, a1[4] = {q[b][1][0], 0u, q[b][1][1], 0u};
+                    mma(acc, a0, e2m1x2<0>(c), e2m1x2<1>(c));
+                    mma(acc, a1, e2m1x2<2>(c), e2m1x2<3>(c));
+                } else {
+                    const uint4 u0 = sq[(b * 2) * 32 + lane], u1 = sq[(b * 2 + 1) * 32 + lane];
+                    const uint32_t a0[4] = {u0.x, u0.y, u0.z, u0.w}, a1[4] = {u1.x, u1.y, u1.z, u1.w};
+                    mma(acc, a0, e2m1x2<0>(c), e2m1x2<1>(c));
+                    mma(acc, a1, e2m1x2<2>(c), e2m1x2<3>(c));
+                }
+#pragma unroll
+                for (int e = 0; e < 2 * NTL; ++e) s[n][e] = fmaf(acc[e], sc[e & 1][b], s[n][e]);
+            }
+        }
+    }
+    // ---- the running maximum
+    float hi[NTL];
+#pragma unroll
+    for (int r = 0; r < NTL; ++r) hi[r] = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 2 * NTL; ++e) {
+            s[n][e] *= f[e >> 1];
+            if (kMask && tok0 + 8 * n + 2 * t4 + (e & 1) >= vis[e >> 1]) s[n][e] = -INFINITY;
+            hi[e >> 1] = fmaxf(hi[e >> 1], s[n][e]);
+        }
+    bool raise = vtop != w.top;
+#pragma unroll
+    for (int r = 0; r < NTL; ++r) raise |= hi[r] > w.m[r] + kLazy;
+    if (__any_sync(0xffffffffu, raise)) {
+        const float unit = ex2((float)((int)w.top - (int)vtop));
+        w.top = vtop;
+#pragma unroll
+        for (int r = 0; r < NTL; ++r) {
+            const float top = fmaxf(w.m[r], quad_max(hi[r]));
+            const float al = w.m[r] == -INFINITY ? 0.f : ex2(w.m[r] - top);
+            w.m[r] = top;
+            w.l[r] *= al;
+            // the accumulators' rows are 8r + 2 t4 and the next: held, as rows, by lanes 8 t4 and 8 t4 + 4
+            const float x = __shfl_sync(0xffffffffu, al, 8 * t4) * unit, y = __shfl_sync(0xffffffffu, al, 8 * t4 + 4) * unit;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    w.o[b][h][r][0] *= x;
+                    w.o[b][h][r][1] *= y;
+                    w.o[b][h][r][2] *= x;
+                    w.o[b][h][r][3] *= y;
+                }
+        }
+    }
+    // ---- exponentials and their sums
+#pragma unroll
+    for (int r = 0; r < NTL; ++r) {
+        const float m = w.m[r] == -INFINITY ? 0.f : w.m[r];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            s[n][2 * r] = ex2(s[n][2 * r] - m);
+            s[n][2 * r + 1] = ex2(s[n][2 * r + 1] - m);
+            w.l[r] += s[n][2 * r] + s[n][2 * r + 1];
+        }
+    }
+    // ---- O^T += V^T P'^T, 16 tokens at a time
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t v0[NB], v1[NB];   // tokens 16h .. +7, and the next 8
+        {
+            uint32_t r[4];
+            ldsm4t(r, codes_at(1, NB == 4 ? 2 * h : h));
+            if constexpr (NB == 4) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) v0[b] = r[b];
+                ldsm4t(r, codes_at(1, 2 * h + 1));
+#pragma unroll
+                for (int b = 0; b < 4; ++b) v1[b] = r[b];
+            } else {
+                v0[0] = r[0]; v0[1] = r[1]; v1[0] = r[2]; v1[1] = r[3];
+            }
+        }
+        float s0[2][NB], s1[2][NB];
+        scales(sv, 2 * h, s0);
+        scales(sv, 2 * h + 1, s1);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            uint32_t pb[NTL][2];
+#pragma unroll
+            for (int r = 0; r < NTL; ++r) {
+                float x[4] = {s[2 * h][2 * r] * s0[0][b], s[2 * h][2 * r + 1] * s0[1][b], s[2 * h + 1][2 * r] * s1[0][b], s[2 * h + 1][2 * r + 1] * s1[1][b]};
+                if constexpr (kMask) {  // (0 times a NaN scale is none of what a row does not see)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (tok0 + 16 * h + 8 * (e >> 1) + 2 * t4 + (e & 1) >= vis[r]) x[e] = 0.f;
+                }
+                pb[r][0] = pack_half(x[0], x[1]);
+                pb[r][1] = pack_half(x[2], x[3]);
+            }
+            const uint32_t e0 = e2m1x2<0>(v0[b]), e1 = e2m1x2<2>(v0[b]), e2 = e2m1x2<0>(v1[b]), e3 = e2m1x2<2>(v1[b]);
+            const uint32_t g0 = e2m1x2<1>(v0[b]), g1 = e2m1x2<3>(v0[b]), g2 = e2m1x2<1>(v1[b]), g3 = e2m1x2<3>(v1[b]);
+            const uint32_t a0[4] = {__byte_perm(e0, e1, 0x5410), __byte_perm(e0, e1, 0x7632), __byte_perm(e2, e3, 0x5410), __byte_perm(e2, e3, 0x7632)};
+            const uint32_t a1[4] = {__byte_perm(g0, g1, 0x5410), __byte_perm(g0, g1, 0x7632), __byte_perm(g2, g3, 0x5410), __byte_perm(g2, g3, 0x7632)};
+#pragma unroll
+            for (int r = 0; r < NTL; ++r) {
+                mma(w.o[b][0][r], a0, pb[r][0], pb[r][1]);
+                mma(w.o[b][1][r], a1, pb[r][0], pb[r][1]);
+            }
+        }
+    }
+}
+
+template <int D, class C>
+__global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
+    using L = CacheLayout<D>;
+    constexpr int NB = C::NB, NTL = C::NTILE, WT = C::WT, WR = C::WR, ST = C::ST, NT = C::NT, NR = C::NR;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t *ring = smem;
+    float *scale = reinterpret_cast<float *>(smem + C::kRing);
+    float *join = reinterpret_cast<float *>(smem + C::kRing + C::kScale);
+    uint4 *sq = reinterpret_cast<uint4 *>(smem + C::kRing + C::kScale + C::kJoin);
+    float *st_m = reinterpret_cast<float *>(smem + C::kRing + C::kScale + C::kJoin + C::kQ);
+    float *st_l = st_m + C::NW * NR;
+    float *st_a = st_l + C::NW * NR;                                   // (joined maximum and sum of each row)
+    uint32_t *bad_pages = reinterpret_cast<uint32_t *>(st_a + C::NW * NR);
+    __shared__ int64_t scan[34];
+    __shared__ int64_t found[2];
+    __shared__ int arrived;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
+    const int wt = warp / WR, wr = warp % WR;                          // which slices, which rows
+    const int G = a.q_heads / a.c.heads;
+
+    // ---- this CTA's share of the line
+    int64_t total = 0;
+    for (int base = 0; base < a.c.B; base += NT) {
+        int64_t all;
+        block_scan<NT>(base + tid < a.c.B ? cost(a, sequence(a, C::ROWS, base + tid)) : 0, all, scan);
+        total += all;
+    }
+    const int64_t share = max((int64_t)WT, (total + gridDim.x - 1) / gridDim.x);
+    int64_t at = share * blockIdx.x;
+    const int64_t end = min(total, at + share);
+    if (at >= end) return;
+    for (int64_t base = 0, before = 0; base < a.c.B; base += NT) {
+        int64_t all;
+        const int64_t c = base + tid < a.c.B ? cost(a, sequence(a, C::ROWS, (int)base + tid)) : 0;
+        const int64_t mine = before + block_scan<NT>(c, all, scan);
+        if (at >= mine && at < mine + c) {
+            found[0] = base + tid;
+            found[1] = at - mine;
+        }
+        before += all;
+        if (at < before) break;
+    }
+    __syncthreads();
+    int b = (int)found[0];
+    Seq seq = sequence(a, C::ROWS, b);
+    int pair = (int)(found[1] / seq.slices), s0 = (int)(found[1] % seq.slices);   // (head, row tile), first slice
+
+    // ---- the ring: slice k of this warp group's in the current pair is slice s0 + wt + k * WT of it
+    uint32_t put = 0, got = 0;                                         // slices copied to and taken from the ring
+    int page_cur[2], page_next[2];                                     // pages of slices k0 + lane, and of the 32 after
+    int copied = 0;                                                    // slices of this pair whose copy was started
+    int n_mine = 0, head = 0, s_first = 0, limit = 0;
+    auto pages_of = [&](int k, int (&p)[2]) {
+        const int64_t t0 = ((int64_t)s_first + wt + (int64_t)k * WT) * kSlice;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) p[i] = k < n_mine && t0 + 16 * i < limit ? cache_page(a.c, b, t0 + 16 * i) : -1;
+    };
+    auto copy = [&]() {  // starts the next slice's copy, or an empty group
+        if (copied < n_mine) {
+            if ((copied & 31) == 0 && copied > 0) {
+                page_cur[0] = page_next[0];
+                page_cur[1] = page_next[1];
+                pages_of(copied + 32 + lane, page_next);
+            }
+            const int64_t t0 = ((int64_t)s_first + wt + (int64_t)copied * WT) * kSlice;
+            const int stage = wt * ST + put % ST;
+            const int p0 = __shfl_sync(0xffffffffu, page_cur[0], copied & 31), p1 = __shfl_sync(0xffffffffu, page_cur[1], copied & 31);
+            const int in_page = (int)(t0 & (a.c.page - 1)) >> 4, in_page1 = (int)((t0 + 16) & (a.c.page - 1)) >> 4;
+            const uint8_t *src0 = a.c.data + (p0 < 0 ? 0 : cache_group<D>(a.c, p0, head, in_page));
+            const uint8_t *src1 = a.c.data + (p1 < 0 ? 0 : cache_group<D>(a.c, p1, head, in_page1));
+            const uint32_t dst = smem_u32(ring + stage * C::kSliceBytes);
+            constexpr int kChunks = L::kGroupBytes / 16;
+#pragma unroll
+            for (int i = 0; i < (2 * kChunks + 32 * WR - 1) / (32 * WR); ++i) {
+                const int c = i * 32 * WR + wr * 32 + lane;
+                const bool second = c >= kChunks;
+                if (c < 2 * kChunks && (second ? p1 : p0) >= 0) cp_async16(dst + c * 16, (second ? src1 - kChunks * 16 : src0) + c * 16);
+            }
+            if (wr == 0 && lane == 0) bad_pages[stage] = (p0 < 0 ? 1u : 0u) | (p1 < 0 ? 2u : 0u);
+            ++put;
+            ++copied;
+        }
+        cp_commit();
+    };
+    auto group_sync = [&]() {
+        if constexpr (WR == 1) __syncwarp();
+        else named_sync(1 + wt, 32 * WR);
+    };
+    auto start_pair = [&](int64_t left) {  // the share's part of pair `pair` from slice s0 on, `left` slices of the share to go
+        head = pair / seq.tiles;
+        s_first = s0;
+        const int count = (int)min((int64_t)(seq.slices - s0), left);
+        limit = min(seq.len, (s0 + count) * kSlice);
+        n_mine = count > wt ? (count - wt + WT - 1) / WT : 0;
+        copied = 0;
+        pages_of(lane, page_cur);
+        pages_of(32 + lane, page_next);
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i) copy();
+        return count;
+    };
+
+    int count = start_pair(end - at);
+    while (true) {
+        const int row0 = (pair % seq.tiles) * C::ROWS, rows = min(C::ROWS, seq.n * G - row0);
+        const int cur_head = head, cur_s0 = s0;
+        const Seq cur = seq;
+        // ---- q: the lane's rows as A fragments, scaled by a power of two to at most 2^4
+        uint32_t q[NB][2][NTL * 2];
+        float f[NTL];
+        int vis[NTL];
+#pragma unroll
+        for (int r = 0; r < NTL; ++r) {
+            const int row = wr * NR + r * 8 + g4;
+            const bool on = row < rows;
+            const int i = (row0 + row) / G;
+            vis[r] = on ? max(0, cur.len - cur.n + i + 1) : 0;
+            float x[NB][8], amax = 0.f;
+            if (on) {
+                const uint16_t *p = a.q + (cur.begin + i) * a.q_stride + (cur_head * G + (row0 + row) % G) * D + t4 * 8;
+#pragma unroll
+                for (int k = 0; k < NB; ++k) unpack8(__ldg(reinterpret_cast<const uint4 *>(p + k * 32)), x[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < NB; ++k)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[k][e]));
+            amax = quad_max(amax);
+            const int up = min(126, 3 + 127 - (int)(__float_as_uint(amax) >> 23));   // amax * 2^up is in [8, 16)
+            const float mul = __uint_as_float((uint32_t)(up + 127) << 23);
+            f[r] = a.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    q[k][h][r] = pack_half(x[k][4 * h] * mul, x[k][4 * h + 1] * mul);
+                    q[k][h][NTL + r] = pack_half(x[k][4 * h + 2] * mul, x[k][4 * h + 3] * mul);
+                }
+        }
+        if constexpr (NTL == 2) {
+            if (wt == 0) {
+#pragma unroll
+                for (int k = 0; k < NB; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        sq[wr * (NB * 2 * 32) + (k * 2 + h) * 32 + lane] = make_uint4(q[k][h][0], q[k][h][1], q[k][h][2], q[k][h][3]);
+            }
+            __syncthreads();
+        }
+        int seen = 0x7fffffff;                                         // tokens that every row sees
+#pragma unroll
+        for (int r = 0; r < NTL; ++r) seen = min(seen, wr * NR + r * 8 + g4 < rows ? vis[r] : 0x7fffffff);
+        seen = __reduce_min_sync(0xffffffffu, seen);
+
+        Warp<D, C> w;
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < NTL; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w.o[k][h][r][e] = 0.f;
+#pragma unroll
+        for (int r = 0; r < NTL; ++r) w.m[r] = -INFINITY, w.l[r] = 0.f;
+        w.top = 0;
+
+        const int n_now = n_mine;
+        for (int k = 0; k < n_now; ++k) {
+            cp_wait<ST - 2>();
+            group_sync();                                              // slice k is there for all, and k - 1 is done with
+            copy();
+            const int stage = wt * ST + got % ST;
+            ++got;
+            const int tok0 = (cur_s0 + wt + k * WT) * kSlice;
+            const uint32_t base = smem_u32(ring + stage * C::kSliceBytes), bad = bad_pages[stage];
+            float *sk = scale + warp * 2 * kSlice * NB, *sv = sk + kSlice * NB;
+            if (tok0 + kSlice <= seen)
+                slice<D, C, false>(w, base, q, sq + wr * (NB * 2 * 32), sk, sv, tok0, cur.len, bad, f, vis);
+            else
+                slice<D, C, true>(w, base, q, sq + wr * (NB * 2 * 32), sk, sv, tok0, cur.len, bad, f, vis);
+            __syncwarp();                                              // (the scales are written anew)
+        }
+        // ---- the next pair's first copies run while this one is joined
+        const int cur_pair = pair;
+        at += count;
+        const bool more = at < end, whole = cur_s0 == 0 && cur_s0 + count == cur.slices;
+        const int64_t pair_begin = at - count - cur_s0;                // on the line
+        group_sync();                                                  // (every warp of the group has read its last slice)
+        if (more) {
+            s0 = 0;
+            if (++pair == a.c.heads * seq.tiles) {
+                pair = 0;
+                do seq = sequence(a, C::ROWS, ++b);
+                while (seq.n == 0);
+            }
+            count = start_pair(end - at);
+        }
+        // ---- the warps' states are joined: rows' maxima and sums first
+#pragma unroll
+        for (int r = 0; r < NTL; ++r) {
+            const float l = quad_sum(w.l[r]);
+            if (t4 == 0) {
+                st_m[warp * NR + r * 8 + g4] = w.m[r];
+                st_l[warp * NR + r * 8 + g4] = l;
+            }
+        }
+        __syncthreads();
+        if (tid < C::ROWS) {  // row tid: warps with wr == tid / NR
+            float m = -INFINITY, l = 0.f;
+            for (int x = 0; x < WT; ++x) m = fmaxf(m, st_m[(x * WR + tid / NR) * NR + tid % NR]);
+            for (int x = 0; x < WT; ++x) {
+                const float mx = st_m[(x * WR + tid / NR) * NR + tid % NR];
+                l = fmaf(st_l[(x * WR + tid / NR) * NR + tid % NR], mx == -INFINITY ? 0.f : ex2(mx - m), l);
+            }
+            st_a[tid] = m;
+            st_a[C::ROWS + tid] = l;
+        }
+        static_assert(2 * C::ROWS <= C::NW * NR, "");
+        __syncthreads();
+        float al[NTL][2];
+        const float unit = ex2((float)((int)w.top - 127 - kGain));
+#pragma unroll
+        for (int r = 0; r < NTL; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = r * 8 + 2 * t4 + e;
+                const float mw = st_m[warp * NR + row];
+                al[r][e] = mw == -INFINITY ? 0.f : ex2(mw - st_a[wr * NR + row]) * unit;
+            }
+        Partial *part = reinterpret_cast<Partial *>(reinterpret_cast<uint8_t *>(a.ctrl) + kControlBytes + kCounterBytes);
+        const int slot = 2 * (int)blockIdx.x + (cur_s0 == 0 ? 1 : 0);
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+#pragma unroll
+            for (int r = 0; r < NTL; ++r)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)  // values 4 g4 .. of rows 8r + 2 t4 + e
+                    *reinterpret_cast<float4 *>(join + (warp * NR + r * 8 + 2 * t4 + e) * 32 + 4 * g4) =
+                        make_float4(w.o[k][0][r][e] * al[r][e], w.o[k][0][r][2 + e] * al[r][e], w.o[k][1][r][e] * al[r][e], w.o[k][1][r][2 + e] * al[r][e]);
+            __syncthreads();
+            for (int row = warp; row < rows; row += C::NW) {
+                float o = 0.f;
+#pragma unroll
+                for (int x = 0; x < WT; ++x) o += join[((x * WR + row / NR) * NR + row % NR) * 32 + lane];
+                if (whole) finish_block(a, cur, cur_head, row0 + row, k, o, st_a[row], st_a[C::ROWS + row]);
+                else part[slot].o[row][k * 32 + lane] = o;
+            }
+            __syncthreads();
+        }
+        // ---- a pair that is cut: the CTA that arrives last joins the parts in order
+        if (!whole) {
+            if (tid < rows) {
+                part[slot].m[tid] = st_a[tid];
+                part[slot].l[tid] = st_a[C::ROWS + tid];
+            }
+            __threadfence();
+            __syncthreads();
+            const int c0 = (int)(pair_begin / share), c1 = (int)((pair_begin + cur.slices - 1) / share);
+            unsigned int *counter = a.ctrl + kControlBytes / 4 + c0;   // one pair at most begins in c0 and goes on
+            if (tid == 0) {
+                const unsigned int before = atomicAdd(counter, 1u);
+                arrived = before == (unsigned)(c1 - c0);
+                if (arrived) *counter = 0;                             // (ready for the next call)
+            }
+            __syncthreads();
+            if (arrived) {
+                __threadfence();
+                float *weight = join + warp * kMaxCtas;
+                for (int task = warp; task < rows * NB; task += C::NW) {
+                    const int row = task / NB, k = task % NB;
+                    float m = -INFINITY, l = 0.f, o = 0.f;
+                    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, __ldcg(&part[2 * c + (c == c0)].m[row]));
+#pragma unroll
+                    for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                    for (int c = c0 + lane; c <= c1; c += 32) {
+                        const float mc = __ldcg(&part[2 * c + (c == c0)].m[row]), x = mc == -INFINITY ? 0.f : ex2(mc - m);
+                        weight[c - c0] = x;
+                        l = fmaf(__ldcg(&part[2 * c + (c == c0)].l[row]), x, l);
+                    }
+                    l = warp_sum(l);
+                    __syncwarp();
+#pragma unroll 8
+                    for (int c = c0; c <= c1; ++c) o = fmaf(__ldcg(&part[2 * c + (c == c0)].o[row][k * 32 + lane]), weight[c - c0], o);
+                    finish_block(a, cur, cur_head, row0 + row, k, o, m, l);
+                    __syncwarp();
+                }
+                __syncthreads();
+            }
+        }
+        if (!more) break;
+        (void)cur_pair;
+    }
+    cp_wait<0>();
+}
+
+template <int D, class C>
+cudaError_t launch_one(const DecodeArgs &a, int num_sms, cudaStream_t stream) {
+    auto kern = decode_kernel<D, C>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    mark_main_kernel(stream, true);
+    kern<<<num_sms < kMaxCtas ? num_sms : kMaxCtas, C::NT, C::kSmem, stream>>>(a);
+    mark_main_kernel(stream, false);
+    return cudaGetLastError();
+}
+
+// By the rows of an average sequence: as few row tiles as there can be, and no more rows than are needed.
+template <int D>
+cudaError_t launch_rows(const DecodeArgs &a, int num_sms, cudaStream_t stream) {
+    const int64_t rows = (a.T + a.c.B - 1) / a.c.B * (a.q_heads / a.c.heads);
+    if (rows <= 8) return launch_one<D, Cfg<D, 8, 1, 12, 3>>(a, num_sms, stream);
+    if (rows <= 16) return launch_one<D, Cfg<D, 16, 1, 12, 3>>(a, num_sms, stream);
+    if (rows <= 32) return launch_one<D, Cfg<D, 16, 2, 12, 3>>(a, num_sms, stream);
+    return launch_one<D, Cfg<D, 16, 4, 12, 3>>(a, num_sms, stream);
 }
 
 }  // namespace
 
-size_t decode_workspace_bytes() { return kControlBytes; }
+size_t decode_workspace_bytes() { return kControlBytes + kCounterBytes + 2 * kMaxCtas * sizeof(Partial); }
 
 cudaError_t launch_decode(const DecodeArgs &a, int num_sms, cudaStream_t stream) {
-    const unsigned grid = (unsigned)((a.T * a.q_heads + kThreads / 32 - 1) / (kThreads / 32));
-    mark_main_kernel(stream, true);
-    if (a.D == 128) decode_rows_kernel<128><<<grid, kThreads, 0, stream>>>(a);
-    else decode_rows_kernel<64><<<grid, kThreads, 0, stream>>>(a);
-    mark_main_kernel(stream, false);
-    return cudaGetLastError();
+    return a.D == 128 ? launch_rows<128>(a, num_sms, stream) : launch_rows<64>(a, num_sms, stream);
 }
 
 }  // namespace mhc
