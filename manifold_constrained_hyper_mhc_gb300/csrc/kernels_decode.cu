@@ -11,15 +11,14 @@
 //
 // The rows of a pair are the tokens times the heads of the group.  For NR = 8 or 16 rows a warp computes, on the legacy
 // tensor path (operands from registers: the codes are converted there and never written back),
-//   S [rows x 32 tokens] = Q K^T   m16n8k16, fp16: E2M1 codes are exact there, and a row of q scaled by a power of two
-//                                  has all its 8 bits; each 32 values' sum is multiplied by its scale in fp32
-//   O^T [D x rows] += V^T P^T      with V's codes and P' = p * 2^(scale - largest scale so far) in fp16 (2^-11 of p; the
-//                                  values that get lost are below 2^-35 of the largest), so V's scales cost nothing on V
+//   S^T [32 tokens x rows] = K Q^T   m16n8k16, fp16: E2M1 codes are exact there, and a row of q scaled by a power of two
+//                                    has all its 8 bits; each 32 values' sum is multiplied by its scale in fp32
+//   O^T [D x rows] += V^T P'^T       with V's codes, and P' = p * 2^(scale - largest scale so far) in fp16 (2^-11 of p, and
+//                                    2^-36 of the largest p; scales below 2^-27 of the largest are lost, as they are in fp32
+//                                    beside that largest)
 // The k order of a product is free: a lane takes 8 neighbouring codes of K (ldmatrix), and 4 of V for two tokens
-// (ldmatrix.trans), as they lie; q and the output follow that order.
-//
-// An ALU instruction takes 1/2 clock a warp and SM here, m16n8k16 2 clocks, so 32 tokens of D = 128 cost about 190 clocks
-// of the ALU and 100 of the tensor pipe for 8 rows, against 190 of memory.
+// (ldmatrix.trans), as they lie; q and the output follow that order.  P crosses from one product's layout to the other's
+// by movmatrix.
 #include "attention.cuh"
 #include "sm100_ptx.cuh"
 
@@ -31,8 +30,13 @@ using namespace ptx;
 constexpr int kMaxCtas = 192;     // partial results and counters in the workspace
 constexpr int kMaxRows = 64;      // rows of a CTA
 constexpr int kSlice = 32;        // tokens
-constexpr float kLazy = 4.f;      // a maximum is raised when a score is above it by more than this (log2): few rescales
-constexpr int kGain = 11;         // P' is p * 2^kGain, at most 2^(kGain + kLazy) (fp16 ends at 2^16)
+// p = 2^(s - m) with m set kHead (log2) below the largest score, and raised when a score is kHead + kLazy above it (few
+// rescales): p is at most 2^12, P' = p * 2^(scale - top + kGain) at most 2^15 (fp16 ends at 2^16).  p loses bits below
+// 2^-14, that is 2^-25 of the largest, and is off by at most 2^-36 of it there.
+constexpr float kHead = 11.f, kLazy = 1.f;
+constexpr int kGain = 3;
+// What a pair costs besides its slices, in slices (its q, its join): 100-token sequences beside long ones.
+constexpr int kPairCost = 12;
 
 struct Partial {                  // of a CTA's share of a pair
     float o[kMaxRows][128];
@@ -47,10 +51,10 @@ struct Cfg {
     static constexpr int WT = NW / WR, ROWS = NR * WR, NT = NW * 32, NB = D / 32, NTILE = NR / 8;
     static constexpr int kSliceBytes = 2 * CacheLayout<D>::kGroupBytes;
     static constexpr int kRing = WT * ST * kSliceBytes;
-    static constexpr int kScale = NW * 2 * kSlice * NB * 4;        // K's and V's scales of a slice in fp32, a warp's own
+    static constexpr int kScale = NW * kSlice * NB * 6;            // a slice's scales, K's in fp32, V's in fp16: a warp's own
     static constexpr int kJoin = NW * NR * 32 * 4;                 // 32 values of every warp's rows; weights of parts
     static_assert(kJoin >= NW * kMaxCtas * 4, "");
-    static constexpr int kQ = NR == 16 ? WR * (D / 16) * 32 * 16 : 0;
+    static constexpr int kQ = NR == 16 ? WR * (D / 16) * 32 * 16 : 0;   // q's fragments
     static constexpr int kStats = 3 * NW * NR * 4 + WT * ST * 4 + 256;
     static constexpr int kSmem = kRing + kScale + kJoin + kQ + kStats;
     static_assert(kSmem <= 232448, "");
@@ -80,13 +84,40 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
 }
-__device__ __forceinline__ float quad_max(float v) {
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // of an 8 x 8 matrix of halves
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+    return d;
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ float quad_max(float v) {   // over the lanes of a group of four
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
     return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
-__device__ __forceinline__ float quad_sum(float v) {
-    v += __shfl_xor_sync(0xffffffffu, v, 1);
-    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+__device__ __forceinline__ float column_max(float v) { // over the lanes with the same place in their group of four
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float column_sum(float v) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// Two scale bytes as fp32 (0 is 2^-127, 255 NaN): the hardware's conversion to bf16, widened.
+__device__ __forceinline__ float2 ue8m0x2(uint32_t bytes) {
+    uint32_t d;
+    asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.bf16x2.ue8m0x2 %0, t; }" : "=r"(d) : "r"(bytes));
+    return make_float2(__uint_as_float(d << 16), __uint_as_float(d & 0xffff0000u));
+}
+// 2^(byte - top + kGain) as fp16 bits, byte <= top: zero below 2^-24, NaN for 255.
+__device__ __forceinline__ uint32_t v_scale(uint32_t byte, uint32_t top) {
+    const int e = (int)byte - (int)top + 15 + kGain;
+    return byte == 255u ? 0x7fffu : e >= 1 ? (uint32_t)e << 10 : e > -10 ? 0x400u >> (1 - e) : 0u;
 }
 
 // What is to be done: a sequence's geometry, and a CTA's place on the line.
@@ -108,7 +139,8 @@ __device__ __forceinline__ Seq sequence(const DecodeArgs &a, int rows, int b) {
     s.slices = max(1, (s.len + kSlice - 1) / kSlice);
     return s;
 }
-__device__ __forceinline__ int64_t cost(const DecodeArgs &a, const Seq &s) { return (int64_t)a.c.heads * s.tiles * s.slices; }
+// On the line a pair is kPairCost places, then its slices.
+__device__ __forceinline__ int64_t cost(const DecodeArgs &a, const Seq &s) { return (int64_t)a.c.heads * s.tiles * (s.slices + kPairCost); }
 
 // A block's exclusive sum; `total` the whole.  Two syncs; `scratch` 33 words.
 template <int NT>
@@ -160,22 +192,24 @@ __device__ __forceinline__ void finish_block(const DecodeArgs &a, const Seq &q, 
 template <int D, class C>
 struct Warp {                              // a warp's running state
     float o[C::NB][2][C::NTILE][4];        // O^T: per 32 values two tiles of 16, per 8 rows
-    float m[C::NTILE], l[C::NTILE];        // row lane / 4 (+ 8): reference maximum, sum of the lane's own tokens
+    float m[C::NTILE][2], l[C::NTILE][2];  // rows 2 (lane % 4) and the next: reference maximum, sum of the lane's own tokens
     uint32_t top;                          // V's largest scale byte so far: o is in units of 2^(top - 127 - kGain)
 };
 
-// A slice of 32 tokens from shared memory.  tok0: its first token; vis: tokens that the lane's rows see.
+// A slice of 32 tokens from shared memory.  tok0: its first token; vis: tokens that rows 2 (lane % 4) and the next see,
+// vis_g: those that row lane / 4 sees; f: the factors of those rows' scores.
 template <int D, class C, bool kMask>
 __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32_t (&q)[C::NB][2][C::NTILE * 2], const uint4 *sq,
-                                      float *sk, float *sv, int tok0, int len, uint32_t bad, const float (&f)[C::NTILE], const int (&vis)[C::NTILE]) {
+                                      float *sk, uint32_t *sv, int tok0, int len, uint32_t bad, const float (&f)[C::NTILE][2],
+                                      const int (&vis)[C::NTILE][2], const int (&vis_g)[C::NTILE]) {
     using L = CacheLayout<D>;
     constexpr int NB = C::NB, NTL = C::NTILE;
-    const int lane = threadIdx.x & 31, t4 = lane & 3;
+    const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
     // ---- scales, a token a lane
-    uint32_t vtop;
+    uint32_t vw, vmax = 0;
     {
         const uint32_t at = base + (lane >> 4) * L::kGroupBytes + L::kScales + (lane & 15) * NB;
-        uint32_t kw, vw;
+        uint32_t kw;
         if constexpr (NB == 4) {
             asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(at));
             asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw) : "r"(at + L::kPart));
@@ -183,44 +217,24 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
             asm volatile("ld.shared.u16 %0, [%1];" : "=r"(kw) : "r"(at));
             asm volatile("ld.shared.u16 %0, [%1];" : "=r"(vw) : "r"(at + L::kPart));
         }
-        if ((bad >> (lane >> 4)) & 1u) kw = vw = 0xffffffffu;   // no such page: NaN
-        const bool there = tok0 + lane < len;
-        uint32_t top = 0;
+        if constexpr (kMask) {
+            if ((bad >> (lane >> 4)) & 1u) kw = vw = 0xffffffffu;   // no such page: NaN
+            if (tok0 + lane >= len) kw = vw = 0u;                   // (what the rest of a page holds)
+        }
+        const float2 k01 = ue8m0x2(kw);
+        if constexpr (NB == 4) {
+            const float2 k23 = ue8m0x2(kw >> 16);
+            *reinterpret_cast<float4 *>(sk + lane * 4) = make_float4(k01.x, k01.y, k23.x, k23.y);
+        } else {
+            *reinterpret_cast<float2 *>(sk + lane * 2) = k01;
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const uint32_t e = (vw >> (8 * b)) & 255u;
-            top = max(top, there && e != 255u ? e : 0u);
-        }
-        vtop = max(w.top, __reduce_max_sync(0xffffffffu, top));
-        float ks[NB], vs[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const uint32_t ke = (kw >> (8 * b)) & 255u, ve = (vw >> (8 * b)) & 255u;
-            ks[b] = there ? ue8m0(ke) : 0.f;
-            const int d = (int)ve - (int)vtop + 127 + kGain;
-            vs[b] = !there || d < 0 ? 0.f : ve == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)d << 23);
-        }
-        if constexpr (NB == 4) {
-            *reinterpret_cast<float4 *>(sk + lane * 4) = make_float4(ks[0], ks[1], ks[2], ks[3]);
-            *reinterpret_cast<float4 *>(sv + lane * 4) = make_float4(vs[0], vs[1], vs[2], vs[3]);
-        } else {
-            *reinterpret_cast<float2 *>(sk + lane * 2) = make_float2(ks[0], ks[1]);
-            *reinterpret_cast<float2 *>(sv + lane * 2) = make_float2(vs[0], vs[1]);
+            vmax = max(vmax, e == 255u ? 0u : e);
         }
         __syncwarp();
     }
-    // the lane's tokens 8n + 2 t4 and the next: [token][block]
-    auto scales = [&](const float *s, int n, float (&x)[2][NB]) {
-        const float4 *p = reinterpret_cast<const float4 *>(s + (8 * n + 2 * t4) * NB);
-        if constexpr (NB == 4) {
-            const float4 u = p[0], v = p[1];
-            x[0][0] = u.x; x[0][1] = u.y; x[0][2] = u.z; x[0][3] = u.w;
-            x[1][0] = v.x; x[1][1] = v.y; x[1][2] = v.z; x[1][3] = v.w;
-        } else {
-            const float4 u = p[0];
-            x[0][0] = u.x; x[0][1] = u.y; x[1][0] = u.z; x[1][1] = u.w;
-        }
-    };
     // the codes of 8 tokens (n) and all blocks, or of 16 tokens (2 n') and both blocks for D = 64
     auto codes_at = [&](int part, int i) {
         const int mi = lane >> 3;
@@ -228,120 +242,168 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
         const int row = (n & 1) * 8 + (lane & 7);
         return base + (n >> 1) * L::kGroupBytes + part * L::kPart + row * L::kRow + ((blk ^ L::swizzle(row)) * 16);
     };
-    // ---- scores
-    float s[4][2 * NTL];
+    // 16 tokens' codes: r0 the first 8, r1 the others, a block each
+    auto fetch = [&](int part, int h, uint32_t (&r0)[NB], uint32_t (&r1)[NB]) {
+        uint32_t r[4];
+        if constexpr (NB == 4) {
+            if (part == 0) ldsm4(r, codes_at(0, 2 * h)); else ldsm4t(r, codes_at(1, 2 * h));
 #pragma unroll
-    for (int i = 0; i < (NB == 4 ? 4 : 2); ++i) {
-        uint32_t kc[4];
-        ldsm4(kc, codes_at(0, i));
+            for (int b = 0; b < 4; ++b) r0[b] = r[b];
+            if (part == 0) ldsm4(r, codes_at(0, 2 * h + 1)); else ldsm4t(r, codes_at(1, 2 * h + 1));
 #pragma unroll
-        for (int nn = 0; nn < (NB == 4 ? 1 : 2); ++nn) {
-            const int n = NB == 4 ? i : 2 * i + nn;
-            float sc[2][NB];
-            scales(sk, n, sc);
+            for (int b = 0; b < 4; ++b) r1[b] = r[b];
+        } else {
+            if (part == 0) ldsm4(r, codes_at(0, h)); else ldsm4t(r, codes_at(1, h));
+            r0[0] = r[0]; r0[1] = r[1]; r1[0] = r[2]; r1[1] = r[3];
+        }
+    };
+    // ---- scores: s[h][r] holds tokens 16 h + g4 (and + 8) x rows 8 r + 2 t4 (and + 1)
+    float s[2][NTL][4];
 #pragma unroll
-            for (int e = 0; e < 2 * NTL; ++e) s[n][e] = 0.f;
+    for (int h = 0; h < 2; ++h) {
+        uint32_t r0[NB], r1[NB];
+        fetch(0, h, r0, r1);
+        float sc0[NB], sc1[NB];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const uint32_t c = kc[NB == 4 ? b : nn * 2 + b];
+        for (int b = 0; b < NB; b += (NB == 4 ? 4 : 2)) {
+            const float *p0 = sk + (16 * h + g4) * NB, *p1 = p0 + 8 * NB;
+            if constexpr (NB == 4) {
+                const float4 u = *reinterpret_cast<const float4 *>(p0), v = *reinterpret_cast<const float4 *>(p1);
+                sc0[0] = u.x; sc0[1] = u.y; sc0[2] = u.z; sc0[3] = u.w;
+                sc1[0] = v.x; sc1[1] = v.y; sc1[2] = v.z; sc1[3] = v.w;
+            } else {
+                const float2 u = *reinterpret_cast<const float2 *>(p0), v = *reinterpret_cast<const float2 *>(p1);
+                sc0[0] = u.x; sc0[1] = u.y; sc1[0] = v.x; sc1[1] = v.y;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t a0[4] = {e2m1x2<0>(r0[b]), e2m1x2<0>(r1[b]), e2m1x2<1>(r0[b]), e2m1x2<1>(r1[b])};
+            const uint32_t a1[4] = {e2m1x2<2>(r0[b]), e2m1x2<2>(r1[b]), e2m1x2<3>(r0[b]), e2m1x2<3>(r1[b])};
+            uint32_t qb[NTL][4];
+            if constexpr (NTL == 1) {
+                qb[0][0] = q[b][0][0]; qb[0][1] = q[b][0][1]; qb[0][2] = q[b][1][0]; qb[0][3] = q[b][1][1];
+            } else {
+                const uint4 u0 = sq[(b * 2) * 32 + lane], u1 = sq[(b * 2 + 1) * 32 + lane];
+                qb[0][0] = u0.x; qb[1][0] = u0.y; qb[0][1] = u0.z; qb[1][1] = u0.w;
+                qb[0][2] = u1.x; qb[1][2] = u1.y; qb[0][3] = u1.z; qb[1][3] = u1.w;
+            }
+#pragma unroll
+            for (int r = 0; r < NTL; ++r) {
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                if constexpr (NTL == 1) {
-                    const uint32_t a0[4] = {q[b][0][0], 0u, q[b][0][1], 0u}, a1[4] = {q[b][1][0], 0u, q[b][1][1], 0u};
-                    mma(acc, a0, e2m1x2<0>(c), e2m1x2<1>(c));
-                    mma(acc, a1, e2m1x2<2>(c), e2m1x2<3>(c));
-                } else {
-                    const uint4 u0 = sq[(b * 2) * 32 + lane], u1 = sq[(b * 2 + 1) * 32 + lane];
-                    const uint32_t a0[4] = {u0.x, u0.y, u0.z, u0.w}, a1[4] = {u1.x, u1.y, u1.z, u1.w};
-                    mma(acc, a0, e2m1x2<0>(c), e2m1x2<1>(c));
-                    mma(acc, a1, e2m1x2<2>(c), e2m1x2<3>(c));
-                }
+                mma(acc, a0, qb[r][0], qb[r][1]);
+                mma(acc, a1, qb[r][2], qb[r][3]);
 #pragma unroll
-                for (int e = 0; e < 2 * NTL; ++e) s[n][e] = fmaf(acc[e], sc[e & 1][b], s[n][e]);
+                for (int e = 0; e < 4; ++e) {
+                    const float k = e < 2 ? sc0[b] : sc1[b];
+                    s[h][r][e] = b == 0 ? acc[e] * k : fmaf(acc[e], k, s[h][r][e]);
+                }
             }
         }
     }
     // ---- the running maximum
-    float hi[NTL];
+    float hi[NTL][2];
+    bool raise = vmax > w.top;
 #pragma unroll
-    for (int r = 0; r < NTL; ++r) hi[r] = -INFINITY;
+    for (int r = 0; r < NTL; ++r)
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int e = 0; e < 2 * NTL; ++e) {
-            s[n][e] *= f[e >> 1];
-            if (kMask && tok0 + 8 * n + 2 * t4 + (e & 1) >= vis[e >> 1]) s[n][e] = -INFINITY;
-            hi[e >> 1] = fmaxf(hi[e >> 1], s[n][e]);
-        }
-    bool raise = vtop != w.top;
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int r = 0; r < NTL; ++r) raise |= hi[r] > w.m[r] + kLazy;
-    if (__any_sync(0xffffffffu, raise)) {
-        const float unit = ex2((float)((int)w.top - (int)vtop));
-        w.top = vtop;
-#pragma unroll
-        for (int r = 0; r < NTL; ++r) {
-            const float top = fmaxf(w.m[r], quad_max(hi[r]));
-            const float al = w.m[r] == -INFINITY ? 0.f : ex2(w.m[r] - top);
-            w.m[r] = top;
-            w.l[r] *= al;
-            // the accumulators' rows are 8r + 2 t4 and the next: held, as rows, by lanes 8 t4 and 8 t4 + 4
-            const float x = __shfl_sync(0xffffffffu, al, 8 * t4) * unit, y = __shfl_sync(0xffffffffu, al, 8 * t4 + 4) * unit;
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    w.o[b][h][r][0] *= x;
-                    w.o[b][h][r][1] *= y;
-                    w.o[b][h][r][2] *= x;
-                    w.o[b][h][r][3] *= y;
+                for (int j = 0; j < 2; ++j) {
+                    float &x = s[h][r][2 * j + e];
+                    x *= f[r][e];
+                    if (kMask && tok0 + 16 * h + 8 * j + g4 >= vis[r][e]) x = -INFINITY;
                 }
+            hi[r][e] = fmaxf(fmaxf(s[0][r][e], s[0][r][2 + e]), fmaxf(s[1][r][e], s[1][r][2 + e]));
+            raise |= hi[r][e] > w.m[r][e] + (kHead + kLazy);
         }
+    if (__any_sync(0xffffffffu, raise)) {
+        const uint32_t top = max(w.top, __reduce_max_sync(0xffffffffu, vmax));
+        const float unit = ex2((float)((int)w.top - (int)top));
+        w.top = top;
+#pragma unroll
+        for (int r = 0; r < NTL; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float m = fmaxf(w.m[r][e], column_max(hi[r][e]) - kHead);
+                const float al = w.m[r][e] == -INFINITY ? 0.f : ex2(w.m[r][e] - m);
+                w.m[r][e] = m;
+                w.l[r][e] *= al;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        w.o[b][h][r][e] *= al * unit;
+                        w.o[b][h][r][2 + e] *= al * unit;
+                    }
+            }
     }
-    // ---- exponentials and their sums
+    // ---- V's scales: word (token pair, block)
+    {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, vw, 1);
+        const uint32_t even = lane & 1 ? other : vw, odd = lane & 1 ? vw : other;
+        uint32_t x[NB / 2];
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) {   // an even lane writes the first half of the blocks, an odd one the second
+            const int sh = 8 * ((lane & 1) * (NB / 2) + i);
+            x[i] = v_scale((even >> sh) & 255u, w.top) | v_scale((odd >> sh) & 255u, w.top) << 16;
+        }
+        if constexpr (NB == 4) *reinterpret_cast<uint2 *>(sv + (lane >> 1) * 4 + (lane & 1) * 2) = make_uint2(x[0], x[1]);
+        else sv[(lane >> 1) * 2 + (lane & 1)] = x[0];
+    }
+    // ---- exponentials and their sums; p as halves, turned: p16[r][n] is row 8 r + g4, tokens 8 n + 2 t4 (and + 1)
+    uint32_t p16[NTL][4];
 #pragma unroll
     for (int r = 0; r < NTL; ++r) {
-        const float m = w.m[r] == -INFINITY ? 0.f : w.m[r];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            s[n][2 * r] = ex2(s[n][2 * r] - m);
-            s[n][2 * r + 1] = ex2(s[n][2 * r + 1] - m);
-            w.l[r] += s[n][2 * r] + s[n][2 * r + 1];
+        for (int e = 0; e < 2; ++e) {
+            const float m = w.m[r][e] == -INFINITY ? 0.f : w.m[r][e];
+            float sum = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    s[h][r][2 * j + e] = ex2(s[h][r][2 * j + e] - m);
+                    sum += s[h][r][2 * j + e];
+                }
+            w.l[r][e] += sum;
         }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) p16[r][n] = transpose8(pack_half(s[n >> 1][r][2 * (n & 1)], s[n >> 1][r][2 * (n & 1) + 1]));
     }
+    __syncwarp();
     // ---- O^T += V^T P'^T, 16 tokens at a time
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        uint32_t v0[NB], v1[NB];   // tokens 16h .. +7, and the next 8
-        {
-            uint32_t r[4];
-            ldsm4t(r, codes_at(1, NB == 4 ? 2 * h : h));
+        uint32_t v0[NB], v1[NB];
+        fetch(1, h, v0, v1);
+        uint32_t sc[2][NB];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t *p = sv + (4 * (2 * h + j) + t4) * NB;
             if constexpr (NB == 4) {
-#pragma unroll
-                for (int b = 0; b < 4; ++b) v0[b] = r[b];
-                ldsm4t(r, codes_at(1, 2 * h + 1));
-#pragma unroll
-                for (int b = 0; b < 4; ++b) v1[b] = r[b];
+                const uint4 u = *reinterpret_cast<const uint4 *>(p);
+                sc[j][0] = u.x; sc[j][1] = u.y; sc[j][2] = u.z; sc[j][3] = u.w;
             } else {
-                v0[0] = r[0]; v0[1] = r[1]; v1[0] = r[2]; v1[1] = r[3];
+                const uint2 u = *reinterpret_cast<const uint2 *>(p);
+                sc[j][0] = u.x; sc[j][1] = u.y;
             }
         }
-        float s0[2][NB], s1[2][NB];
-        scales(sv, 2 * h, s0);
-        scales(sv, 2 * h + 1, s1);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             uint32_t pb[NTL][2];
 #pragma unroll
-            for (int r = 0; r < NTL; ++r) {
-                float x[4] = {s[2 * h][2 * r] * s0[0][b], s[2 * h][2 * r + 1] * s0[1][b], s[2 * h + 1][2 * r] * s1[0][b], s[2 * h + 1][2 * r + 1] * s1[1][b]};
-                if constexpr (kMask) {  // (0 times a NaN scale is none of what a row does not see)
+            for (int r = 0; r < NTL; ++r)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (tok0 + 16 * h + 8 * (e >> 1) + 2 * t4 + (e & 1) >= vis[r]) x[e] = 0.f;
+                for (int j = 0; j < 2; ++j) {
+                    pb[r][j] = mul_half2(p16[r][2 * h + j], sc[j][b]);
+                    if constexpr (kMask) {  // (0 times a NaN scale is no part of what a row does not see)
+                        const int tok = tok0 + 16 * h + 8 * j + 2 * t4;
+                        pb[r][j] &= (tok < vis_g[r] ? 0xffffu : 0u) | (tok + 1 < vis_g[r] ? 0xffff0000u : 0u);
+                    }
                 }
-                pb[r][0] = pack_half(x[0], x[1]);
-                pb[r][1] = pack_half(x[2], x[3]);
-            }
             const uint32_t e0 = e2m1x2<0>(v0[b]), e1 = e2m1x2<2>(v0[b]), e2 = e2m1x2<0>(v1[b]), e3 = e2m1x2<2>(v1[b]);
             const uint32_t g0 = e2m1x2<1>(v0[b]), g1 = e2m1x2<3>(v0[b]), g2 = e2m1x2<1>(v1[b]), g3 = e2m1x2<3>(v1[b]);
             const uint32_t a0[4] = {__byte_perm(e0, e1, 0x5410), __byte_perm(e0, e1, 0x7632), __byte_perm(e2, e3, 0x5410), __byte_perm(e2, e3, 0x7632)};
@@ -400,11 +462,12 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
     __syncthreads();
     int b = (int)found[0];
     Seq seq = sequence(a, C::ROWS, b);
-    int pair = (int)(found[1] / seq.slices), s0 = (int)(found[1] % seq.slices);   // (head, row tile), first slice
+    int pair = (int)(found[1] / (seq.slices + kPairCost));                          // (head, row tile)
+    int s0 = (int)(found[1] % (seq.slices + kPairCost)) - kPairCost;                // first slice; below 0: the pair's own cost
 
     // ---- the ring: slice k of this warp group's in the current pair is slice s0 + wt + k * WT of it
     uint32_t put = 0, got = 0;                                         // slices copied to and taken from the ring
-    int page_cur[2], page_next[2];                                     // pages of slices k0 + lane, and of the 32 after
+    int page_cur[2] = {-1, -1}, page_next[2] = {-1, -1};                                     // pages of slices k0 + lane, and of the 32 after
     int copied = 0;                                                    // slices of this pair whose copy was started
     int n_mine = 0, head = 0, s_first = 0, limit = 0;
     auto pages_of = [&](int k, int (&p)[2]) {
@@ -419,20 +482,25 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
                 page_cur[1] = page_next[1];
                 pages_of(copied + 32 + lane, page_next);
             }
-            const int64_t t0 = ((int64_t)s_first + wt + (int64_t)copied * WT) * kSlice;
+            const int t0 = (s_first + wt + copied * WT) * kSlice;
             const int stage = wt * ST + put % ST;
             const int p0 = __shfl_sync(0xffffffffu, page_cur[0], copied & 31), p1 = __shfl_sync(0xffffffffu, page_cur[1], copied & 31);
-            const int in_page = (int)(t0 & (a.c.page - 1)) >> 4, in_page1 = (int)((t0 + 16) & (a.c.page - 1)) >> 4;
-            const uint8_t *src0 = a.c.data + (p0 < 0 ? 0 : cache_group<D>(a.c, p0, head, in_page));
-            const uint8_t *src1 = a.c.data + (p1 < 0 ? 0 : cache_group<D>(a.c, p1, head, in_page1));
-            const uint32_t dst = smem_u32(ring + stage * C::kSliceBytes);
-            constexpr int kChunks = L::kGroupBytes / 16;
+            constexpr int kChunks = L::kGroupBytes / 16, kRound = kChunks / 32 * 32;   // whole warps' rounds, then both groups' rest
+            const uint32_t dst = smem_u32(ring + stage * C::kSliceBytes) + lane * 16;
+            const uint8_t *src0 = a.c.data + cache_group<D>(a.c, max(p0, 0), head, (t0 & (a.c.page - 1)) >> 4) + lane * 16;
+            const uint8_t *src1 = a.c.data + cache_group<D>(a.c, max(p1, 0), head, ((t0 + 16) & (a.c.page - 1)) >> 4) + lane * 16;
+            constexpr int kRest = kChunks - kRound;                                     // 8 or 4: lanes 0 .. for the first group, then the second
+            static_assert(2 * kRest <= 32, "");
+            if (p0 >= 0) {
 #pragma unroll
-            for (int i = 0; i < (2 * kChunks + 32 * WR - 1) / (32 * WR); ++i) {
-                const int c = i * 32 * WR + wr * 32 + lane;
-                const bool second = c >= kChunks;
-                if (c < 2 * kChunks && (second ? p1 : p0) >= 0) cp_async16(dst + c * 16, (second ? src1 - kChunks * 16 : src0) + c * 16);
+                for (int i = wr * 512; i < kRound * 16; i += WR * 512) cp_async16(dst + i, src0 + i);
             }
+            if (p1 >= 0) {
+#pragma unroll
+                for (int i = wr * 512; i < kRound * 16; i += WR * 512) cp_async16(dst + L::kGroupBytes + i, src1 + i);
+            }
+            if (wr == 0 && lane < 2 * kRest && (lane < kRest ? p0 : p1) >= 0)
+                cp_async16(dst + kRound * 16 + (lane < kRest ? 0 : L::kGroupBytes - kRest * 16), (lane < kRest ? src0 : src1 - kRest * 16) + kRound * 16);
             if (wr == 0 && lane == 0) bad_pages[stage] = (p0 < 0 ? 1u : 0u) | (p1 < 0 ? 2u : 0u);
             ++put;
             ++copied;
@@ -443,15 +511,25 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
         if constexpr (WR == 1) __syncwarp();
         else named_sync(1 + wt, 32 * WR);
     };
-    auto start_pair = [&](int64_t left) {  // the share's part of pair `pair` from slice s0 on, `left` slices of the share to go
+    uint4 qw[NTL][NB];                                                 // q of the lane's rows, 8 values of each block
+    auto start_pair = [&](int64_t left) {  // the share's part of pair `pair` from place s0 on, `left` places of the share to go
         head = pair / seq.tiles;
-        s_first = s0;
         const int count = (int)min((int64_t)(seq.slices - s0), left);
-        limit = min(seq.len, (s0 + count) * kSlice);
-        n_mine = count > wt ? (count - wt + WT - 1) / WT : 0;
+        s_first = max(s0, 0);
+        const int s_end = s0 + count;
+        limit = min(seq.len, max(0, s_end) * kSlice);
+        n_mine = s_end - s_first > wt ? (s_end - s_first - wt + WT - 1) / WT : 0;
         copied = 0;
         pages_of(lane, page_cur);
         pages_of(32 + lane, page_next);
+        const int row0 = (pair % seq.tiles) * C::ROWS, rows = min(C::ROWS, seq.n * G - row0);
+#pragma unroll
+        for (int r = 0; r < NTL; ++r) {
+            const int row = wr * NR + r * 8 + g4, i = (row0 + row) / G;
+            const uint16_t *p = a.q + (seq.begin + i) * a.q_stride + (head * G + (row0 + row) % G) * D + t4 * 8;
+#pragma unroll
+            for (int k = 0; k < NB; ++k) qw[r][k] = row < rows ? __ldg(reinterpret_cast<const uint4 *>(p + k * 32)) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
         for (int i = 0; i < ST - 1; ++i) copy();
         return count;
@@ -460,37 +538,34 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
     int count = start_pair(end - at);
     while (true) {
         const int row0 = (pair % seq.tiles) * C::ROWS, rows = min(C::ROWS, seq.n * G - row0);
-        const int cur_head = head, cur_s0 = s0;
+        const int cur_head = head, cur_s0 = s0, cur_first = s_first;
         const Seq cur = seq;
-        // ---- q: the lane's rows as A fragments, scaled by a power of two to at most 2^4
+        // ---- q: row lane / 4 (+ 8) as B fragments, scaled by a power of two to at most 2^4
         uint32_t q[NB][2][NTL * 2];
-        float f[NTL];
-        int vis[NTL];
+        float f[NTL][2];
+        int vis[NTL][2], vis_g[NTL];
+        int seen = 0x7fffffff;                                         // tokens that every row sees
 #pragma unroll
         for (int r = 0; r < NTL; ++r) {
             const int row = wr * NR + r * 8 + g4;
-            const bool on = row < rows;
-            const int i = (row0 + row) / G;
-            vis[r] = on ? max(0, cur.len - cur.n + i + 1) : 0;
+            vis_g[r] = row < rows ? max(0, cur.len - cur.n + (row0 + row) / G + 1) : 0;
+            seen = min(seen, row < rows ? vis_g[r] : 0x7fffffff);
             float x[NB][8], amax = 0.f;
-            if (on) {
-                const uint16_t *p = a.q + (cur.begin + i) * a.q_stride + (cur_head * G + (row0 + row) % G) * D + t4 * 8;
 #pragma unroll
-                for (int k = 0; k < NB; ++k) unpack8(__ldg(reinterpret_cast<const uint4 *>(p + k * 32)), x[k]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < NB; ++k)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
-            }
-#pragma unroll
-            for (int k = 0; k < NB; ++k)
+            for (int k = 0; k < NB; ++k) {
+                unpack8(qw[r][k], x[k]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[k][e]));
+            }
             amax = quad_max(amax);
             const int up = min(126, 3 + 127 - (int)(__float_as_uint(amax) >> 23));   // amax * 2^up is in [8, 16)
             const float mul = __uint_as_float((uint32_t)(up + 127) << 23);
-            f[r] = a.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 - up) << 23);
+            const float fg = a.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                f[r][e] = __shfl_sync(0xffffffffu, fg, 8 * t4 + 4 * e);
+                vis[r][e] = __shfl_sync(0xffffffffu, vis_g[r], 8 * t4 + 4 * e);
+            }
 #pragma unroll
             for (int k = 0; k < NB; ++k)
 #pragma unroll
@@ -499,6 +574,7 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
                     q[k][h][NTL + r] = pack_half(x[k][4 * h + 2] * mul, x[k][4 * h + 3] * mul);
                 }
         }
+        seen = __reduce_min_sync(0xffffffffu, seen);
         if constexpr (NTL == 2) {
             if (wt == 0) {
 #pragma unroll
@@ -509,11 +585,6 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             }
             __syncthreads();
         }
-        int seen = 0x7fffffff;                                         // tokens that every row sees
-#pragma unroll
-        for (int r = 0; r < NTL; ++r) seen = min(seen, wr * NR + r * 8 + g4 < rows ? vis[r] : 0x7fffffff);
-        seen = __reduce_min_sync(0xffffffffu, seen);
-
         Warp<D, C> w;
 #pragma unroll
         for (int k = 0; k < NB; ++k)
@@ -524,7 +595,9 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w.o[k][h][r][e] = 0.f;
 #pragma unroll
-        for (int r = 0; r < NTL; ++r) w.m[r] = -INFINITY, w.l[r] = 0.f;
+        for (int r = 0; r < NTL; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) w.m[r][e] = -INFINITY, w.l[r][e] = 0.f;
         w.top = 0;
 
         const int n_now = n_mine;
@@ -534,23 +607,23 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             copy();
             const int stage = wt * ST + got % ST;
             ++got;
-            const int tok0 = (cur_s0 + wt + k * WT) * kSlice;
+            const int tok0 = (cur_first + wt + k * WT) * kSlice;
             const uint32_t base = smem_u32(ring + stage * C::kSliceBytes), bad = bad_pages[stage];
-            float *sk = scale + warp * 2 * kSlice * NB, *sv = sk + kSlice * NB;
-            if (tok0 + kSlice <= seen)
-                slice<D, C, false>(w, base, q, sq + wr * (NB * 2 * 32), sk, sv, tok0, cur.len, bad, f, vis);
+            float *sk = scale + warp * (kSlice * NB * 3 / 2);
+            uint32_t *sv = reinterpret_cast<uint32_t *>(sk + kSlice * NB);
+            if (tok0 + kSlice <= seen && bad == 0)
+                slice<D, C, false>(w, base, q, sq + wr * (NB * 2 * 32), sk, sv, tok0, cur.len, bad, f, vis, vis_g);
             else
-                slice<D, C, true>(w, base, q, sq + wr * (NB * 2 * 32), sk, sv, tok0, cur.len, bad, f, vis);
+                slice<D, C, true>(w, base, q, sq + wr * (NB * 2 * 32), sk, sv, tok0, cur.len, bad, f, vis, vis_g);
             __syncwarp();                                              // (the scales are written anew)
         }
         // ---- the next pair's first copies run while this one is joined
-        const int cur_pair = pair;
         at += count;
-        const bool more = at < end, whole = cur_s0 == 0 && cur_s0 + count == cur.slices;
-        const int64_t pair_begin = at - count - cur_s0;                // on the line
+        const bool more = at < end, whole = cur_s0 == -kPairCost && cur_s0 + count == cur.slices;
+        const int64_t pair_begin = at - count - (cur_s0 + kPairCost);  // on the line
         group_sync();                                                  // (every warp of the group has read its last slice)
         if (more) {
-            s0 = 0;
+            s0 = -kPairCost;
             if (++pair == a.c.heads * seq.tiles) {
                 pair = 0;
                 do seq = sequence(a, C::ROWS, ++b);
@@ -560,13 +633,15 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
         }
         // ---- the warps' states are joined: rows' maxima and sums first
 #pragma unroll
-        for (int r = 0; r < NTL; ++r) {
-            const float l = quad_sum(w.l[r]);
-            if (t4 == 0) {
-                st_m[warp * NR + r * 8 + g4] = w.m[r];
-                st_l[warp * NR + r * 8 + g4] = l;
+        for (int r = 0; r < NTL; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float l = column_sum(w.l[r][e]);
+                if (g4 == 0) {
+                    st_m[warp * NR + r * 8 + 2 * t4 + e] = w.m[r][e];
+                    st_l[warp * NR + r * 8 + 2 * t4 + e] = l;
+                }
             }
-        }
         __syncthreads();
         if (tid < C::ROWS) {  // row tid: warps with wr == tid / NR
             float m = -INFINITY, l = 0.f;
@@ -586,12 +661,10 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
         for (int r = 0; r < NTL; ++r)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int row = r * 8 + 2 * t4 + e;
-                const float mw = st_m[warp * NR + row];
-                al[r][e] = mw == -INFINITY ? 0.f : ex2(mw - st_a[wr * NR + row]) * unit;
+                al[r][e] = w.m[r][e] == -INFINITY ? 0.f : ex2(w.m[r][e] - st_a[wr * NR + r * 8 + 2 * t4 + e]) * unit;
             }
         Partial *part = reinterpret_cast<Partial *>(reinterpret_cast<uint8_t *>(a.ctrl) + kControlBytes + kCounterBytes);
-        const int slot = 2 * (int)blockIdx.x + (cur_s0 == 0 ? 1 : 0);
+        const int slot = 2 * (int)blockIdx.x + (cur_s0 == -kPairCost ? 1 : 0);
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
 #pragma unroll
@@ -618,7 +691,7 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             }
             __threadfence();
             __syncthreads();
-            const int c0 = (int)(pair_begin / share), c1 = (int)((pair_begin + cur.slices - 1) / share);
+            const int c0 = (int)(pair_begin / share), c1 = (int)((pair_begin + kPairCost + cur.slices - 1) / share);
             unsigned int *counter = a.ctrl + kControlBytes / 4 + c0;   // one pair at most begins in c0 and goes on
             if (tid == 0) {
                 const unsigned int before = atomicAdd(counter, 1u);
@@ -651,7 +724,6 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             }
         }
         if (!more) break;
-        (void)cur_pair;
     }
     cp_wait<0>();
 }

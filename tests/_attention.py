@@ -111,7 +111,8 @@ def attend(q, k, v, scale, p_type):
     The bound: each score is a sum of D products in fp32 (any order, each addition off by at most 2^-23 of the sum of
     magnitudes, truncation included), so off by D 2^-23 sum|q k| scale, and by 2^-21 of itself from the scaling and the
     exponential's own error; p_j is rounded to p_type; the sums over the keys run in fp32, n 2^-23 of the sum of
-    magnitudes, with the running rescales (as many roundings again at most); l gets the same relative errors."""
+    magnitudes, with the running rescales (as many roundings again at most); l gets the same relative errors.  In fp16 p ends at
+    2^-25 of 2^-11 of the largest: each of the L terms is off by at most 2^-36 of its v beside the rounding."""
     n, Hq, D = q.shape
     L, Hkv, _ = k.shape
     G = Hq // Hkv
@@ -137,7 +138,7 @@ def attend(q, k, v, scale, p_type):
     A = w @ vz.abs()
     delta = (D * 2.0 ** -23 * mag + 2.0 ** -21 * torch.where(hide, 0.0, s).abs()).amax(-1, keepdim=True) + 2.0 ** -21
     rest = 2 * L * 2.0 ** -23
-    tol = A * (U[p_type] + 2 * delta + 2 * rest) + vz.abs().amax((1, 2), keepdim=True) * 2.0 ** -36
+    tol = A * (U[p_type] + 2 * delta + 2 * rest) + vz.abs().amax((1, 2), keepdim=True) * (L * 2.0 ** -36 if p_type == "f16" else 2.0 ** -36)
     lse = torch.where(empty, m, m0 + l.log())[..., 0]
     tol_lse = (delta + rest)[..., 0] + 2.0 ** -21 * torch.where(empty[..., 0], 0.0, lse).abs()
     return out.permute(1, 0, 2), lse.t(), tol.permute(1, 0, 2), tol_lse.t()
