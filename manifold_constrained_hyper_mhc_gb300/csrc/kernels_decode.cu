@@ -3,11 +3,11 @@
 //   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(s_j - m),  s_j = sm_scale log2(e) <q, k_j>,  m the largest s so far
 //
 // The cache is read once (17/32 byte a value): that is the floor, and what must not be in its way are the conversions,
-// about three instructions for every four codes.  One CTA an SM; the keys of all (sequence, kv head) pairs are one long
-// line of slices of 32 tokens, cut into equal shares whatever the lengths (the host knows none of them).  A CTA's warps
-// take the slices of its share in turn, each with its own running maximum, sum and accumulators, copied ahead into its
-// own ring in shared memory, and are joined at the end of each pair; a pair that is cut leaves its parts in the
-// workspace, and the CTA that arrives last joins them, in order.
+// about three instructions for every four codes.  The keys of all (sequence, kv head) pairs are one long line of slices of
+// 32 tokens, cut into equal shares whatever the lengths (the host knows none of them), a share for each warp of one CTA an
+// SM (a group of warps where there are many rows).  A warp keeps its own running maximum, sum and accumulators, and its
+// copies run ahead into its own ring in shared memory: no two warps wait for each other.  A pair that lies in one share is
+// finished there; of the others each share leaves its part in the workspace, and a second kernel joins them.
 //
 // The rows of a pair are the tokens times the heads of the group.  For NR = 8 or 16 rows a warp computes, on the legacy
 // tensor path (operands from registers: the codes are converted there and never written back),
@@ -20,6 +20,7 @@
 // (ldmatrix.trans), as they lie; q and the output follow that order.  P crosses from one product's layout to the other's
 // by movmatrix.
 #include "attention.cuh"
+#include "mhc.h"
 #include "sm100_ptx.cuh"
 
 namespace mhc {
@@ -27,8 +28,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kMaxCtas = 192;     // partial results and counters in the workspace
-constexpr int kMaxRows = 64;      // rows of a CTA
+constexpr int kMaxCtas = 160;
 constexpr int kSlice = 32;        // tokens
 // p = 2^(s - m) with m set kHead (log2) below the largest score, and raised when a score is kHead + kLazy above it (few
 // rescales): p is at most 2^12, P' = p * 2^(scale - top + kGain) at most 2^15 (fp16 ends at 2^16).  p loses bits below
@@ -36,14 +36,15 @@ constexpr int kSlice = 32;        // tokens
 constexpr float kHead = 11.f, kLazy = 1.f;
 constexpr int kGain = 3;
 // What a pair costs besides its slices, in slices (its q, its join): 100-token sequences beside long ones.
-constexpr int kPairCost = 12;
+constexpr int kPairCost = 3;
 
-struct Partial {                  // of a CTA's share of a pair
-    float o[kMaxRows][128];
-    float m[kMaxRows], l[kMaxRows];
-};
-constexpr size_t kCounterBytes = 1024;  // kMaxCtas counters
-static_assert(kMaxCtas * 4 <= kCounterBytes, "");
+// The workspace after its control block: where each sequence begins on the line and the line's length (int64 [B + 1]), then
+// the parts, two for each share (of a pair that began in an earlier share, and of one that goes on in a later one): their
+// sums [row][D], and each row's maximum and sum.
+constexpr size_t kStartBytes = (MHC_MAX_SEQUENCES + 2) * 8;
+constexpr int kFewRows = 1024;          // rows of a call up to which eight warps join one (of 1,824 parts and 8 to a pair's rows, 8 each)
+constexpr int kMaxUnitRows = 128;       // rows of all shares of a CTA
+constexpr size_t kPartFloats = 128 + 2;
 
 template <int D, int NR_, int WR_, int NW_, int ST_>
 struct Cfg {
@@ -52,13 +53,22 @@ struct Cfg {
     static constexpr int kSliceBytes = 2 * CacheLayout<D>::kGroupBytes;
     static constexpr int kRing = WT * ST * kSliceBytes;
     static constexpr int kScale = NW * kSlice * NB * 6;            // a slice's scales, K's in fp32, V's in fp16: a warp's own
-    static constexpr int kJoin = NW * NR * 32 * 4;                 // 32 values of every warp's rows; weights of parts
-    static_assert(kJoin >= NW * kMaxCtas * 4, "");
-    static constexpr int kQ = NR == 16 ? WR * (D / 16) * 32 * 16 : 0;   // q's fragments
-    static constexpr int kStats = 3 * NW * NR * 4 + WT * ST * 4 + 256;
-    static constexpr int kSmem = kRing + kScale + kJoin + kQ + kStats;
-    static_assert(kSmem <= 232448, "");
+    static constexpr int kQ = NR == 16 ? NW * (D / 16) * 32 * 16 : 0;   // q's fragments
+    static constexpr int kSmem = kRing + kScale + kQ + WT * ST * 4;
+    static_assert(kSmem <= 231000 && WT * ROWS <= kMaxUnitRows, "");
 };
+
+// The parts of a launch.
+struct Parts {
+    int64_t *start;       // [B + 1]
+    float *o, *ml;        // [2 * units][rows][D], [2 * units][rows][2]
+};
+template <int D, class C>
+__host__ __device__ __forceinline__ Parts parts_of(unsigned int *ctrl, int ctas) {
+    uint8_t *p = reinterpret_cast<uint8_t *>(ctrl) + kControlBytes;
+    float *o = reinterpret_cast<float *>(p + kStartBytes);
+    return {reinterpret_cast<int64_t *>(p), o, o + (size_t)2 * ctas * C::WT * C::ROWS * D};
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -142,6 +152,9 @@ __device__ __forceinline__ Seq sequence(const DecodeArgs &a, int rows, int b) {
 // On the line a pair is kPairCost places, then its slices.
 __device__ __forceinline__ int64_t cost(const DecodeArgs &a, const Seq &s) { return (int64_t)a.c.heads * s.tiles * (s.slices + kPairCost); }
 
+// A share's length: at least two places.
+__device__ __forceinline__ int64_t share_of(int64_t total, int64_t units) { return max((int64_t)2, (total + units - 1) / units); }
+
 // A block's exclusive sum; `total` the whole.  Two syncs; `scratch` 33 words.
 template <int NT>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t &total, int64_t *scratch) {
@@ -163,30 +176,6 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t &total, int64_t
     __syncthreads();
     total = all;
     return before + x - v;
-}
-
-// 32 values of one head's row, one a lane (block `blk` of the head).
-__device__ __forceinline__ void write_block(const AttnOut &o, int D, int64_t t, int head, int blk, float v) {
-    const int lane = threadIdx.x & 31;
-    const int64_t at = (t * o.heads + head) * (int64_t)D + blk * 32 + lane;
-    if (o.out != nullptr) o.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-    if (o.mx.q != nullptr) {
-        float amax = fabsf(v);
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-        const int E = mx_exp(amax, o.mx.mode);
-        o.mx.q[at] = (uint8_t)__nv_cvt_float_to_fp8(v * __uint_as_float((uint32_t)(127 - E) << 23), __NV_SATFINITE, __NV_E4M3);
-        if (lane == 0) o.mx.scale[mx_scale_offset(t, head * (D / 32) + blk, o.heads * D)] = (uint8_t)(E + 127);
-    }
-}
-// The row's result from its sums: what sees nothing gives zeros and -inf.
-__device__ __forceinline__ void finish_block(const DecodeArgs &a, const Seq &q, int head, int r, int blk, float o, float m, float l) {
-    const int G = a.q_heads / a.c.heads, i = r / G;
-    const bool sees = q.len - q.n + i >= 0;
-    const int64_t t = q.begin + i;
-    const int hq = head * G + r % G;
-    write_block(a.o, a.D, t, hq, blk, sees ? o / l : 0.f);
-    if (blk == 0 && a.o.lse != nullptr && (threadIdx.x & 31) == 0) a.o.lse[t * a.o.heads + hq] = sees ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 template <int D, class C>
@@ -424,65 +413,79 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *ring = smem;
     float *scale = reinterpret_cast<float *>(smem + C::kRing);
-    float *join = reinterpret_cast<float *>(smem + C::kRing + C::kScale);
-    uint4 *sq = reinterpret_cast<uint4 *>(smem + C::kRing + C::kScale + C::kJoin);
-    float *st_m = reinterpret_cast<float *>(smem + C::kRing + C::kScale + C::kJoin + C::kQ);
-    float *st_l = st_m + C::NW * NR;
-    float *st_a = st_l + C::NW * NR;                                   // (joined maximum and sum of each row)
-    uint32_t *bad_pages = reinterpret_cast<uint32_t *>(st_a + C::NW * NR);
+    uint4 *sq = reinterpret_cast<uint4 *>(smem + C::kRing + C::kScale);
+    uint32_t *bad_pages = reinterpret_cast<uint32_t *>(smem + C::kRing + C::kScale + C::kQ);
     __shared__ int64_t scan[34];
-    __shared__ int64_t found[2];
-    __shared__ int arrived;
+    __shared__ int64_t found[WT][2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
-    const int wt = warp / WR, wr = warp % WR;                          // which slices, which rows
+    const int wt = warp / WR, wr = warp % WR;                          // which share, which rows
     const int G = a.q_heads / a.c.heads;
+    const int unit = (int)blockIdx.x * WT + wt;
+    const Parts parts = parts_of<D, C>(a.ctrl, gridDim.x);
+    asm volatile("griddepcontrol.launch_dependents;");                 // (the second kernel waits for all of this one)
 
-    // ---- this CTA's share of the line
+    // ---- the shares of the line
     int64_t total = 0;
     for (int base = 0; base < a.c.B; base += NT) {
         int64_t all;
         block_scan<NT>(base + tid < a.c.B ? cost(a, sequence(a, C::ROWS, base + tid)) : 0, all, scan);
         total += all;
     }
-    const int64_t share = max((int64_t)WT, (total + gridDim.x - 1) / gridDim.x);
-    int64_t at = share * blockIdx.x;
-    const int64_t end = min(total, at + share);
-    if (at >= end) return;
-    for (int64_t base = 0, before = 0; base < a.c.B; base += NT) {
-        int64_t all;
-        const int64_t c = base + tid < a.c.B ? cost(a, sequence(a, C::ROWS, (int)base + tid)) : 0;
-        const int64_t mine = before + block_scan<NT>(c, all, scan);
-        if (at >= mine && at < mine + c) {
-            found[0] = base + tid;
-            found[1] = at - mine;
+    const int64_t share = share_of(total, (int64_t)gridDim.x * WT);
+    {
+        const int64_t first = share * blockIdx.x * WT;
+        int64_t before = 0;
+        for (int64_t base = 0; base < a.c.B; base += NT) {
+            int64_t all;
+            const int64_t c = base + tid < a.c.B ? cost(a, sequence(a, C::ROWS, (int)base + tid)) : 0;
+            const int64_t mine = before + block_scan<NT>(c, all, scan);
+            for (int w = 0; w < WT; ++w)
+                if (first + w * share >= mine && first + w * share < mine + c) {
+                    found[w][0] = base + tid;
+                    found[w][1] = first + w * share - mine;
+                }
+            if (blockIdx.x == 0 && base + tid < a.c.B) parts.start[base + tid] = mine;
+            before += all;
         }
-        before += all;
-        if (at < before) break;
+        if (blockIdx.x == 0 && tid == 0) parts.start[a.c.B] = before;
     }
     __syncthreads();
-    int b = (int)found[0];
-    Seq seq = sequence(a, C::ROWS, b);
-    int pair = (int)(found[1] / (seq.slices + kPairCost));                          // (head, row tile)
-    int s0 = (int)(found[1] % (seq.slices + kPairCost)) - kPairCost;                // first slice; below 0: the pair's own cost
+    int64_t at = share * unit;
+    const int64_t end = min(total, at + share);
+    if (at >= end) return;
+    // (from here on no barrier of the CTA)
 
-    // ---- the ring: slice k of this warp group's in the current pair is slice s0 + wt + k * WT of it
-    uint32_t put = 0, got = 0;                                         // slices copied to and taken from the ring
-    int page_cur[2] = {-1, -1}, page_next[2] = {-1, -1};                                     // pages of slices k0 + lane, and of the 32 after
-    int copied = 0;                                                    // slices of this pair whose copy was started
-    int n_mine = 0, head = 0, s_first = 0, limit = 0;
-    auto pages_of = [&](int k, int (&p)[2]) {
-        const int64_t t0 = ((int64_t)s_first + wt + (int64_t)k * WT) * kSlice;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) p[i] = k < n_mine && t0 + 16 * i < limit ? cache_page(a.c, b, t0 + 16 * i) : -1;
+    // ---- a pair, and a share's part of it
+    struct Pair {
+        Seq seq;
+        int b, pair;             // sequence; head * tiles + row tile
+        int s0, count;           // first place (slices from 0; below 0: the pair's own cost), places in this share
+        int first, n, limit;     // first slice and number of slices; tokens up to the last
     };
-    auto copy = [&]() {  // starts the next slice's copy, or an empty group
-        if (copied < n_mine) {
+    auto part_of = [&](Pair &p, int64_t left) {
+        p.count = (int)min((int64_t)(p.seq.slices - p.s0), left);
+        p.first = max(p.s0, 0);
+        p.n = max(0, p.s0 + p.count - p.first);
+        p.limit = min(p.seq.len, (p.first + p.n) * kSlice);
+    };
+    auto pages_of = [&](const Pair &p, int k, int (&page)[2]) {  // of slice k of the part, a slice a lane
+        const int64_t t0 = (int64_t)(p.first + k) * kSlice;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) page[i] = k < p.n && t0 + 16 * i < p.limit ? cache_page(a.c, p.b, t0 + 16 * i) : -1;
+    };
+
+    // ---- the ring
+    uint32_t put = 0, got = 0;                                         // slices copied to and taken from it
+    int page_cur[2], page_next[2], page_look[2] = {-1, -1};            // pages of slices k0 + lane, the 32 after, and the next pair's
+    int copied = 0;                                                    // slices of this part whose copy was started
+    auto copy = [&](const Pair &p) {  // starts the next slice's copy, or an empty group
+        if (copied < p.n) {
             if ((copied & 31) == 0 && copied > 0) {
                 page_cur[0] = page_next[0];
                 page_cur[1] = page_next[1];
-                pages_of(copied + 32 + lane, page_next);
+                pages_of(p, copied + 32 + lane, page_next);
             }
-            const int t0 = (s_first + wt + copied * WT) * kSlice;
+            const int t0 = (p.first + copied) * kSlice, head = p.pair / p.seq.tiles;
             const int stage = wt * ST + put % ST;
             const int p0 = __shfl_sync(0xffffffffu, page_cur[0], copied & 31), p1 = __shfl_sync(0xffffffffu, page_cur[1], copied & 31);
             constexpr int kChunks = L::kGroupBytes / 16, kRound = kChunks / 32 * 32;   // whole warps' rounds, then both groups' rest
@@ -512,35 +515,50 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
         else named_sync(1 + wt, 32 * WR);
     };
     uint4 qw[NTL][NB];                                                 // q of the lane's rows, 8 values of each block
-    auto start_pair = [&](int64_t left) {  // the share's part of pair `pair` from place s0 on, `left` places of the share to go
-        head = pair / seq.tiles;
-        const int count = (int)min((int64_t)(seq.slices - s0), left);
-        s_first = max(s0, 0);
-        const int s_end = s0 + count;
-        limit = min(seq.len, max(0, s_end) * kSlice);
-        n_mine = s_end - s_first > wt ? (s_end - s_first - wt + WT - 1) / WT : 0;
-        copied = 0;
-        pages_of(lane, page_cur);
-        pages_of(32 + lane, page_next);
-        const int row0 = (pair % seq.tiles) * C::ROWS, rows = min(C::ROWS, seq.n * G - row0);
+    auto load_q = [&](const Pair &p) {
+        const int row0 = (p.pair % p.seq.tiles) * C::ROWS, rows = min(C::ROWS, p.seq.n * G - row0), head = p.pair / p.seq.tiles;
 #pragma unroll
         for (int r = 0; r < NTL; ++r) {
             const int row = wr * NR + r * 8 + g4, i = (row0 + row) / G;
-            const uint16_t *p = a.q + (seq.begin + i) * a.q_stride + (head * G + (row0 + row) % G) * D + t4 * 8;
+            const uint16_t *x = a.q + (p.seq.begin + i) * a.q_stride + (head * G + (row0 + row) % G) * D + t4 * 8;
 #pragma unroll
-            for (int k = 0; k < NB; ++k) qw[r][k] = row < rows ? __ldg(reinterpret_cast<const uint4 *>(p + k * 32)) : make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < NB; ++k) qw[r][k] = row < rows ? __ldg(reinterpret_cast<const uint4 *>(x + k * 32)) : make_uint4(0, 0, 0, 0);
         }
+    };
+    auto begin = [&](const Pair &p) {  // its pages known (page_cur)
+        copied = 0;
+        pages_of(p, 32 + lane, page_next);
+        if constexpr (NTL == 1) load_q(p);
 #pragma unroll
-        for (int i = 0; i < ST - 1; ++i) copy();
-        return count;
+        for (int i = 0; i < ST - 1; ++i) copy(p);
     };
 
-    int count = start_pair(end - at);
+    Pair cur;
+    cur.b = (int)found[wt][0];
+    cur.seq = sequence(a, C::ROWS, cur.b);
+    cur.pair = (int)(found[wt][1] / (cur.seq.slices + kPairCost));
+    cur.s0 = (int)(found[wt][1] % (cur.seq.slices + kPairCost)) - kPairCost;
+    part_of(cur, end - at);
+    pages_of(cur, lane, page_cur);
+    begin(cur);
     while (true) {
-        const int row0 = (pair % seq.tiles) * C::ROWS, rows = min(C::ROWS, seq.n * G - row0);
-        const int cur_head = head, cur_s0 = s0, cur_first = s_first;
-        const Seq cur = seq;
+        // ---- what comes next, ahead of its use
+        at += cur.count;
+        const bool more = at < end;
+        Pair next = cur;
+        if (more) {
+            next.s0 = -kPairCost;
+            if (++next.pair == a.c.heads * next.seq.tiles) {
+                next.pair = 0;
+                do next.seq = sequence(a, C::ROWS, ++next.b);
+                while (next.seq.n == 0);
+            }
+            part_of(next, end - at);
+            pages_of(next, lane, page_look);
+        }
+        const int row0 = (cur.pair % cur.seq.tiles) * C::ROWS, rows = min(C::ROWS, cur.seq.n * G - row0), head = cur.pair / cur.seq.tiles;
         // ---- q: row lane / 4 (+ 8) as B fragments, scaled by a power of two to at most 2^4
+        if constexpr (NTL == 2) load_q(cur);
         uint32_t q[NB][2][NTL * 2];
         float f[NTL][2];
         int vis[NTL][2], vis_g[NTL];
@@ -548,7 +566,7 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
 #pragma unroll
         for (int r = 0; r < NTL; ++r) {
             const int row = wr * NR + r * 8 + g4;
-            vis_g[r] = row < rows ? max(0, cur.len - cur.n + (row0 + row) / G + 1) : 0;
+            vis_g[r] = row < rows ? max(0, cur.seq.len - cur.seq.n + (row0 + row) / G + 1) : 0;
             seen = min(seen, row < rows ? vis_g[r] : 0x7fffffff);
             float x[NB][8], amax = 0.f;
 #pragma unroll
@@ -576,15 +594,13 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
         }
         seen = __reduce_min_sync(0xffffffffu, seen);
         if constexpr (NTL == 2) {
-            if (wt == 0) {
 #pragma unroll
-                for (int k = 0; k < NB; ++k)
+            for (int k = 0; k < NB; ++k)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        sq[wr * (NB * 2 * 32) + (k * 2 + h) * 32 + lane] = make_uint4(q[k][h][0], q[k][h][1], q[k][h][2], q[k][h][3]);
-            }
-            __syncthreads();
+                for (int h = 0; h < 2; ++h) sq[(warp * NB * 2 + k * 2 + h) * 32 + lane] = make_uint4(q[k][h][0], q[k][h][1], q[k][h][2], q[k][h][3]);
+            __syncwarp();
         }
+
         Warp<D, C> w;
 #pragma unroll
         for (int k = 0; k < NB; ++k)
@@ -600,132 +616,166 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             for (int e = 0; e < 2; ++e) w.m[r][e] = -INFINITY, w.l[r][e] = 0.f;
         w.top = 0;
 
-        const int n_now = n_mine;
-        for (int k = 0; k < n_now; ++k) {
+        for (int k = 0; k < cur.n; ++k) {
             cp_wait<ST - 2>();
             group_sync();                                              // slice k is there for all, and k - 1 is done with
-            copy();
+            copy(cur);
             const int stage = wt * ST + got % ST;
             ++got;
-            const int tok0 = (cur_first + wt + k * WT) * kSlice;
+            const int tok0 = (cur.first + k) * kSlice;
             const uint32_t base = smem_u32(ring + stage * C::kSliceBytes), bad = bad_pages[stage];
             float *sk = scale + warp * (kSlice * NB * 3 / 2);
             uint32_t *sv = reinterpret_cast<uint32_t *>(sk + kSlice * NB);
             if (tok0 + kSlice <= seen && bad == 0)
-                slice<D, C, false>(w, base, q, sq + wr * (NB * 2 * 32), sk, sv, tok0, cur.len, bad, f, vis, vis_g);
+                slice<D, C, false>(w, base, q, sq + warp * (NB * 2 * 32), sk, sv, tok0, cur.seq.len, bad, f, vis, vis_g);
             else
-                slice<D, C, true>(w, base, q, sq + wr * (NB * 2 * 32), sk, sv, tok0, cur.len, bad, f, vis, vis_g);
+                slice<D, C, true>(w, base, q, sq + warp * (NB * 2 * 32), sk, sv, tok0, cur.seq.len, bad, f, vis, vis_g);
             __syncwarp();                                              // (the scales are written anew)
         }
-        // ---- the next pair's first copies run while this one is joined
-        at += count;
-        const bool more = at < end, whole = cur_s0 == -kPairCost && cur_s0 + count == cur.slices;
-        const int64_t pair_begin = at - count - (cur_s0 + kPairCost);  // on the line
         group_sync();                                                  // (every warp of the group has read its last slice)
+        // ---- the next pair's first copies run while this one is written
         if (more) {
-            s0 = -kPairCost;
-            if (++pair == a.c.heads * seq.tiles) {
-                pair = 0;
-                do seq = sequence(a, C::ROWS, ++b);
-                while (seq.n == 0);
-            }
-            count = start_pair(end - at);
+            page_cur[0] = page_look[0];
+            page_cur[1] = page_look[1];
+            begin(next);
         }
-        // ---- the warps' states are joined: rows' maxima and sums first
+        const bool whole = cur.s0 == -kPairCost && cur.s0 + cur.count == cur.seq.slices;
+        const float units = ex2((float)((int)w.top - 127 - kGain));
+        const int slot = 2 * unit + (cur.s0 == -kPairCost ? 1 : 0);
 #pragma unroll
         for (int r = 0; r < NTL; ++r)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < 2; ++e) {  // row 8 r + 2 t4 + e, values 32 k + 4 g4 ..
                 const float l = column_sum(w.l[r][e]);
-                if (g4 == 0) {
-                    st_m[warp * NR + r * 8 + 2 * t4 + e] = w.m[r][e];
-                    st_l[warp * NR + r * 8 + 2 * t4 + e] = l;
-                }
-            }
-        __syncthreads();
-        if (tid < C::ROWS) {  // row tid: warps with wr == tid / NR
-            float m = -INFINITY, l = 0.f;
-            for (int x = 0; x < WT; ++x) m = fmaxf(m, st_m[(x * WR + tid / NR) * NR + tid % NR]);
-            for (int x = 0; x < WT; ++x) {
-                const float mx = st_m[(x * WR + tid / NR) * NR + tid % NR];
-                l = fmaf(st_l[(x * WR + tid / NR) * NR + tid % NR], mx == -INFINITY ? 0.f : ex2(mx - m), l);
-            }
-            st_a[tid] = m;
-            st_a[C::ROWS + tid] = l;
-        }
-        static_assert(2 * C::ROWS <= C::NW * NR, "");
-        __syncthreads();
-        float al[NTL][2];
-        const float unit = ex2((float)((int)w.top - 127 - kGain));
+                const int row = wr * NR + r * 8 + 2 * t4 + e;
+                const bool on = row < rows;
+                if (!whole) {
+                    float *o = parts.o + ((size_t)slot * C::ROWS + row) * D + 4 * g4;
+                    if (on) {
 #pragma unroll
-        for (int r = 0; r < NTL; ++r)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                al[r][e] = w.m[r][e] == -INFINITY ? 0.f : ex2(w.m[r][e] - st_a[wr * NR + r * 8 + 2 * t4 + e]) * unit;
-            }
-        Partial *part = reinterpret_cast<Partial *>(reinterpret_cast<uint8_t *>(a.ctrl) + kControlBytes + kCounterBytes);
-        const int slot = 2 * (int)blockIdx.x + (cur_s0 == -kPairCost ? 1 : 0);
-#pragma unroll
-        for (int k = 0; k < NB; ++k) {
-#pragma unroll
-            for (int r = 0; r < NTL; ++r)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)  // values 4 g4 .. of rows 8r + 2 t4 + e
-                    *reinterpret_cast<float4 *>(join + (warp * NR + r * 8 + 2 * t4 + e) * 32 + 4 * g4) =
-                        make_float4(w.o[k][0][r][e] * al[r][e], w.o[k][0][r][2 + e] * al[r][e], w.o[k][1][r][e] * al[r][e], w.o[k][1][r][2 + e] * al[r][e]);
-            __syncthreads();
-            for (int row = warp; row < rows; row += C::NW) {
-                float o = 0.f;
-#pragma unroll
-                for (int x = 0; x < WT; ++x) o += join[((x * WR + row / NR) * NR + row % NR) * 32 + lane];
-                if (whole) finish_block(a, cur, cur_head, row0 + row, k, o, st_a[row], st_a[C::ROWS + row]);
-                else part[slot].o[row][k * 32 + lane] = o;
-            }
-            __syncthreads();
-        }
-        // ---- a pair that is cut: the CTA that arrives last joins the parts in order
-        if (!whole) {
-            if (tid < rows) {
-                part[slot].m[tid] = st_a[tid];
-                part[slot].l[tid] = st_a[C::ROWS + tid];
-            }
-            __threadfence();
-            __syncthreads();
-            const int c0 = (int)(pair_begin / share), c1 = (int)((pair_begin + kPairCost + cur.slices - 1) / share);
-            unsigned int *counter = a.ctrl + kControlBytes / 4 + c0;   // one pair at most begins in c0 and goes on
-            if (tid == 0) {
-                const unsigned int before = atomicAdd(counter, 1u);
-                arrived = before == (unsigned)(c1 - c0);
-                if (arrived) *counter = 0;                             // (ready for the next call)
-            }
-            __syncthreads();
-            if (arrived) {
-                __threadfence();
-                float *weight = join + warp * kMaxCtas;
-                for (int task = warp; task < rows * NB; task += C::NW) {
-                    const int row = task / NB, k = task % NB;
-                    float m = -INFINITY, l = 0.f, o = 0.f;
-                    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, __ldcg(&part[2 * c + (c == c0)].m[row]));
-#pragma unroll
-                    for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-                    for (int c = c0 + lane; c <= c1; c += 32) {
-                        const float mc = __ldcg(&part[2 * c + (c == c0)].m[row]), x = mc == -INFINITY ? 0.f : ex2(mc - m);
-                        weight[c - c0] = x;
-                        l = fmaf(__ldcg(&part[2 * c + (c == c0)].l[row]), x, l);
+                        for (int k = 0; k < NB; ++k)
+                            *reinterpret_cast<float4 *>(o + 32 * k) =
+                                make_float4(w.o[k][0][r][e] * units, w.o[k][0][r][2 + e] * units, w.o[k][1][r][e] * units, w.o[k][1][r][2 + e] * units);
+                        if (g4 == 0) *reinterpret_cast<float2 *>(parts.ml + ((size_t)slot * C::ROWS + row) * 2) = make_float2(w.m[r][e], l);
                     }
-                    l = warp_sum(l);
-                    __syncwarp();
-#pragma unroll 8
-                    for (int c = c0; c <= c1; ++c) o = fmaf(__ldcg(&part[2 * c + (c == c0)].o[row][k * 32 + lane]), weight[c - c0], o);
-                    finish_block(a, cur, cur_head, row0 + row, k, o, m, l);
-                    __syncwarp();
+                    continue;
                 }
-                __syncthreads();
+                const int i = (row0 + row) / G, hq = head * G + (row0 + row) % G;
+                const bool sees = cur.seq.len - cur.seq.n + i >= 0;    // what sees nothing gives zeros and -inf
+                const int64_t t = cur.seq.begin + i;
+                const float inv = units / l;                           // (keys whose scores are all -inf: NaN, 0 * inf)
+#pragma unroll
+                for (int k = 0; k < NB; ++k) {
+                    float v[4] = {w.o[k][0][r][e] * inv, w.o[k][0][r][2 + e] * inv, w.o[k][1][r][e] * inv, w.o[k][1][r][2 + e] * inv};
+                    if (!sees) v[0] = v[1] = v[2] = v[3] = 0.f;
+                    const int64_t o = (t * a.q_heads + hq) * (int64_t)D + 32 * k + 4 * g4;
+                    if (on && a.o.out != nullptr) *reinterpret_cast<uint2 *>(a.o.out + o) = make_uint2(pack2_rn(v[0], v[1]), pack2_rn(v[2], v[3]));
+                    if (a.o.mx.q != nullptr) {
+                        const float amax = column_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
+                        const int E = mx_exp(amax, a.o.mx.mode);
+                        const float m = __uint_as_float((uint32_t)(127 - E) << 23);
+                        if (on) {
+                            *reinterpret_cast<uint32_t *>(a.o.mx.q + o) =
+                                (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[0] * m, v[1] * m), __NV_SATFINITE, __NV_E4M3) |
+                                (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[2] * m, v[3] * m), __NV_SATFINITE, __NV_E4M3) << 16;
+                            if (g4 == 0) a.o.mx.scale[mx_scale_offset(t, hq * NB + k, a.q_heads * D)] = (uint8_t)(E + 127);
+                        }
+                    }
+                }
+                if (on && g4 == 0 && a.o.lse != nullptr) a.o.lse[t * a.q_heads + hq] = sees ? (w.m[r][e] + log2f(l)) * kLn2 : -INFINITY;
             }
-        }
         if (!more) break;
+        cur = next;
     }
     cp_wait<0>();
+}
+
+// Joins the parts of the pairs that were cut: kWarps warps a row (token, q head), each a run of the parts, eight loads in
+// flight.  The order is fixed by the lengths alone.
+template <int D, class C, int kWarps>
+__global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) join_kernel(const __grid_constant__ DecodeArgs a, int ctas) {
+    constexpr int N = D / 32, kRows = kWarps == 1 ? 4 : 1;
+    const int lane = threadIdx.x & 31, warp = kWarps == 1 ? 0 : threadIdx.x >> 5;
+    const int64_t item = (int64_t)blockIdx.x * kRows + (kWarps == 1 ? threadIdx.x >> 5 : 0);
+    const int64_t t = item / a.q_heads;
+    const int hq = (int)(item % a.q_heads), G = a.q_heads / a.c.heads;
+    SeqOfRow s{-1, 0, 0};
+    Seq seq{};
+    if (t < a.T) s = find_sequence(a.c.offsets, a.c.B, t, a.T);
+    if (s.b >= 0) seq = sequence(a, C::ROWS, s.b);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (s.b < 0) return;
+    const Parts parts = parts_of<D, C>(a.ctrl, ctas);
+    const int64_t start = __ldcg(parts.start + s.b), share = share_of(__ldcg(parts.start + a.c.B), (int64_t)ctas * C::WT);
+    const int r = (int)(t - s.begin) * G + hq % G, row = r % C::ROWS;
+    const int64_t place = start + (int64_t)((hq / G) * seq.tiles + r / C::ROWS) * (seq.slices + kPairCost);
+    const int u0 = (int)(place / share), u1 = (int)((place + seq.slices + kPairCost - 1) / share);
+    if (u0 == u1) return;  // not cut (the same for all warps of a row)
+    auto at = [&](int u) { return (size_t)(2 * u + (u == u0 ? 1 : 0)) * C::ROWS + row; };
+    const int per = (u1 - u0 + kWarps) / kWarps, lo = u0 + warp * per, hi = min(u1 + 1, lo + per);   // this warp's parts
+    float m = -INFINITY, l = 0.f, o[N] = {};
+    for (int base = lo; base < hi; base += 32) {
+        const float2 ml = base + lane < hi ? __ldcg(reinterpret_cast<const float2 *>(parts.ml + at(base + lane) * 2)) : make_float2(-INFINITY, 0.f);
+        float top = ml.x;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        top = fmaxf(top, m);
+        const float old = m == -INFINITY ? 0.f : ex2(m - top), weight = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+        m = top;
+        l = fmaf(ml.y, weight, l * old);
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] *= old;
+        const int n = min(32, hi - base);
+        for (int j = 0; j < n; j += 8) {
+            float v[8][N];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float *p = parts.o + at(min(base + j + i, hi - 1)) * D + lane * N;
+                if constexpr (N == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(p));
+                    v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
+                } else {
+                    const float2 x = __ldcg(reinterpret_cast<const float2 *>(p));
+                    v[i][0] = x.x; v[i][1] = x.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float x = __shfl_sync(0xffffffffu, weight, (j + i) & 31);
+#pragma unroll
+                for (int e = 0; e < N; ++e) o[e] = j + i < n ? fmaf(v[i][e], x, o[e]) : o[e];
+            }
+        }
+    }
+    l = warp_sum(l);
+    if constexpr (kWarps > 1) {
+        __shared__ float so[kWarps][D], sm[kWarps], sl[kWarps];
+#pragma unroll
+        for (int i = 0; i < N; ++i) so[warp][lane * N + i] = o[i];
+        if (lane == 0) {
+            sm[warp] = m;
+            sl[warp] = l;
+        }
+        __syncthreads();
+        if (warp != 0) return;
+        m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm[w]);
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float x = sm[w] == -INFINITY ? 0.f : ex2(sm[w] - m);
+            l = fmaf(sl[w], x, l);
+#pragma unroll
+            for (int i = 0; i < N; ++i) o[i] = fmaf(so[w][lane * N + i], x, o[i]);
+        }
+    }
+    const bool sees = seq.len - seq.n + (int)(t - s.begin) >= 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = sees ? o[i] / l : 0.f;
+    write_head_row<D>(a.o, t, hq, o, sees ? (m + log2f(l)) * kLn2 : -INFINITY);
 }
 
 template <int D, class C>
@@ -733,25 +783,42 @@ cudaError_t launch_one(const DecodeArgs &a, int num_sms, cudaStream_t stream) {
     auto kern = decode_kernel<D, C>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
+    const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
     mark_main_kernel(stream, true);
-    kern<<<num_sms < kMaxCtas ? num_sms : kMaxCtas, C::NT, C::kSmem, stream>>>(a);
+    kern<<<ctas, C::NT, C::kSmem, stream>>>(a);
     mark_main_kernel(stream, false);
-    return cudaGetLastError();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its prologue runs beside the first kernel's end
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // Few rows have many parts each: eight warps a row.
+    if (a.T * a.q_heads <= kFewRows) {
+        cfg.gridDim = dim3((unsigned)(a.T * a.q_heads));
+        cfg.blockDim = dim3(256);
+        return cudaLaunchKernelEx(&cfg, join_kernel<D, C, 8>, a, ctas);
+    }
+    cfg.gridDim = dim3((unsigned)((a.T * a.q_heads + 3) / 4));
+    cfg.blockDim = dim3(128);
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, C, 1>, a, ctas);
 }
 
 // By the rows of an average sequence: as few row tiles as there can be, and no more rows than are needed.
 template <int D>
 cudaError_t launch_rows(const DecodeArgs &a, int num_sms, cudaStream_t stream) {
     const int64_t rows = (a.T + a.c.B - 1) / a.c.B * (a.q_heads / a.c.heads);
-    if (rows <= 8) return launch_one<D, Cfg<D, 8, 1, 12, 3>>(a, num_sms, stream);
-    if (rows <= 16) return launch_one<D, Cfg<D, 16, 1, 12, 3>>(a, num_sms, stream);
-    if (rows <= 32) return launch_one<D, Cfg<D, 16, 2, 12, 3>>(a, num_sms, stream);
-    return launch_one<D, Cfg<D, 16, 4, 12, 3>>(a, num_sms, stream);
+    if (rows <= 8) return launch_one<D, Cfg<D, 8, 1, 12, 4>>(a, num_sms, stream);
+    if (rows <= 16) return launch_one<D, Cfg<D, 16, 1, 8, 4>>(a, num_sms, stream);
+    if (rows <= 32) return launch_one<D, Cfg<D, 16, 2, 8, 4>>(a, num_sms, stream);
+    return launch_one<D, Cfg<D, 16, 4, 8, 4>>(a, num_sms, stream);
 }
 
 }  // namespace
 
-size_t decode_workspace_bytes() { return kControlBytes + kCounterBytes + 2 * kMaxCtas * sizeof(Partial); }
+size_t decode_workspace_bytes() { return kControlBytes + kStartBytes + (size_t)2 * kMaxCtas * kMaxUnitRows * kPartFloats * 4; }
 
 cudaError_t launch_decode(const DecodeArgs &a, int num_sms, cudaStream_t stream) {
     return a.D == 128 ? launch_rows<128>(a, num_sms, stream) : launch_rows<64>(a, num_sms, stream);

@@ -1037,7 +1037,7 @@ mhc_status mhc_decode_attention_mxfp4(const mhc_bf16 *q, int64_t q_stride, int64
                       static_cast<unsigned int *>(workspace)};
     const cudaError_t e = mhc::launch_decode(a, dev.sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
-    g_launches = 1;
+    g_launches = 2;
     return MHC_OK;
 }
 
