@@ -54,7 +54,7 @@ struct Cfg {
     static constexpr int kRing = WT * ST * kSliceBytes;
     static constexpr int kScale = NW * kSlice * NB * 6;            // a slice's scales, K's in fp32, V's in fp16: a warp's own
     static constexpr int kQ = NR == 16 ? NW * (D / 16) * 32 * 16 : 0;   // q's fragments
-    static constexpr int kSmem = kRing + kScale + kQ + WT * ST * 4;
+    static constexpr int kSmem = kRing + kScale + kQ;
     static_assert(kSmem <= 231000 && WT * ROWS <= kMaxUnitRows, "");
 };
 
@@ -78,14 +78,15 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+template <bool kTrans, int kAt>
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+    if constexpr (kTrans)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4 + %5];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr), "n"(kAt));
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4 + %5];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr), "n"(kAt));
 }
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -96,7 +97,7 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // of an 8 x 8 matrix of halves
     uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
     return d;
 }
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
@@ -124,6 +125,7 @@ __device__ __forceinline__ float2 ue8m0x2(uint32_t bytes) {
     asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.bf16x2.ue8m0x2 %0, t; }" : "=r"(d) : "r"(bytes));
     return make_float2(__uint_as_float(d << 16), __uint_as_float(d & 0xffff0000u));
 }
+constexpr uint32_t kNormal = 15 + kGain;   // scale bytes whose factor is a normal half: the largest one's exponent field
 // 2^(byte - top + kGain) as fp16 bits, byte <= top: zero below 2^-24, NaN for 255.
 __device__ __forceinline__ uint32_t v_scale(uint32_t byte, uint32_t top) {
     const int e = (int)byte - (int)top + 15 + kGain;
@@ -182,8 +184,37 @@ template <int D, class C>
 struct Warp {                              // a warp's running state
     float o[C::NB][2][C::NTILE][4];        // O^T: per 32 values two tiles of 16, per 8 rows
     float m[C::NTILE][2], l[C::NTILE][2];  // rows 2 (lane % 4) and the next: reference maximum, sum of the lane's own tokens
-    uint32_t top;                          // V's largest scale byte so far: o is in units of 2^(top - 127 - kGain)
+    uint32_t top, low;                     // V's largest scale byte so far: o is in units of 2^(top - 127 - kGain); the
+                                           // smallest whose factor is a normal half
 };
+
+// 16 tokens' codes (half kHalf of a slice) of K or V (kPart): r0 the first 8 tokens', r1 the others', a block each.
+// codes: the slice's address and lane_codes().
+template <int D, int kPart, int kHalf>
+__device__ __forceinline__ void fetch(uint32_t codes, uint32_t (&r0)[D / 32], uint32_t (&r1)[D / 32]) {
+    using L = CacheLayout<D>;
+    constexpr int kAt = kHalf * L::kGroupBytes + kPart * L::kPart;
+    uint32_t r[4];
+    ldsm4<kPart == 1, kAt>(r, codes);
+    if constexpr (D == 128) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) r0[b] = r[b];
+        ldsm4<kPart == 1, kAt + 8 * L::kRow>(r, codes);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) r1[b] = r[b];
+    } else {
+        r0[0] = r[0]; r0[1] = r[1]; r1[0] = r[2]; r1[1] = r[3];
+    }
+}
+// Where a lane's row of such a load lies: matrices are the blocks of 8 tokens, or of 8 and the next 8 for D = 64 (rows 8
+// apart have the same chunk order).
+template <int D>
+__device__ __forceinline__ uint32_t lane_codes() {
+    using L = CacheLayout<D>;
+    const int lane = threadIdx.x & 31, mi = lane >> 3;
+    const int row = (lane & 7) + (D == 128 ? 0 : (mi >> 1) * 8), blk = D == 128 ? mi : mi & 1;
+    return row * L::kRow + (blk ^ L::swizzle(row)) * 16;
+}
 
 // A slice of 32 tokens from shared memory.  tok0: its first token; vis: tokens that rows 2 (lane % 4) and the next see,
 // vis_g: those that row lane / 4 sees; f: the factors of those rows' scores.
@@ -194,17 +225,18 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
     using L = CacheLayout<D>;
     constexpr int NB = C::NB, NTL = C::NTILE;
     const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
+    const uint32_t codes = base + lane_codes<D>();
     // ---- scales, a token a lane
-    uint32_t vw, vmax = 0;
+    uint32_t vw, v_hi, v_lo;   // V's scale bytes, the largest and the smallest of them
     {
         const uint32_t at = base + (lane >> 4) * L::kGroupBytes + L::kScales + (lane & 15) * NB;
         uint32_t kw;
         if constexpr (NB == 4) {
             asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(at));
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw) : "r"(at + L::kPart));
+            asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(vw) : "r"(at), "n"(L::kPart));
         } else {
             asm volatile("ld.shared.u16 %0, [%1];" : "=r"(kw) : "r"(at));
-            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(vw) : "r"(at + L::kPart));
+            asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=r"(vw) : "r"(at), "n"(L::kPart));
         }
         if constexpr (kMask) {
             if ((bad >> (lane >> 4)) & 1u) kw = vw = 0xffffffffu;   // no such page: NaN
@@ -214,44 +246,23 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
         if constexpr (NB == 4) {
             const float2 k23 = ue8m0x2(kw >> 16);
             *reinterpret_cast<float4 *>(sk + lane * 4) = make_float4(k01.x, k01.y, k23.x, k23.y);
+            const uint32_t even = vw & 0x00ff00ffu, odd = (vw >> 8) & 0x00ff00ffu, hi = __vmaxu2(even, odd), lo = __vminu2(even, odd);
+            v_hi = max(hi & 0xffffu, hi >> 16);
+            v_lo = min(lo & 0xffffu, lo >> 16);
         } else {
             *reinterpret_cast<float2 *>(sk + lane * 2) = k01;
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const uint32_t e = (vw >> (8 * b)) & 255u;
-            vmax = max(vmax, e == 255u ? 0u : e);
+            v_hi = max(vw & 255u, (vw >> 8) & 255u);
+            v_lo = min(vw & 255u, (vw >> 8) & 255u);
         }
         __syncwarp();
     }
-    // the codes of 8 tokens (n) and all blocks, or of 16 tokens (2 n') and both blocks for D = 64
-    auto codes_at = [&](int part, int i) {
-        const int mi = lane >> 3;
-        const int n = NB == 4 ? i : 2 * i + (mi >> 1), blk = NB == 4 ? mi : mi & 1;
-        const int row = (n & 1) * 8 + (lane & 7);
-        return base + (n >> 1) * L::kGroupBytes + part * L::kPart + row * L::kRow + ((blk ^ L::swizzle(row)) * 16);
-    };
-    // 16 tokens' codes: r0 the first 8, r1 the others, a block each
-    auto fetch = [&](int part, int h, uint32_t (&r0)[NB], uint32_t (&r1)[NB]) {
-        uint32_t r[4];
-        if constexpr (NB == 4) {
-            if (part == 0) ldsm4(r, codes_at(0, 2 * h)); else ldsm4t(r, codes_at(1, 2 * h));
-#pragma unroll
-            for (int b = 0; b < 4; ++b) r0[b] = r[b];
-            if (part == 0) ldsm4(r, codes_at(0, 2 * h + 1)); else ldsm4t(r, codes_at(1, 2 * h + 1));
-#pragma unroll
-            for (int b = 0; b < 4; ++b) r1[b] = r[b];
-        } else {
-            if (part == 0) ldsm4(r, codes_at(0, h)); else ldsm4t(r, codes_at(1, h));
-            r0[0] = r[0]; r0[1] = r[1]; r1[0] = r[2]; r1[1] = r[3];
-        }
-    };
     // ---- scores: s[h][r] holds tokens 16 h + g4 (and + 8) x rows 8 r + 2 t4 (and + 1)
     float s[2][NTL][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint32_t r0[NB], r1[NB];
-        fetch(0, h, r0, r1);
+        if (h == 0) fetch<D, 0, 0>(codes, r0, r1);
+        else fetch<D, 0, 1>(codes, r0, r1);
         float sc0[NB], sc1[NB];
 #pragma unroll
         for (int b = 0; b < NB; b += (NB == 4 ? 4 : 2)) {
@@ -292,7 +303,8 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
     }
     // ---- the running maximum
     float hi[NTL][2];
-    bool raise = vmax > w.top;
+    bool raise = v_hi > w.top || v_lo < w.low;
+    bool far = false;          // a V scale is NaN, or too far below the largest to be a normal half
 #pragma unroll
     for (int r = 0; r < NTL; ++r)
 #pragma unroll
@@ -309,7 +321,15 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
             raise |= hi[r][e] > w.m[r][e] + (kHead + kLazy);
         }
     if (__any_sync(0xffffffffu, raise)) {
-        const uint32_t top = max(w.top, __reduce_max_sync(0xffffffffu, vmax));
+        uint32_t mine = 0;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t e = (vw >> (8 * b)) & 255u;
+            mine = max(mine, e == 255u ? 0u : e);
+        }
+        const uint32_t top = max(w.top, __reduce_max_sync(0xffffffffu, mine));
+        w.low = max((int)top - (kNormal - 1), 0);
+        far = __any_sync(0xffffffffu, v_hi == 255u || v_lo < w.low);
         const float unit = ex2((float)((int)w.top - (int)top));
         w.top = top;
 #pragma unroll
@@ -334,10 +354,17 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
         const uint32_t other = __shfl_xor_sync(0xffffffffu, vw, 1);
         const uint32_t even = lane & 1 ? other : vw, odd = lane & 1 ? vw : other;
         uint32_t x[NB / 2];
+        if (far) {
 #pragma unroll
-        for (int i = 0; i < NB / 2; ++i) {   // an even lane writes the first half of the blocks, an odd one the second
-            const int sh = 8 * ((lane & 1) * (NB / 2) + i);
-            x[i] = v_scale((even >> sh) & 255u, w.top) | v_scale((odd >> sh) & 255u, w.top) << 16;
+            for (int i = 0; i < NB / 2; ++i) {   // an even lane writes the first half of the blocks, an odd one the second
+                const int sh = 8 * ((lane & 1) * (NB / 2) + i);
+                x[i] = v_scale((even >> sh) & 255u, w.top) | v_scale((odd >> sh) & 255u, w.top) << 16;
+            }
+        } else {  // the same for four bytes at once: each is top - kNormal + 1 .. top, its exponent field 1 .. kNormal
+            const uint32_t down = (w.top - kNormal) * 0x01010101u, fe = even - down, fo = odd - down;
+#pragma unroll
+            for (int i = 0; i < NB / 2; ++i)     // the two bytes to bits 8 and 24, then up by two: a half's exponent
+                x[i] = __byte_perm(fe, fo, lane & 1 ? (NB == 4 ? (i ? 0x7030 : 0x6020) : 0x5010) : (i ? 0x5010 : 0x4000)) << 2 & 0x7c007c00u;
         }
         if constexpr (NB == 4) *reinterpret_cast<uint2 *>(sv + (lane >> 1) * 4 + (lane & 1) * 2) = make_uint2(x[0], x[1]);
         else sv[(lane >> 1) * 2 + (lane & 1)] = x[0];
@@ -367,7 +394,8 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint32_t v0[NB], v1[NB];
-        fetch(1, h, v0, v1);
+        if (h == 0) fetch<D, 1, 0>(codes, v0, v1);
+        else fetch<D, 1, 1>(codes, v0, v1);
         uint32_t sc[2][NB];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -414,7 +442,6 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
     uint8_t *ring = smem;
     float *scale = reinterpret_cast<float *>(smem + C::kRing);
     uint4 *sq = reinterpret_cast<uint4 *>(smem + C::kRing + C::kScale);
-    uint32_t *bad_pages = reinterpret_cast<uint32_t *>(smem + C::kRing + C::kScale + C::kQ);
     __shared__ int64_t scan[34];
     __shared__ int64_t found[WT][2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
@@ -461,12 +488,14 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
         int b, pair;             // sequence; head * tiles + row tile
         int s0, count;           // first place (slices from 0; below 0: the pair's own cost), places in this share
         int first, n, limit;     // first slice and number of slices; tokens up to the last
+        const uint8_t *src;      // the head in page 0, the lane's 16 bytes
     };
     auto part_of = [&](Pair &p, int64_t left) {
         p.count = (int)min((int64_t)(p.seq.slices - p.s0), left);
         p.first = max(p.s0, 0);
         p.n = max(0, p.s0 + p.count - p.first);
         p.limit = min(p.seq.len, (p.first + p.n) * kSlice);
+        p.src = a.c.data + (int64_t)(p.pair / p.seq.tiles) * (a.c.page >> 4) * L::kGroupBytes + lane * 16;
     };
     auto pages_of = [&](const Pair &p, int k, int (&page)[2]) {  // of slice k of the part, a slice a lane
         const int64_t t0 = (int64_t)(p.first + k) * kSlice;
@@ -478,6 +507,8 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
     uint32_t put = 0, got = 0;                                         // slices copied to and taken from it
     int page_cur[2], page_next[2], page_look[2] = {-1, -1};            // pages of slices k0 + lane, the 32 after, and the next pair's
     int copied = 0;                                                    // slices of this part whose copy was started
+    uint32_t bad_pages = 0;                                            // two bits a copied slice, the last one's lowest
+    const int page_bytes = a.c.heads * (a.c.page >> 4) * L::kGroupBytes;
     auto copy = [&](const Pair &p) {  // starts the next slice's copy, or an empty group
         if (copied < p.n) {
             if ((copied & 31) == 0 && copied > 0) {
@@ -485,26 +516,30 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
                 page_cur[1] = page_next[1];
                 pages_of(p, copied + 32 + lane, page_next);
             }
-            const int t0 = (p.first + copied) * kSlice, head = p.pair / p.seq.tiles;
-            const int stage = wt * ST + put % ST;
+            const int t0 = (p.first + copied) * kSlice;
             const int p0 = __shfl_sync(0xffffffffu, page_cur[0], copied & 31), p1 = __shfl_sync(0xffffffffu, page_cur[1], copied & 31);
             constexpr int kChunks = L::kGroupBytes / 16, kRound = kChunks / 32 * 32;   // whole warps' rounds, then both groups' rest
-            const uint32_t dst = smem_u32(ring + stage * C::kSliceBytes) + lane * 16;
-            const uint8_t *src0 = a.c.data + cache_group<D>(a.c, max(p0, 0), head, (t0 & (a.c.page - 1)) >> 4) + lane * 16;
-            const uint8_t *src1 = a.c.data + cache_group<D>(a.c, max(p1, 0), head, ((t0 + 16) & (a.c.page - 1)) >> 4) + lane * 16;
             constexpr int kRest = kChunks - kRound;                                     // 8 or 4: lanes 0 .. for the first group, then the second
             static_assert(2 * kRest <= 32, "");
-            if (p0 >= 0) {
+            const uint32_t dst = smem_u32(ring + (wt * ST + put % ST) * C::kSliceBytes) + lane * 16;
+            const uint8_t *src0 = p.src + (int64_t)p0 * page_bytes + ((t0 & (a.c.page - 1)) >> 4) * L::kGroupBytes;
+            const uint8_t *src1 = p.src + (int64_t)p1 * page_bytes + (((t0 + 16) & (a.c.page - 1)) >> 4) * L::kGroupBytes;
+            bad_pages = bad_pages << 2 | (p0 < 0 ? 1u : 0u) | (p1 < 0 ? 2u : 0u);
+            if ((p0 | p1) >= 0) {
 #pragma unroll
-                for (int i = wr * 512; i < kRound * 16; i += WR * 512) cp_async16(dst + i, src0 + i);
+                for (int i = 0; i < kRound * 16; i += WR * 512) {
+                    const int o = i + wr * 512;
+                    if (WR * 512 > kRound * 16 && o >= kRound * 16) continue;   // (D = 64 has two rounds for four warps)
+                    cp_async16(dst + o, src0 + o);
+                    cp_async16(dst + o + L::kGroupBytes, src1 + o);
+                }
+                if (wr == 0 && lane < 2 * kRest)
+                    cp_async16(dst + kRound * 16 + (lane < kRest ? 0 : L::kGroupBytes - kRest * 16), (lane < kRest ? src0 : src1 - kRest * 16) + kRound * 16);
+            } else if (p0 >= 0 || p1 >= 0) {
+                const uint8_t *src = p0 >= 0 ? src0 : src1;
+                for (int i = wr * 512; i < L::kGroupBytes; i += WR * 512)
+                    if (i + lane * 16 < L::kGroupBytes) cp_async16(dst + i + (p0 >= 0 ? 0 : L::kGroupBytes), src + i);
             }
-            if (p1 >= 0) {
-#pragma unroll
-                for (int i = wr * 512; i < kRound * 16; i += WR * 512) cp_async16(dst + L::kGroupBytes + i, src1 + i);
-            }
-            if (wr == 0 && lane < 2 * kRest && (lane < kRest ? p0 : p1) >= 0)
-                cp_async16(dst + kRound * 16 + (lane < kRest ? 0 : L::kGroupBytes - kRest * 16), (lane < kRest ? src0 : src1 - kRest * 16) + kRound * 16);
-            if (wr == 0 && lane == 0) bad_pages[stage] = (p0 < 0 ? 1u : 0u) | (p1 < 0 ? 2u : 0u);
             ++put;
             ++copied;
         }
@@ -614,7 +649,7 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
         for (int r = 0; r < NTL; ++r)
 #pragma unroll
             for (int e = 0; e < 2; ++e) w.m[r][e] = -INFINITY, w.l[r][e] = 0.f;
-        w.top = 0;
+        w.top = w.low = 0;
 
         for (int k = 0; k < cur.n; ++k) {
             cp_wait<ST - 2>();
@@ -623,7 +658,7 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             const int stage = wt * ST + got % ST;
             ++got;
             const int tok0 = (cur.first + k) * kSlice;
-            const uint32_t base = smem_u32(ring + stage * C::kSliceBytes), bad = bad_pages[stage];
+            const uint32_t base = smem_u32(ring + stage * C::kSliceBytes), bad = bad_pages >> (2 * (copied - 1 - k)) & 3u;
             float *sk = scale + warp * (kSlice * NB * 3 / 2);
             uint32_t *sv = reinterpret_cast<uint32_t *>(sk + kSlice * NB);
             if (tok0 + kSlice <= seen && bad == 0)
@@ -810,7 +845,7 @@ cudaError_t launch_one(const DecodeArgs &a, int num_sms, cudaStream_t stream) {
 template <int D>
 cudaError_t launch_rows(const DecodeArgs &a, int num_sms, cudaStream_t stream) {
     const int64_t rows = (a.T + a.c.B - 1) / a.c.B * (a.q_heads / a.c.heads);
-    if (rows <= 8) return launch_one<D, Cfg<D, 8, 1, 12, 4>>(a, num_sms, stream);
+    if (rows <= 8) return launch_one<D, Cfg<D, 8, 1, 12, 3>>(a, num_sms, stream);
     if (rows <= 16) return launch_one<D, Cfg<D, 16, 1, 8, 4>>(a, num_sms, stream);
     if (rows <= 32) return launch_one<D, Cfg<D, 16, 2, 8, 4>>(a, num_sms, stream);
     return launch_one<D, Cfg<D, 16, 4, 8, 4>>(a, num_sms, stream);
