@@ -490,7 +490,7 @@ MHC_API size_t mhc_decode_workspace_size(void);
 MHC_API size_t mhc_prompt_workspace_size(void);
 
 /* Attention of each sequence's last tokens (one, or a verify block's few; their k and v already written) over the cache:
- *   out[i][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(s_j - max s),  s_j = sm_scale * <q[i][h], k_j>, over the j it sees
+ *   out[i][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(s_j - max s),  s_j = sm_scale * <q[i][h], k_j> (sm_scale > 0), over the j it sees
  *   q            [T][q_heads][head_dim] bf16
  *   attn_out     [T][q_heads][head_dim] bf16, or NULL
  *   attn_fp8, attn_scales   the result as MXFP8 [T][q_heads * head_dim] (scale tiles as above, one scale per 32 values,

@@ -49,6 +49,29 @@ __device__ __forceinline__ SeqOfRow find_sequence(const int32_t *__restrict__ of
     return {b, begin, end};
 }
 
+// A block's exclusive sum; `total` the whole.  Two syncs; `scratch` 33 words.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t &total, int64_t *scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+        const int64_t y = scratch[w];
+        if (w < warp) before += y;
+        all += y;
+    }
+    __syncthreads();
+    total = all;
+    return before + x - v;
+}
+
 // ---- the cache ----------------------------------------------------------------------
 // [pages][heads][page / 16 groups] of 17 * D bytes: K of the group's 16 tokens (8 * D bytes of E2M1 codes, then
 // D / 2 bytes of scales), V the same way.  A row of codes is D / 2 bytes, two codes a byte (the even value in the

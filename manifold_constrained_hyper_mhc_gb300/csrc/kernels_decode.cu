@@ -157,29 +157,6 @@ __device__ __forceinline__ int64_t cost(const DecodeArgs &a, const Seq &s) { ret
 // A share's length: at least two places.
 __device__ __forceinline__ int64_t share_of(int64_t total, int64_t units) { return max((int64_t)2, (total + units - 1) / units); }
 
-// A block's exclusive sum; `total` the whole.  Two syncs; `scratch` 33 words.
-template <int NT>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t &total, int64_t *scratch) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) scratch[warp] = x;
-    __syncthreads();
-    int64_t before = 0, all = 0;
-    for (int w = 0; w < NT / 32; ++w) {
-        const int64_t y = scratch[w];
-        if (w < warp) before += y;
-        all += y;
-    }
-    __syncthreads();
-    total = all;
-    return before + x - v;
-}
-
 template <int D, class C>
 struct Warp {                              // a warp's running state
     float o[C::NB][2][C::NTILE][4];        // O^T: per 32 values two tiles of 16, per 8 rows

@@ -1,45 +1,504 @@
 // Causal attention over packed prompts, with grouped heads.
+//
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(s_j - m),  s_j = sm_scale log2(e) <q, k_j>,  m near the largest s so far
+//
+// 4 D operations for each query head and visible key: the tensor cores are the floor.  The rows of one kv head are its
+// tokens times the heads of the group, NT = 128 / G whole tokens to a tile of 128 rows, so that a tile's rows see nearly
+// the same keys whatever G is.  A CTA takes two such tiles (A and B) over all their keys, 128 at a time, so that the
+// tensor cores work for one while the other's exponentials are taken:
+//   warps 0-3, 4-7  a row a thread: S from tensor memory, the row's maximum and sum, P as bf16 back over S (2^-8 of p: the
+//                   products take it beside bf16 v); a maximum is raised only when a score is kLazy above it (p is then
+//                   at most 2^kLazy), so the accumulators are rescaled a few times a row
+//   warp 8          the products: S = Q K^T from shared memory, O += P V with P from tensor memory
+//   warp 9          the copies: Q once, then K and V in turn into a ring (TMA, rows of a sequence in 128-byte swizzles)
+//   warp 10         what else a tile's V may hold: rows behind the sequence are zeroed, and the tiles that some row sees
+//                   only in part are searched for values that are not finite (0 times such a value is not 0).  One found,
+//                   or scores beyond 2^28, sends the CTA's rows through a plain fp32 loop instead.
+// Every mbarrier wait is bounded in time; one that gives up sets bit 0 of the status word.
+#include <algorithm>
+#include <cstring>
+
 #include "attention.cuh"
+#include "sm100_ptx.cuh"
+#include "tma_encode.h"
 
 namespace mhc {
 namespace {
 
-constexpr int kThreads = 128;
+using namespace ptx;
+
+constexpr int kKeys = 128;                           // of a tile
+constexpr float kLazy = 8.f;
+constexpr float kFar = 268435456.f;                  // 2^28: from here on s - m rounded once may be off by 2^4
+constexpr uint64_t kWaitLimitNs = 1000000000ull;     // 1 s per wait
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kThreads = 11 * 32;
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) prompt_rows_kernel(PromptArgs a) {
+struct Cfg {
+    static constexpr int NH = D / 64;                // 128-byte wide halves of a row
+    static constexpr int kHalf = 128 * 128;          // bytes of 128 such rows
+    static constexpr int kTile = NH * kHalf;         // Q of a tile, or 128 keys' K or V
+    static constexpr int ST = D == 128 ? 5 : 8;      // ring
+    static constexpr int kSmem = 1024 + 2 * kTile + ST * kTile;
+};
+
+struct PromptMaps {
+    CUtensorMap q, k, v;
+};
+
+struct Bars {
+    uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], fixed, drained;
+};
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+    return ok != 0;
+}
+// A wait by a whole warp: `dead` stays the same in all lanes.
+__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &dead) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || dead) return;
+    mbar_wait_timed(bar, parity, dead, kWaitLimitNs);
+    dead = __any_sync(0xffffffffu, dead);
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+        "r"(r[31])
+        : "memory");
+}
+// D[tmem] (+)= A[smem] x B[smem], bf16.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// V [keys][64] halves as the N x K operand: N contiguous (64-wide 128-byte swizzled atoms kHalf apart), groups of 8 keys
+// 1,024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_v(uint32_t saddr, uint32_t half_bytes) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((half_bytes >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+struct PromptSeq {
+    int64_t begin, k0;   // first packed query, first packed key
+    int n, len;          // queries and keys
+};
+__device__ __forceinline__ PromptSeq prompt_sequence(const PromptArgs &a, int b) {
+    const int64_t lo = clamp_row(__ldg(a.q_offsets + b), a.Tq), hi = clamp_row(__ldg(a.q_offsets + b + 1), a.Tq);
+    const int64_t k0 = clamp_row(__ldg(a.k_offsets + b), a.Tk), k1 = clamp_row(__ldg(a.k_offsets + b + 1), a.Tk);
+    return {lo, k0, hi > lo ? (int)(hi - lo) : 0, k1 > k0 ? (int)(k1 - k0) : 0};
+}
+
+// One row by a warp, in fp32: the plain form.
+template <int D>
+__device__ __noinline__ void plain_row(const PromptArgs &a, const PromptSeq &s, int i, int head, int g) {
     constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t t = item / a.q_heads;
-    if (t >= a.Tq) return;
-    const int hq = (int)(item % a.q_heads), head = hq / (a.q_heads / a.kv_heads);
-    const SeqOfRow s = find_sequence(a.q_offsets, a.B, t, a.Tq);
-    if (s.b < 0) return;
-    const int64_t k0 = clamp_row(__ldg(a.k_offsets + s.b), a.Tk), k1 = clamp_row(__ldg(a.k_offsets + s.b + 1), a.Tk);
-    const int64_t sees = max((int64_t)0, max((int64_t)0, k1 - k0) - (s.end - t) + 1);
-    float q[N], o[N];
-    const uint16_t *qp = a.q + t * a.q_stride + hq * D + lane * N;
+    const int lane = threadIdx.x & 31, hq = head * (a.q_heads / a.kv_heads) + g;
     auto widen = [](const uint16_t *p, float (&x)[N]) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = __uint_as_float((uint32_t)__ldg(p + i) << 16);
+        for (int e = 0; e < N; ++e) x[e] = __uint_as_float((uint32_t)__ldg(p + e) << 16);
     };
-    widen(qp, q);
+    float q[N], o[N];
+    widen(a.q + (s.begin + i) * a.q_stride + hq * D + lane * N, q);
     const float lse = attend_row<D>(
-        q, a.sm_scale * kLog2e, sees, [&](int64_t j, float (&x)[N]) { widen(a.k + (k0 + j) * a.k_stride + head * D + lane * N, x); },
-        [&](int64_t j, float (&x)[N]) { widen(a.v + (k0 + j) * a.v_stride + head * D + lane * N, x); }, o);
-    write_head_row<D>(a.o, t, hq, o, lse);
+        q, a.sm_scale * kLog2e, max(0, s.len - s.n + i + 1), [&](int64_t j, float (&x)[N]) { widen(a.k + (s.k0 + j) * a.k_stride + head * D + lane * N, x); },
+        [&](int64_t j, float (&x)[N]) { widen(a.v + (s.k0 + j) * a.v_stride + head * D + lane * N, x); }, o);
+    write_head_row<D>(a.o, s.begin + i, hq, o, lse);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ PromptMaps maps, const __grid_constant__ PromptArgs a) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *sQ = smem, *ring = smem + 2 * C::kTile;
+    __shared__ Bars bar;
+    __shared__ uint32_t tmem_base;
+    __shared__ int found[2], redo;
+    __shared__ int64_t scan[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int G = a.q_heads / a.kv_heads, NT = 128 / G;
+    const int head = (int)(blockIdx.x % (unsigned)a.kv_heads), place = (int)(blockIdx.x / (unsigned)a.kv_heads);
+
+    // ---- which pair of tiles: from the last sequence's last (which sees most keys) on
+    if (tid == 0) found[0] = -1, redo = 0;
+    __syncthreads();
+    int64_t before = 0;
+    for (int base = 0; base < a.B; base += kThreads) {
+        const int b = a.B - 1 - base - tid;
+        const int pairs = b >= 0 ? (prompt_sequence(a, b).n + 2 * NT - 1) / (2 * NT) : 0;
+        int64_t all;
+        const int64_t mine = before + block_scan<kThreads>((int64_t)pairs, all, scan);
+        if (place >= mine && place < mine + pairs) {
+            found[0] = b;
+            found[1] = pairs - 1 - (int)(place - mine);
+        }
+        before += all;
+        if (place < before) break;
+    }
+    __syncthreads();
+    if (found[0] < 0) return;
+    const PromptSeq s = prompt_sequence(a, found[0]);
+    const int q0 = found[1] * 2 * NT;
+    int tokens[2], tiles[2];  // of tile A and B: tokens, and tiles of keys that the last of them sees
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        tokens[x] = min(NT, max(0, s.n - q0 - x * NT));
+        const int end = tokens[x] > 0 ? max(0, s.len - s.n + q0 + x * NT + tokens[x]) : 0;
+        tiles[x] = (end + kKeys - 1) / kKeys;
+    }
+    const int n_tiles = max(tiles[0], tiles[1]);
+
+    if (tid == 0) {
+        mbar_init(&bar.q_full, 1);
+        for (int i = 0; i < C::ST; ++i) {
+            mbar_init(&bar.kv_full[i], 1);
+            mbar_init(&bar.kv_empty[i], 2);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&bar.s_full[x], 1);
+            mbar_init(&bar.p_full[x], 128);
+            mbar_init(&bar.o_full[x], 1);
+        }
+        mbar_init(&bar.fixed, 1);
+        mbar_init(&bar.drained, 1);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&tmem_base, 512);
+        tmem_relinquish();
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tm = tmem_base;            // columns: S of A, S of B (P over them), O of A, O of B
+    bool dead = false;
+
+    if (warp < 8) {
+        // ---- a row a thread
+        const int x = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tm + lanes + x * 128, tO = tm + lanes + 256 + x * 128;
+        const int i = row / G, g = row - i * G, tok = q0 + x * NT + i;
+        const bool on = i < tokens[x];
+        const int vis = on ? max(0, s.len - s.n + tok + 1) : 0;
+        const float f = a.sm_scale * kLog2e;
+        float m = -INFINITY;
+        float2 l2 = make_float2(0.f, 0.f);
+        const int n = tiles[x];
+        for (int j = 0; j < n && !dead; ++j) {
+            wait(&bar.s_full[x], j & 1, dead);
+            if (dead) break;
+            tmem_fence_after();
+            uint32_t r[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, r[c]);
+            tmem_wait_ld();
+            const int lim = vis - j * kKeys;
+            if (__any_sync(0xffffffffu, lim < kKeys)) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * c + e >= lim) r[c][e] = 0xff800000u;
+            }
+            float hi[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                hi[c] = __uint_as_float(r[c][0]);
+#pragma unroll
+                for (int e = 1; e < 31; e += 2) hi[c] = fmaxf(hi[c], fmaxf(__uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1])));
+                hi[c] = fmaxf(hi[c], __uint_as_float(r[c][31]));
+            }
+            const float top = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])) * f;
+            if (__any_sync(0xffffffffu, top > m + kLazy)) {
+                const float m1 = fmaxf(m, top), al = m == -INFINITY ? 0.f : ex2(m - m1);
+                if (fabsf(m1) > kFar && fabsf(m1) < INFINITY) redo = 1;
+                m = m1;
+                l2.x *= al;
+                l2.y *= al;
+                if (j > 0) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32 * c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                        tmem_st32(tO + 32 * c, o);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            const float2 f2 = make_float2(f, f), nb = make_float2(-base, -base);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t p[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float2 v = __ffma2_rn(make_float2(__uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1])), f2, nb);
+                    v.x = ex2(v.x);
+                    v.y = ex2(v.y);
+                    l2 = __fadd2_rn(l2, v);
+                    p[e] = pack2_rn(v.x, v.y);
+                }
+                tmem_st16(tS + 16 * c, p);
+            }
+            tmem_wait_st();
+            tmem_fence_before();
+            mbar_arrive(&bar.p_full[x]);
+        }
+        if (n > 0) wait(&bar.o_full[x], 0, dead);
+        tmem_fence_after();
+        named_sync(1, 288);                   // (with the check warp: `redo` is known)
+        if (redo) {
+            for (int r = warp; r < (tokens[0] + tokens[1]) * G; r += 8) plain_row<D>(a, s, q0 + r / G, head, r % G);
+        } else if (!dead) {
+            const float l = l2.x + l2.y, inv = vis > 0 ? 1.f / l : 0.f;   // (scores that are all -inf: NaN, 0 * inf)
+            const int64_t t = s.begin + tok;
+            const int hq = head * G + g;
+            uint32_t scales = 0;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32(tO + 32 * c, o);
+                    tmem_wait_ld();
+                }
+                float v[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = vis > 0 ? __uint_as_float(o[e]) * inv : 0.f;
+                const int64_t at = (t * a.q_heads + hq) * (int64_t)D + 32 * c;
+                if (on && a.o.out != nullptr) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4 *>(a.o.out + at + e) =
+                            make_uint4(pack2_rn(v[e], v[e + 1]), pack2_rn(v[e + 2], v[e + 3]), pack2_rn(v[e + 4], v[e + 5]), pack2_rn(v[e + 6], v[e + 7]));
+                }
+                if (on && a.o.mx.q != nullptr) {
+                    float amax = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) amax = fmaxf(amax, fabsf(v[e]));
+                    const int E = mx_exp(amax, a.o.mx.mode);
+                    const float k = __uint_as_float((uint32_t)(127 - E) << 23);
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        w[e] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * e] * k, v[4 * e + 1] * k), __NV_SATFINITE, __NV_E4M3) |
+                               (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * e + 2] * k, v[4 * e + 3] * k), __NV_SATFINITE, __NV_E4M3) << 16;
+                    *reinterpret_cast<uint4 *>(a.o.mx.q + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4 *>(a.o.mx.q + at + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+                    scales |= (uint32_t)(E + 127) << (8 * c);
+                }
+                __syncwarp();
+            }
+            if (on && a.o.mx.q != nullptr) {  // the head's blocks lie next to each other in a scale tile
+                uint8_t *p = a.o.mx.scale + mx_scale_offset(t, hq * (D / 32), a.q_heads * D);
+                if constexpr (D == 128) *reinterpret_cast<uint32_t *>(p) = scales;
+                else *reinterpret_cast<uint16_t *>(p) = (uint16_t)scales;
+            }
+            if (on && a.o.lse != nullptr) a.o.lse[t * a.q_heads + hq] = vis > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+        }
+        tmem_fence_before();
+    } else if (warp == kMmaWarp) {
+        // ---- products
+        constexpr uint32_t idS = idesc_bf16_f32(128, kKeys), idO = idesc_bf16_f32(128, D) | (1u << 16);   // (V: N contiguous)
+        if (n_tiles > 0) wait(&bar.q_full, 0, dead);
+        auto scores = [&](int x, int stage) {
+            const uint32_t q = smem_u32(sQ + x * C::kTile), k = smem_u32(ring + stage * C::kTile);
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = (kk / 4) * C::kHalf + (kk % 4) * 32;
+                    umma_ss(tm + x * 128, sdesc_kmajor_sw128(q + o, 1024), sdesc_kmajor_sw128(k + o, 1024), idS, kk > 0);
+                }
+                umma_commit(&bar.s_full[x]);
+            }
+            __syncwarp();
+        };
+        auto release = [&](int use) {
+            if (elect_one()) umma_commit(&bar.kv_empty[use % C::ST]);
+            __syncwarp();
+        };
+        if (n_tiles > 0) {
+            wait(&bar.kv_full[0], 0, dead);
+            tmem_fence_after();
+            for (int x = 0; x < 2 && !dead; ++x)
+                if (tiles[x] > 0) scores(x, 0);
+            release(0);
+        }
+        for (int j = 0; j < n_tiles && !dead; ++j) {
+            const int uv = 2 * j + 1, uk = 2 * j + 2;
+            bool have_v = false, have_k = false;
+            for (int x = 0; x < 2 && !dead; ++x) {
+                if (j >= tiles[x]) continue;
+                wait(&bar.p_full[x], j & 1, dead);
+                if (!have_v) {
+                    wait(&bar.kv_full[uv % C::ST], (uv / C::ST) & 1, dead);
+                    if (j == n_tiles - 1 && n_tiles * kKeys > s.len) wait(&bar.fixed, 0, dead);
+                    have_v = true;
+                }
+                if (dead) break;
+                tmem_fence_after();
+                const uint32_t v = smem_u32(ring + (uv % C::ST) * C::kTile);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        umma_tmemA(tm + 256 + x * 128, tm + x * 128 + kk * 8, sdesc_v(v + kk * 2048, C::kHalf), idO, j > 0 || kk > 0);
+                    if (j == tiles[x] - 1) umma_commit(&bar.o_full[x]);
+                }
+                __syncwarp();
+                if (j + 1 < tiles[x]) {
+                    if (!have_k) {
+                        wait(&bar.kv_full[uk % C::ST], (uk / C::ST) & 1, dead);
+                        have_k = true;
+                        if (dead) break;
+                    }
+                    scores(x, uk % C::ST);
+                }
+            }
+            if (dead) break;
+            release(uv);
+            if (have_k) release(uk);
+        }
+        if (dead) {  // the products in flight must end before their operands and accumulators go
+            if (elect_one()) umma_commit(&bar.drained);
+            __syncwarp();
+            bool d = false;
+            wait(&bar.drained, 0, d);
+        }
+    } else if (warp == kLoadWarp) {
+        // ---- copies
+        const int uses = 2 * n_tiles;
+        int i = 0;
+        if (n_tiles > 0) {
+            if (elect_one()) {
+                const uint32_t bytes = (uint32_t)(C::NH * NT * G * 128);
+                mbar_arrive_expect_tx(&bar.q_full, 2 * bytes);
+                for (int x = 0; x < 2; ++x)
+                    for (int h = 0; h < C::NH; ++h)
+                        tma_load_4d(sQ + x * C::kTile + h * C::kHalf, &maps.q, 64 * h, 0, head, (int)(s.begin + q0 + x * NT), &bar.q_full);
+            }
+            __syncwarp();
+            for (; i < uses; ++i) {
+                const int st = i % C::ST;
+                wait(&bar.kv_empty[st], ((i / C::ST) & 1) ^ 1, dead);
+                if (dead) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&bar.kv_full[st], C::kTile);
+                    for (int h = 0; h < C::NH; ++h)
+                        tma_load_3d(ring + st * C::kTile + h * C::kHalf, i & 1 ? &maps.v : &maps.k, 64 * h, head, (int)(s.k0 + (i / 2) * kKeys), &bar.kv_full[st]);
+                }
+                __syncwarp();
+            }
+            // every copy has to land before the CTA's shared memory goes (where nothing gave up, they have been used)
+            for (int u = max(0, i - C::ST); u < i; ++u) {
+                bool d = false;
+                wait(&bar.kv_full[u % C::ST], (u / C::ST) & 1, d);
+                dead |= d;
+            }
+        }
+    } else {
+        // ---- rows of V that are no part of the sequence, values that are not finite
+        const int first = max(0, s.len - s.n + q0 + 1);   // keys that every row sees
+        for (int i = 0; i < 2 * n_tiles; ++i) {
+            const int st = i % C::ST, j = i / 2;
+            wait(&bar.kv_full[st], (i / C::ST) & 1, dead);
+            if (dead) break;
+            if (i & 1) {
+                uint8_t *v = ring + st * C::kTile;
+                const int rows = min(kKeys, s.len - j * kKeys);
+                if (j == n_tiles - 1 && rows < kKeys) {
+                    for (int h = 0; h < C::NH; ++h)
+                        for (int o = rows * 128 + lane * 16; o < C::kHalf; o += 512) *reinterpret_cast<uint4 *>(v + h * C::kHalf + o) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.fixed);
+                }
+                if ((j + 1) * kKeys > first) {
+                    uint32_t bad = 0;
+                    for (int h = 0; h < C::NH; ++h)
+#pragma unroll 4
+                        for (int o = lane * 16; o < rows * 128; o += 512) {
+                            const uint4 w = *reinterpret_cast<const uint4 *>(v + h * C::kHalf + o);
+                            // an exponent of all ones carries into the sign's place
+                            bad |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) | ((w.z & 0x7f807f80u) + 0x00800080u) |
+                                   ((w.w & 0x7f807f80u) + 0x00800080u);
+                        }
+                    if (bad & 0x80008000u) redo = 1;
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.kv_empty[st]);
+        }
+        __syncwarp();
+        named_sync(1, 288);
+    }
+    if (__syncthreads_or(dead) && tid == 0) atomicOr(a.status, 1u);
+    if (warp == kMmaWarp) {
+        tmem_fence_after();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+template <int D>
+cudaError_t launch_one(const PromptArgs &a, cudaStream_t stream) {
+    using C = Cfg<D>;
+    tma::EncodeTiledFn fn;
+    cudaError_t e = tma::encoder(fn);
+    if (e != cudaSuccess) return e;
+    const int G = a.q_heads / a.kv_heads, NT = 128 / G;
+    PromptMaps maps;
+    std::memset(&maps, 0, sizeof maps);
+    {
+        const cuuint64_t dq[4] = {D, (cuuint64_t)G, (cuuint64_t)a.kv_heads, (cuuint64_t)a.Tq}, sq[3] = {D * 2, (cuuint64_t)G * D * 2, (cuuint64_t)a.q_stride * 2};
+        const cuuint32_t bq[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)NT};
+        if ((e = tma::encode_bf16(fn, &maps.q, 4, a.q, dq, sq, bq, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
+        const cuuint64_t dk[3] = {D, (cuuint64_t)a.kv_heads, (cuuint64_t)std::max<int64_t>(a.Tk, 1)};
+        const cuuint32_t bk[3] = {64, 1, kKeys};
+        // (without keys nothing is copied: any address does)
+        const cuuint64_t sk[2] = {D * 2, (cuuint64_t)a.k_stride * 2}, sv[2] = {D * 2, (cuuint64_t)a.v_stride * 2};
+        if ((e = tma::encode_bf16(fn, &maps.k, 3, a.Tk > 0 ? a.k : a.q, dk, sk, bk, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
+        if ((e = tma::encode_bf16(fn, &maps.v, 3, a.Tk > 0 ? a.v : a.q, dk, sv, bk, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
+    }
+    auto kern = prompt_kernel<D>;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) != cudaSuccess) return e;
+    const int64_t pairs = a.Tq / (2 * NT) + std::min<int64_t>(a.B, a.Tq);   // at most: the lengths are on the device
+    mark_main_kernel(stream, true);
+    kern<<<(unsigned)(pairs * a.kv_heads), kThreads, C::kSmem, stream>>>(maps, a);
+    mark_main_kernel(stream, false);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_prompt(const PromptArgs &a, int num_sms, cudaStream_t stream) {
-    const unsigned grid = (unsigned)((a.Tq * a.q_heads + kThreads / 32 - 1) / (kThreads / 32));
-    mark_main_kernel(stream, true);
-    if (a.D == 128) prompt_rows_kernel<128><<<grid, kThreads, 0, stream>>>(a);
-    else prompt_rows_kernel<64><<<grid, kThreads, 0, stream>>>(a);
-    mark_main_kernel(stream, false);
-    return cudaGetLastError();
+    (void)num_sms;
+    return a.D == 128 ? launch_one<128>(a, stream) : launch_one<64>(a, stream);
 }
 
 }  // namespace mhc

@@ -1021,7 +1021,7 @@ mhc_status mhc_decode_attention_mxfp4(const mhc_bf16 *q, int64_t q_stride, int64
         return st;
     const int64_t row = q_heads * head_dim;
     if ((st = check_stride("q_stride", q_stride, row)) != MHC_OK) return st;
-    if (!std::isfinite(sm_scale)) return fail(MHC_ERR_INVALID_ARG, "sm_scale must be finite");
+    if (!std::isfinite(sm_scale) || sm_scale <= 0.f) return fail(MHC_ERR_INVALID_ARG, "sm_scale must be finite and above 0");
     if (T == 0 || B == 0) return MHC_OK;
     if ((st = check_ptrs({{q, "q"}, {cache, "cache"}})) != MHC_OK) return st;
     if ((st = check_index({{offsets, "offsets"}, {seq_lens, "seq_lens"}, {page_table, "page_table"}})) != MHC_OK) return st;
@@ -1055,7 +1055,7 @@ mhc_status mhc_prompt_attention(const mhc_bf16 *q, int64_t q_stride, const mhc_b
     if ((st = check_stride("q_stride", q_stride, row)) != MHC_OK || (st = check_stride("k_stride", k_stride, kv_row)) != MHC_OK ||
         (st = check_stride("v_stride", v_stride, kv_row)) != MHC_OK)
         return st;
-    if (!std::isfinite(sm_scale)) return fail(MHC_ERR_INVALID_ARG, "sm_scale must be finite");
+    if (!std::isfinite(sm_scale) || sm_scale <= 0.f) return fail(MHC_ERR_INVALID_ARG, "sm_scale must be finite and above 0");
     if (Tq == 0 || B == 0) return MHC_OK;
     if ((st = check_ptrs({{q, "q"}})) != MHC_OK) return st;
     if (Tk > 0 && (st = check_ptrs({{k, "k"}, {v, "v"}})) != MHC_OK) return st;
