@@ -9,11 +9,13 @@
 //   warps 0-3, 4-7  a row a thread: S from tensor memory, the row's maximum and sum, P as bf16 back over S (2^-8 of p: the
 //                   products take it beside bf16 v); a maximum is raised only when a score is kLazy above it (p is then
 //                   at most 2^kLazy), so the accumulators are rescaled a few times a row
-//   warp 8          the products: S = Q K^T from shared memory, O += P V with P from tensor memory
-//   warp 9          the copies: Q once, then K and V in turn into a ring (TMA, rows of a sequence in 128-byte swizzles)
-//   warp 10         what else a tile's V may hold: rows behind the sequence are zeroed, and the tiles that some row sees
-//                   only in part are searched for values that are not finite (0 times such a value is not 0).  One found,
-//                   or scores beyond 2^28, sends the CTA's rows through a plain fp32 loop instead.
+//   warps 8, 9      A's and B's products: S = Q K^T from shared memory, O += P V with P from tensor memory.  They take
+//                   turns, O and the next S of one tile at a time (products of both at once end together, and both tiles
+//                   then wait for their exponentials together); the waits and commits of one are covered by the other's
+//   warp 10         the copies: Q once, then K and V in turn into a ring (TMA, rows of a sequence in 128-byte swizzles).
+//                   Then what else the last tiles of V hold: rows behind the sequence are zeroed, and the tiles that some
+//                   row sees only in part are searched for values that are not finite (0 times such a value is not 0).
+//                   One found, or scores beyond 2^28, sends the CTA's rows through a plain fp32 loop instead.
 // Every mbarrier wait is bounded in time; one that gives up sets bit 0 of the status word.
 #include <algorithm>
 #include <cstring>
@@ -31,7 +33,7 @@ constexpr int kKeys = 128;                           // of a tile
 constexpr float kLazy = 8.f;
 constexpr float kFar = 268435456.f;                  // 2^28: from here on s - m rounded once may be off by 2^4
 constexpr uint64_t kWaitLimitNs = 1000000000ull;     // 1 s per wait
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kThreads = 11 * 32;
+constexpr int kMmaWarp = 8 /* and 9 */, kLoadWarp = 10, kThreads = 12 * 32;
 
 template <int D>
 struct Cfg {
@@ -47,7 +49,7 @@ struct PromptMaps {
 };
 
 struct Bars {
-    uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], fixed, drained;
+    uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], turn[2], fixed, drained[2];
 };
 
 __device__ __forceinline__ bool elect_one() {
@@ -55,11 +57,23 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
     return ok != 0;
 }
-// A wait by a whole warp: `dead` stays the same in all lanes.
+// A wait by a whole warp, back-to-back tests; `dead` stays the same in all lanes.
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &dead) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || dead) return;
-    mbar_wait_timed(bar, parity, dead, kWaitLimitNs);
-    dead = __any_sync(0xffffffffu, dead);
+    const uint64_t t0 = globaltimer_ns();
+    do {
+        for (int i = 0; i < 64; ++i)
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
+    } while (!__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs));
+    dead = true;
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
@@ -182,10 +196,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mbar_init(&bar.s_full[x], 1);
             mbar_init(&bar.p_full[x], 128);
             mbar_init(&bar.o_full[x], 1);
+            mbar_init(&bar.turn[x], 1);
         }
         mbar_init(&bar.fixed, 1);
-        mbar_init(&bar.drained, 1);
+        for (int x = 0; x < 2; ++x) mbar_init(&bar.drained[x], 1);
         fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    if (warp < 8 && (tid & 127) >= NT * G) {   // the rows that no token fills, once: nothing is copied there
+        for (int h = 0; h < C::NH; ++h)
+            for (int o = 0; o < 128; o += 16)
+                *reinterpret_cast<uint4 *>(sQ + (warp >> 2) * C::kTile + h * C::kHalf + (tid & 127) * 128 + o) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
     }
     if (warp == kMmaWarp) {
@@ -197,50 +218,75 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     tmem_fence_after();
     const uint32_t tm = tmem_base;            // columns: S of A, S of B (P over them), O of A, O of B
     bool dead = false;
+    // The registers of the launch (168 a thread), split anew: 2 * 208 + 88 = 3 * 168.
+    auto finish = [&]() {  // by every thread, at its role's end
+        if (dead && lane == 0) atomicOr(a.status, 1u);
+        tmem_fence_before();
+        named_sync(2, kThreads);
+    };
 
     if (warp < 8) {
+        more_registers<208>();
         // ---- a row a thread
         const int x = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tm + lanes + x * 128, tO = tm + lanes + 256 + x * 128;
         const int i = row / G, g = row - i * G, tok = q0 + x * NT + i;
         const bool on = i < tokens[x];
-        const int vis = on ? max(0, s.len - s.n + tok + 1) : 0;
+        const int vis = on ? max(0, s.len - s.n + tok + 1) : 0x7fffffff;   // (a row that is none has nothing to hide)
         const float f = a.sm_scale * kLog2e;
         float m = -INFINITY;
         float2 l2 = make_float2(0.f, 0.f);
         const int n = tiles[x];
+        const float2 f2 = make_float2(f, f);
+        uint32_t r[4][32];                    // the row's scores, 32 keys at a time
+        float hi[4];
+        auto maximum = [&](int c) {
+            hi[c] = __uint_as_float(r[c][0]);
+#pragma unroll
+            for (int e = 1; e < 31; e += 2) hi[c] = fmaxf(hi[c], fmaxf(__uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1])));
+            hi[c] = fmaxf(hi[c], __uint_as_float(r[c][31]));
+        };
+        auto exponentials = [&](int c, float2 nb) {  // P of chunk c, over S's first columns (loaded by then)
+            uint32_t p[16];
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                float2 v = __ffma2_rn(make_float2(__uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1])), f2, nb);
+                v.x = ex2(v.x);
+                v.y = ex2(v.y);
+                sum = __fadd2_rn(sum, v);
+                p[e] = pack2_rn(v.x, v.y);
+            }
+            l2 = __fadd2_rn(l2, sum);
+            tmem_st16(tS + 16 * c, p);
+        };
         for (int j = 0; j < n && !dead; ++j) {
             wait(&bar.s_full[x], j & 1, dead);
             if (dead) break;
             tmem_fence_after();
-            uint32_t r[4][32];
+            const int lim = vis - j * kKeys;
+            const float2 before_l = l2;
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, r[c]);
             tmem_wait_ld();
-            const int lim = vis - j * kKeys;
             if (__any_sync(0xffffffffu, lim < kKeys)) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
+                    const int seen = lim - 32 * c;                           // of the chunk's keys, as bits
+                    const uint32_t bits = seen >= 32 ? 0xffffffffu : seen <= 0 ? 0u : (1u << seen) - 1u;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * c + e >= lim) r[c][e] = 0xff800000u;
+                    for (int e = 0; e < 32; ++e) r[c][e] = bits >> e & 1u ? r[c][e] : 0xff800000u;
+                }
             }
-            float hi[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                hi[c] = __uint_as_float(r[c][0]);
-#pragma unroll
-                for (int e = 1; e < 31; e += 2) hi[c] = fmaxf(hi[c], fmaxf(__uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1])));
-                hi[c] = fmaxf(hi[c], __uint_as_float(r[c][31]));
-            }
+            for (int c = 0; c < 4; ++c) maximum(c);
             const float top = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])) * f;
             if (__any_sync(0xffffffffu, top > m + kLazy)) {
                 const float m1 = fmaxf(m, top), al = m == -INFINITY ? 0.f : ex2(m - m1);
-                if (fabsf(m1) > kFar && fabsf(m1) < INFINITY) redo = 1;
+                if (on && fabsf(m1) > kFar && fabsf(m1) < INFINITY) redo = 1;
                 m = m1;
-                l2.x *= al;
-                l2.y *= al;
+                l2 = make_float2(before_l.x * al, before_l.y * al);
                 if (j > 0) {
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
@@ -254,27 +300,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 }
             }
             const float base = m == -INFINITY ? 0.f : m;
-            const float2 f2 = make_float2(f, f), nb = make_float2(-base, -base);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t p[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float2 v = __ffma2_rn(make_float2(__uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1])), f2, nb);
-                    v.x = ex2(v.x);
-                    v.y = ex2(v.y);
-                    l2 = __fadd2_rn(l2, v);
-                    p[e] = pack2_rn(v.x, v.y);
-                }
-                tmem_st16(tS + 16 * c, p);
-            }
+            for (int c = 0; c < 4; ++c) exponentials(c, make_float2(-base, -base));
             tmem_wait_st();
             tmem_fence_before();
             mbar_arrive(&bar.p_full[x]);
         }
         if (n > 0) wait(&bar.o_full[x], 0, dead);
         tmem_fence_after();
-        named_sync(1, 288);                   // (with the check warp: `redo` is known)
+        named_sync(1, 288);                   // (with the copies' warp: `redo` is known)
         if (redo) {
             for (int r = warp; r < (tokens[0] + tokens[1]) * G; r += 8) plain_row<D>(a, s, q0 + r / G, head, r % G);
         } else if (!dead) {
@@ -323,73 +357,66 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             }
             if (on && a.o.lse != nullptr) a.o.lse[t * a.q_heads + hq] = vis > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
         }
-        tmem_fence_before();
-    } else if (warp == kMmaWarp) {
-        // ---- products
+        finish();
+        return;
+    }
+    fewer_registers<88>();
+    if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+        // ---- products of tile A, of tile B: what one warp spends on waits and commits, the other's products cover
         constexpr uint32_t idS = idesc_bf16_f32(128, kKeys), idO = idesc_bf16_f32(128, D) | (1u << 16);   // (V: N contiguous)
-        if (n_tiles > 0) wait(&bar.q_full, 0, dead);
-        auto scores = [&](int x, int stage) {
-            const uint32_t q = smem_u32(sQ + x * C::kTile), k = smem_u32(ring + stage * C::kTile);
+        const int x = warp - kMmaWarp, n = tiles[x];
+        const uint32_t tS = tm + x * 128, tO = tm + 256 + x * 128, q = smem_u32(sQ + x * C::kTile);
+        auto scores = [&](int use) {  // S of the K that use number `use` of the ring holds; then K is done with
+            const uint32_t k = smem_u32(ring + (use % C::ST) * C::kTile);
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t o = (kk / 4) * C::kHalf + (kk % 4) * 32;
-                    umma_ss(tm + x * 128, sdesc_kmajor_sw128(q + o, 1024), sdesc_kmajor_sw128(k + o, 1024), idS, kk > 0);
+                    umma_ss(tS, sdesc_kmajor_sw128(q + o, 1024), sdesc_kmajor_sw128(k + o, 1024), idS, kk > 0);
                 }
                 umma_commit(&bar.s_full[x]);
+                umma_commit(&bar.kv_empty[use % C::ST]);
             }
             __syncwarp();
         };
-        auto release = [&](int use) {
-            if (elect_one()) umma_commit(&bar.kv_empty[use % C::ST]);
-            __syncwarp();
-        };
-        if (n_tiles > 0) {
+        if (n > 0) {
+            wait(&bar.q_full, 0, dead);
             wait(&bar.kv_full[0], 0, dead);
             tmem_fence_after();
-            for (int x = 0; x < 2 && !dead; ++x)
-                if (tiles[x] > 0) scores(x, 0);
-            release(0);
+            if (!dead) scores(0);
         }
-        for (int j = 0; j < n_tiles && !dead; ++j) {
+        for (int j = 0; j < n && !dead; ++j) {
             const int uv = 2 * j + 1, uk = 2 * j + 2;
-            bool have_v = false, have_k = false;
-            for (int x = 0; x < 2 && !dead; ++x) {
-                if (j >= tiles[x]) continue;
-                wait(&bar.p_full[x], j & 1, dead);
-                if (!have_v) {
-                    wait(&bar.kv_full[uv % C::ST], (uv / C::ST) & 1, dead);
-                    if (j == n_tiles - 1 && n_tiles * kKeys > s.len) wait(&bar.fixed, 0, dead);
-                    have_v = true;
-                }
-                if (dead) break;
-                tmem_fence_after();
-                const uint32_t v = smem_u32(ring + (uv % C::ST) * C::kTile);
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        umma_tmemA(tm + 256 + x * 128, tm + x * 128 + kk * 8, sdesc_v(v + kk * 2048, C::kHalf), idO, j > 0 || kk > 0);
-                    if (j == tiles[x] - 1) umma_commit(&bar.o_full[x]);
-                }
-                __syncwarp();
-                if (j + 1 < tiles[x]) {
-                    if (!have_k) {
-                        wait(&bar.kv_full[uk % C::ST], (uk / C::ST) & 1, dead);
-                        have_k = true;
-                        if (dead) break;
-                    }
-                    scores(x, uk % C::ST);
-                }
-            }
+            wait(&bar.kv_full[uv % C::ST], (uv / C::ST) & 1, dead);
+            if (j == n_tiles - 1 && n_tiles * kKeys > s.len) wait(&bar.fixed, 0, dead);
+            if (j + 1 < n) wait(&bar.kv_full[uk % C::ST], (uk / C::ST) & 1, dead);
+            wait(&bar.p_full[x], j & 1, dead);
+            if (x == 0 ? j > 0 && j - 1 < tiles[1] : j < tiles[0]) wait(&bar.turn[x], (x == 0 ? j - 1 : j) & 1, dead);
             if (dead) break;
-            release(uv);
-            if (have_k) release(uk);
+            tmem_fence_after();
+            const uint32_t v = smem_u32(ring + (uv % C::ST) * C::kTile);
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk) umma_tmemA(tO, tS + kk * 8, sdesc_v(v + kk * 2048, C::kHalf), idO, j > 0 || kk > 0);
+                umma_commit(&bar.kv_empty[uv % C::ST]);
+                if (j == n - 1) umma_commit(&bar.o_full[x]);
+            }
+            __syncwarp();
+            if (j + 1 < n) scores(uk);
+            if (lane == 0) mbar_arrive(&bar.turn[1 - x]);
+            __syncwarp();
+        }
+        // (the ring is the other tile's too: what this one does not use)
+        for (int use = 2 * n; use < 2 * n_tiles && !dead; ++use) {
+            wait(&bar.kv_full[use % C::ST], (use / C::ST) & 1, dead);
+            if (lane == 0) mbar_arrive(&bar.kv_empty[use % C::ST]);
+            __syncwarp();
         }
         if (dead) {  // the products in flight must end before their operands and accumulators go
-            if (elect_one()) umma_commit(&bar.drained);
+            if (elect_one()) umma_commit(&bar.drained[x]);
             __syncwarp();
             bool d = false;
-            wait(&bar.drained, 0, d);
+            wait(&bar.drained[x], 0, d);
         }
     } else if (warp == kLoadWarp) {
         // ---- copies
@@ -415,6 +442,33 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 }
                 __syncwarp();
             }
+            // ---- what else the last tiles of V hold (those that some row sees only in part: the tokens of both tiles lie
+            // in three of them at most, and nothing is copied over the last three)
+            static_assert(C::ST >= 5, "");
+            const int first = max(0, s.len - s.n + q0 + 1) / kKeys;
+            for (int j = max(first, n_tiles - 3); j < n_tiles && !dead; ++j) {
+                const int use = 2 * j + 1;
+                wait(&bar.kv_full[use % C::ST], (use / C::ST) & 1, dead);
+                uint8_t *v = ring + (use % C::ST) * C::kTile;
+                const int rows = min(kKeys, s.len - j * kKeys);
+                if (rows < kKeys) {   // rows behind the sequence
+                    for (int h = 0; h < C::NH; ++h)
+                        for (int o = rows * 128 + lane * 16; o < C::kHalf; o += 512) *reinterpret_cast<uint4 *>(v + h * C::kHalf + o) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.fixed);
+                }
+                uint32_t bad = 0;
+                for (int h = 0; h < C::NH; ++h)
+#pragma unroll 4
+                    for (int o = lane * 16; o < rows * 128; o += 512) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(v + h * C::kHalf + o);
+                        // an exponent of all ones carries into the sign's place
+                        bad |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) | ((w.z & 0x7f807f80u) + 0x00800080u) |
+                               ((w.w & 0x7f807f80u) + 0x00800080u);
+                    }
+                if (bad & 0x80008000u) redo = 1;
+            }
             // every copy has to land before the CTA's shared memory goes (where nothing gave up, they have been used)
             for (int u = max(0, i - C::ST); u < i; ++u) {
                 bool d = false;
@@ -422,43 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 dead |= d;
             }
         }
-    } else {
-        // ---- rows of V that are no part of the sequence, values that are not finite
-        const int first = max(0, s.len - s.n + q0 + 1);   // keys that every row sees
-        for (int i = 0; i < 2 * n_tiles; ++i) {
-            const int st = i % C::ST, j = i / 2;
-            wait(&bar.kv_full[st], (i / C::ST) & 1, dead);
-            if (dead) break;
-            if (i & 1) {
-                uint8_t *v = ring + st * C::kTile;
-                const int rows = min(kKeys, s.len - j * kKeys);
-                if (j == n_tiles - 1 && rows < kKeys) {
-                    for (int h = 0; h < C::NH; ++h)
-                        for (int o = rows * 128 + lane * 16; o < C::kHalf; o += 512) *reinterpret_cast<uint4 *>(v + h * C::kHalf + o) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.fixed);
-                }
-                if ((j + 1) * kKeys > first) {
-                    uint32_t bad = 0;
-                    for (int h = 0; h < C::NH; ++h)
-#pragma unroll 4
-                        for (int o = lane * 16; o < rows * 128; o += 512) {
-                            const uint4 w = *reinterpret_cast<const uint4 *>(v + h * C::kHalf + o);
-                            // an exponent of all ones carries into the sign's place
-                            bad |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) | ((w.z & 0x7f807f80u) + 0x00800080u) |
-                                   ((w.w & 0x7f807f80u) + 0x00800080u);
-                        }
-                    if (bad & 0x80008000u) redo = 1;
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.kv_empty[st]);
-        }
         __syncwarp();
         named_sync(1, 288);
     }
-    if (__syncthreads_or(dead) && tid == 0) atomicOr(a.status, 1u);
+    finish();
     if (warp == kMmaWarp) {
         tmem_fence_after();
         tmem_dealloc(tm, 512);
