@@ -603,73 +603,85 @@ def kv_cache_shape(pages: int, kv_heads: int, page_size: int, head_dim: int):
     return (pages, kv_heads, page_size // 16, 17 * head_dim)
 
 
-def _strided(t, name, dtypes, dev):
+def _rows(t, name, dtypes, shape, dev):
     """A [T, heads, D] argument that may be part of wider rows: its address and a token's distance in values."""
+    if t.shape == shape and t.dtype in dtypes and t.device == dev:
+        st, sh, sd = t.stride()
+        T, heads, D = shape
+        if sd == 1 and (sh == D or heads == 1):
+            return t.data_ptr(), (st if T > 1 else heads * D)
+        if T == 0:
+            return t.data_ptr(), heads * D
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d).removeprefix('torch.') for d in dtypes)}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be a tensor on {dev} whose heads lie next to each other")
+
+
+def _three(t, name):
+    """The sizes of a [tokens, heads, head_dim] argument."""
     if t.dim() != 3:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens, heads, head_dim]")
-    T, heads, D = t.shape
-    st, sh, sd = t.stride()
-    if t.device != dev or (T > 0 and ((sd != 1 and D > 1) or (sh != D and heads > 1))):
-        raise ValueError(f"{name} must be a tensor on {dev} whose heads lie next to each other")
-    return t.data_ptr(), (st if T > 1 else heads * D)
+    return t.shape
 
 
-def _cache(cache, page_table, seq_lens, offsets, dev):
-    """The checked cache: its address and sizes, and the addresses of its index tensors."""
-    _, fp8, _, _, i32 = _dtypes()
-    if cache.dim() != 4 or cache.shape[3] not in (17 * 64, 17 * 128):
-        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected that of kv_cache_shape()")
-    pages, heads, groups, width = cache.shape
+def _cache(cache, page_table, seq_lens, offsets, types):
+    """The checked cache: its device, its address, its sizes (pages, heads, page_size, head_dim), and the geometry's
+    arguments of a call."""
+    dev = _cuda(cache, "cache")
+    shape = cache.shape
+    if len(shape) != 4 or shape[3] != 2176 and shape[3] != 1088:
+        raise ValueError(f"cache has shape {tuple(shape)}, expected that of kv_cache_shape()")
     if page_table.dim() != 2:
         raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [sequences, pages]")
     B, W = page_table.shape
-    return (_arg(cache, "cache", fp8[:1], cache.shape, dev), (pages, heads, groups * 16, width // 17),
+    i32 = types[4]
+    return (dev, _arg(cache, "cache", types[1][:1], shape, dev), (shape[0], shape[1], shape[2] * 16, shape[3] // 17),
             (_arg(offsets, "offsets", i32, (B + 1,), dev), _arg(seq_lens, "seq_lens", i32, (B,), dev),
-             _arg(page_table, "page_table", i32, (B, W), dev)), (B, W))
+             _arg(page_table, "page_table", i32, (B, W), dev), B, W))
 
 
-def _attn_out(T, heads, D, dev, out, want_bf16, want_mxfp8, want_lse, workspace, size, stream):
-    """The output dict of an attention, the addresses of its forms, and the workspace's."""
-    torch = _torch()
-    bf16, fp8, e8m0, f32, _ = _dtypes()
+def _attn_out(T, heads, D, dev, types, out, want_bf16, want_mxfp8, want_lse, scale_mode, workspace, size, stream):
+    """The output dict of an attention, and the last arguments of its call."""
+    torch = _torch_mod
     o = dict(out) if out else {}
-    K = heads * D
-    tiles = _scale_shape(T, K)
-    if want_bf16 and "attn_out" not in o:
-        o["attn_out"] = _new((T, heads, D), torch.bfloat16, dev, stream)
-    if want_mxfp8:
-        if "attn_fp8" not in o:
+    b = q = s = e = None
+    if "attn_out" in o or want_bf16:
+        if "attn_out" not in o:
+            o["attn_out"] = _new((T, heads, D), torch.bfloat16, dev, stream)
+        b = _arg(o["attn_out"], "attn_out", types[0], (T, heads, D), dev)
+    if want_mxfp8 or "attn_fp8" in o or "attn_scales" in o:
+        K = heads * D
+        tiles = _scale_shape(T, K)
+        if want_mxfp8 and "attn_fp8" not in o:
             o["attn_fp8"] = _new((T, K), torch.uint8, dev, stream)
-        if "attn_scales" not in o:
+        if want_mxfp8 and "attn_scales" not in o:
             o["attn_scales"] = _new(tiles, torch.uint8, dev, stream)
-    if want_lse and "lse" not in o:
-        o["lse"] = _new((T, heads), torch.float32, dev, stream)
+        q = _arg(o["attn_fp8"], "attn_fp8", types[1], (T, K), dev) if "attn_fp8" in o else None
+        s = _arg(o["attn_scales"], "attn_scales", types[2], tiles, dev) if "attn_scales" in o else None
+    if "lse" in o or want_lse:
+        if "lse" not in o:
+            o["lse"] = _new((T, heads), torch.float32, dev, stream)
+        e = _arg(o["lse"], "lse", types[3], (T, heads), dev)
     if workspace is None:
         workspace = _new((size(),), torch.uint8, dev, stream, zero=True)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    b, q, s, e = o.get("attn_out"), o.get("attn_fp8"), o.get("attn_scales"), o.get("lse")
-    return (o, None if b is None else _arg(b, "attn_out", bf16, (T, heads, D), dev), None if q is None else _arg(q, "attn_fp8", fp8, (T, K), dev),
-            None if s is None else _arg(s, "attn_scales", e8m0, tiles, dev), None if e is None else _arg(e, "lse", f32, (T, heads), dev),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace)
+    return o, (b, q, s, int(scale_mode), e, workspace.data_ptr(), workspace.nbytes), workspace
 
 
 def kv_write_mxfp4(k, v, cache, page_table, seq_lens, offsets, *, scale_mode=MX_SCALE_FLOOR, stream=None):
     """mhc_kv_write_mxfp4: quantizes k and v [T, kv_heads, head_dim] (bfloat16 or float32, both the same; parts of a
     wider row are fine) into the cache.  offsets [B+1] are the packed rows of each sequence, the last of its
     seq_lens [B] tokens; page_table [B, W].  Returns the cache."""
-    dev = _cuda(cache, "cache")
-    bf16, _, _, f32, _ = _dtypes()
-    wide = k.dtype == f32[0]
-    (kp, ks), (vp, vs) = _strided(k, "k", bf16 + f32, dev), _strided(v, "v", f32 if wide else bf16, dev)
-    address, sizes, index, (B, W) = _cache(cache, page_table, seq_lens, offsets, dev)
-    T = k.shape[0]
-    for t, name in ((k, "k"), (v, "v")):
-        if t.shape != (T, sizes[1], sizes[3]):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, sizes[1], sizes[3])}")
-    _run("mhc_kv_write_mxfp4", dev, stream, kp, vp, int(wide), ks, vs, T, *index, B, W, address, *sizes, int(scale_mode))
+    types = _dtypes()
+    dev, address, sizes, index = _cache(cache, page_table, seq_lens, offsets, types)
+    wide = k.dtype == types[3][0]
+    shape = (k.shape[0], sizes[1], sizes[3])
+    kp, ks = _rows(k, "k", types[0] + types[3], shape, dev)
+    vp, vs = _rows(v, "v", types[3] if wide else types[0], shape, dev)
+    _run("mhc_kv_write_mxfp4", dev, stream, kp, vp, int(wide), ks, vs, shape[0], *index, address, *sizes, int(scale_mode))
     return cache
 
 
@@ -677,9 +689,8 @@ def kv_read_mxfp4(cache, page_table, seq_lens, offsets, *, rows=None, out=None, 
     """mhc_kv_read_mxfp4: the last offsets[b+1] - offsets[b] tokens of each sequence as bfloat16.  Returns a dict with k
     and v [rows, kv_heads, head_dim]; ``out`` may supply them (both), otherwise ``rows`` says how many packed rows
     there are."""
-    torch = _torch()
-    dev = _cuda(cache, "cache")
-    address, sizes, index, (B, W) = _cache(cache, page_table, seq_lens, offsets, dev)
+    types = _dtypes()
+    dev, address, sizes, index = _cache(cache, page_table, seq_lens, offsets, types)
     o = dict(out) if out else {}
     if rows is None:
         if "k" not in o:
@@ -688,10 +699,9 @@ def kv_read_mxfp4(cache, page_table, seq_lens, offsets, *, rows=None, out=None, 
     shape = (rows, sizes[1], sizes[3])
     for n in ("k", "v"):
         if n not in o:
-            o[n] = _new(shape, torch.bfloat16, dev, stream)
-    bf16 = _dtypes()[0]
-    _run("mhc_kv_read_mxfp4", dev, stream, address, *sizes, *index, B, W, rows, _arg(o["k"], "k", bf16, shape, dev),
-         _arg(o["v"], "v", bf16, shape, dev))
+            o[n] = _new(shape, _torch_mod.bfloat16, dev, stream)
+    _run("mhc_kv_read_mxfp4", dev, stream, address, *sizes, *index, rows, _arg(o["k"], "k", types[0], shape, dev),
+         _arg(o["v"], "v", types[0], shape, dev))
     return o
 
 
@@ -710,15 +720,15 @@ def decode_attention_mxfp4(q, cache, page_table, seq_lens, offsets, *, sm_scale=
     attn_out [T, q_heads, head_dim] bf16, attn_fp8 [T, q_heads * head_dim] and attn_scales (the MXFP8 form that
     linear_mxfp8 reads) and lse [T, q_heads], those that are wanted or given in ``out``.  workspace:
     decode_workspace_size() zeroed bytes, for calls in order; without one the call fills a new one with zeros."""
-    dev = _cuda(cache, "cache")
-    qp, qs = _strided(q, "q", _dtypes()[0], dev)
-    T, heads, D = q.shape
-    address, sizes, index, (B, W) = _cache(cache, page_table, seq_lens, offsets, dev)
+    types = _dtypes()
+    dev, address, sizes, index = _cache(cache, page_table, seq_lens, offsets, types)
+    T, heads, D = _three(q, "q")
     if D != sizes[3]:
         raise ValueError(f"q has shape {tuple(q.shape)}, but the cache's head_dim is {sizes[3]}")
-    o, b, f, s, e, ws, n, keep = _attn_out(T, heads, D, dev, out, want_bf16, want_mxfp8, want_lse, workspace, decode_workspace_size, stream)
-    _run("mhc_decode_attention_mxfp4", dev, stream, qp, qs, T, heads, *index, B, W, address, *sizes,
-         D ** -0.5 if sm_scale is None else float(sm_scale), b, f, s, int(scale_mode), e, ws, n)
+    qp, qs = _rows(q, "q", types[0], (T, heads, D), dev)
+    o, tail, keep = _attn_out(T, heads, D, dev, types, out, want_bf16, want_mxfp8, want_lse, scale_mode, workspace, decode_workspace_size,
+                              stream)
+    _run("mhc_decode_attention_mxfp4", dev, stream, qp, qs, T, heads, *index, address, *sizes, D ** -0.5 if sm_scale is None else sm_scale, *tail)
     return o
 
 
@@ -728,18 +738,19 @@ def prompt_attention(q, k, v, q_offsets, k_offsets, *, sm_scale=None, want_bf16=
     head_dim] bf16 (parts of a wider row are fine); the rows q_offsets[b] .. are the last of the keys k_offsets[b] ...
     Options and result as decode_attention_mxfp4's; workspace: prompt_workspace_size() zeroed bytes, which any calls
     may share (a wait in the kernel that gave up is noted there: check_status)."""
+    types = _dtypes()
     dev = _cuda(q, "q")
-    bf16, _, _, _, i32 = _dtypes()
-    (qp, qs), (kp, ks), (vp, vs) = (_strided(t, n, bf16, dev) for t, n in ((q, "q"), (k, "k"), (v, "v")))
-    Tq, heads, D = q.shape
-    Tk, kv_heads = k.shape[:2]
-    for t, name in ((k, "k"), (v, "v")):
-        if t.shape != (Tk, kv_heads, D):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(Tk, kv_heads, D)}")
+    Tq, heads, D = _three(q, "q")
+    Tk, kv_heads, _ = _three(k, "k")
+    bf16, i32 = types[0], types[4]
+    qp, qs = _rows(q, "q", bf16, (Tq, heads, D), dev)
+    kp, ks = _rows(k, "k", bf16, (Tk, kv_heads, D), dev)
+    vp, vs = _rows(v, "v", bf16, (Tk, kv_heads, D), dev)
     B = q_offsets.shape[0] - 1
-    o, b, f, s, e, ws, n, keep = _attn_out(Tq, heads, D, dev, out, want_bf16, want_mxfp8, want_lse, workspace, prompt_workspace_size, stream)
+    o, tail, keep = _attn_out(Tq, heads, D, dev, types, out, want_bf16, want_mxfp8, want_lse, scale_mode, workspace, prompt_workspace_size,
+                              stream)
     _run("mhc_prompt_attention", dev, stream, qp, qs, kp, ks, vp, vs, Tq, Tk, heads, kv_heads, D, _arg(q_offsets, "q_offsets", i32, (B + 1,), dev),
-         _arg(k_offsets, "k_offsets", i32, (B + 1,), dev), B, D ** -0.5 if sm_scale is None else float(sm_scale), b, f, s, int(scale_mode), e, ws, n)
+         _arg(k_offsets, "k_offsets", i32, (B + 1,), dev), B, D ** -0.5 if sm_scale is None else sm_scale, *tail)
     return o
 
 

@@ -4,6 +4,8 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "mhc_device.cuh"
 #include "mhc_kernels.h"
 
@@ -15,6 +17,19 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, hardware approximation 
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// The kernel's dynamic shared memory, set once for each device (the call takes half a microsecond).
+template <class Kernel>
+inline cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // ---- the packed batch -------------------------------------------------------------

@@ -793,7 +793,8 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) join_kernel(c
 template <int D, class C>
 cudaError_t launch_one(const DecodeArgs &a, int num_sms, cudaStream_t stream) {
     auto kern = decode_kernel<D, C>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(kern, C::kSmem, allowed);
     if (e != cudaSuccess) return e;
     const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
     mark_main_kernel(stream, true);

@@ -507,7 +507,8 @@ cudaError_t launch_one(const PromptArgs &a, cudaStream_t stream) {
         if ((e = tma::encode_bf16(fn, &maps.v, 3, a.Tk > 0 ? a.v : a.q, dk, sv, bk, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
     }
     auto kern = prompt_kernel<D>;
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) != cudaSuccess) return e;
+    static std::atomic<uint64_t> allowed{0};
+    if ((e = allow_smem(kern, C::kSmem, allowed)) != cudaSuccess) return e;
     const int64_t pairs = a.Tq / (2 * NT) + std::min<int64_t>(a.B, a.Tq);   // at most: the lengths are on the device
     mark_main_kernel(stream, true);
     kern<<<(unsigned)(pairs * a.kv_heads), kThreads, C::kSmem, stream>>>(maps, a);

@@ -83,13 +83,23 @@ struct Device {
     int id, sms, major, minor;
 };
 
+// (The attributes are read once for each device: they take about a microsecond.)
 mhc_status current_device(Device &d) {
+    constexpr int kDevices = 64;
+    static std::atomic<uint64_t> known[kDevices];  // sms << 32 | major << 16 | minor, 0 before
     cudaError_t e = cudaGetDevice(&d.id);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, d.id)) != cudaSuccess ||
-        (e = cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, d.id)) != cudaSuccess ||
-        (e = cudaDeviceGetAttribute(&d.minor, cudaDevAttrComputeCapabilityMinor, d.id)) != cudaSuccess)
-        return cuda_fail(e, "cudaDeviceGetAttribute");
+    const bool in = d.id >= 0 && d.id < kDevices;
+    const uint64_t k = in ? known[d.id].load(std::memory_order_relaxed) : 0;
+    if (k != 0) {
+        d.sms = (int)(k >> 32), d.major = (int)(k >> 16 & 0xffff), d.minor = (int)(k & 0xffff);
+    } else {
+        if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, d.id)) != cudaSuccess ||
+            (e = cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, d.id)) != cudaSuccess ||
+            (e = cudaDeviceGetAttribute(&d.minor, cudaDevAttrComputeCapabilityMinor, d.id)) != cudaSuccess)
+            return cuda_fail(e, "cudaDeviceGetAttribute");
+        if (in) known[d.id].store((uint64_t)d.sms << 32 | (uint64_t)d.major << 16 | (uint64_t)d.minor, std::memory_order_relaxed);
+    }
     if (d.major != 10 || d.minor != 3)
         return fail(MHC_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_103a",
                     d.id, d.major, d.minor);
