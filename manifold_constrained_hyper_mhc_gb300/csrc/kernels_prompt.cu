@@ -4,18 +4,20 @@
 //
 // 4 D operations for each query head and visible key: the tensor cores are the floor.  The rows of one kv head are its
 // tokens times the heads of the group, NT = 128 / G whole tokens to a tile of 128 rows, so that a tile's rows see nearly
-// the same keys whatever G is.  A CTA takes two such tiles (A and B) over all their keys, 128 at a time, so that the
-// tensor cores work for one while the other's exponentials are taken:
-//   warps 0-3, 4-7  a row a thread: S from tensor memory, the row's maximum and sum, P as bf16 back over S (2^-8 of p: the
-//                   products take it beside bf16 v); a maximum is raised only when a score is kLazy above it (p is then
-//                   at most 2^kLazy), so the accumulators are rescaled a few times a row
-//   warps 8, 9      A's and B's products: S = Q K^T from shared memory, O += P V with P from tensor memory.  They take
-//                   turns, O and the next S of one tile at a time (products of both at once end together, and both tiles
-//                   then wait for their exponentials together); the waits and commits of one are covered by the other's
-//   warp 10         the copies: Q once, then K and V in turn into a ring (TMA, rows of a sequence in 128-byte swizzles).
-//                   Then what else the last tiles of V hold: rows behind the sequence are zeroed, and the tiles that some
-//                   row sees only in part are searched for values that are not finite (0 times such a value is not 0).
-//                   One found, or scores beyond 2^28, sends the CTA's rows through a plain fp32 loop instead.
+// the same keys whatever G is.  A CTA takes two such tiles (A and B) over all their keys, 128 at a time:
+//   warps 0-3, 4-7  A's and B's rows, a row a thread: S from tensor memory, the row's maximum and sum, P as bf16 back to
+//                   tensor memory (2^-8 of p: the products take it beside bf16 v); a maximum is raised only when a score
+//                   is kLazy above it (p is then at most 2^kLazy), so the accumulators are rescaled a few times a row
+//   warp 8          S = Q K^T from shared memory, A's and B's in turn into the same columns: S is in registers soon after
+//                   it is there, so the next one is computed beside the exponentials of this one
+//   warp 9          O += P V with P from tensor memory
+//   warp 10         the copies: Q, then K and V in turn into a ring (TMA, rows of a sequence in 128-byte swizzles)
+//   warp 11         what else the last tiles of V hold: rows behind the sequence are zeroed, and the tiles that some row sees
+//                   only in part are searched for values that are not finite (0 times such a value is not 0).  One
+//                   found, or scores beyond 2^28, sends the tile's rows through a plain fp32 loop instead.
+// The grid has a block for every pair of tiles; a CTA that has issued its pair's copies takes over a block that has not
+// begun (cluster launch control), so that its next pair's copies and first products run beside the present one's end, and
+// pairs of all lengths fill the device.
 // Every mbarrier wait is bounded in time; one that gives up sets bit 0 of the status word.
 #include <algorithm>
 #include <cstring>
@@ -48,8 +50,12 @@ struct PromptMaps {
     CUtensorMap q, k, v;
 };
 
+constexpr int kPart = 3;   // tiles of keys that a pair's rows see only in part: its tokens are at most 256 neighbours
+
 struct Bars {
-    uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], turn[2], fixed, drained[2];
+    uint64_t item_full[2], item_empty[2], next;
+    uint64_t q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], s_taken, p_full[2], pv_done[2];
+    uint64_t go[2][kPart], checked[2][kPart], drained[2];
 };
 
 __device__ __forceinline__ bool elect_one() {
@@ -120,10 +126,73 @@ struct PromptSeq {
     int64_t begin, k0;   // first packed query, first packed key
     int n, len;          // queries and keys
 };
-__device__ __forceinline__ PromptSeq prompt_sequence(const PromptArgs &a, int b) {
-    const int64_t lo = clamp_row(__ldg(a.q_offsets + b), a.Tq), hi = clamp_row(__ldg(a.q_offsets + b + 1), a.Tq);
+// A pair of tiles of one kv head.
+struct Item {
+    PromptSeq s;
+    int more, head, q0;      // whether there is one; its kv head, and its first token
+    int tokens[2], tiles[2]; // of tile A and B: tokens, and tiles of keys that the last of them sees
+    int n_tiles, part;       // tiles of keys, and the first that some row sees only in part
+};
+
+// Which pair is `place`, by one warp.  Sequence b's pairs are the places from floor(offset_b / X) + b on, X tokens to a pair: they
+// never reach the next sequence's, and the range of places that holds the last b with floor(offset_b / X) + b <= place is
+// narrowed to a 32nd a step.  Places without a pair are left over, one a sequence at most.  Places are taken from the
+// last on, so that a sequence's longest pairs come first.
+__device__ __forceinline__ Item locate(const PromptArgs &a, unsigned block, unsigned blocks, int NT) {
+    const int lane = threadIdx.x & 31, X = 2 * NT;
+    Item it{};
+    it.more = 1;
+    it.head = (int)(block % (unsigned)a.kv_heads);
+    const int64_t place = (int64_t)(blocks / (unsigned)a.kv_heads) - 1 - (int64_t)(block / (unsigned)a.kv_heads);
+    auto key = [&](int b) { return clamp_row(__ldg(a.q_offsets + b), a.Tq) / X + b; };
+    int lo = 0, n = a.B;
+    while (n > 32) {
+        const int step = (n + 31) / 32;
+        const bool le = lane * step < n && key(lo + lane * step) <= place;
+        const int k = __popc(__ballot_sync(0xffffffffu, le));
+        if (k == 0) return it;
+        lo += (k - 1) * step;
+        n = min(step, n - (k - 1) * step);
+    }
+    const bool le = lane < n && key(lo + lane) <= place;
+    const int b = lo + __popc(__ballot_sync(0xffffffffu, le)) - 1;
+    if (b < 0) return it;
+    const int64_t begin = clamp_row(__ldg(a.q_offsets + b), a.Tq), end = clamp_row(__ldg(a.q_offsets + b + 1), a.Tq);
     const int64_t k0 = clamp_row(__ldg(a.k_offsets + b), a.Tk), k1 = clamp_row(__ldg(a.k_offsets + b + 1), a.Tk);
-    return {lo, k0, hi > lo ? (int)(hi - lo) : 0, k1 > k0 ? (int)(k1 - k0) : 0};
+    const int64_t pair = place - (begin / X + b);
+    if (end <= begin || pair * X >= end - begin) return it;
+    it.s = {begin, k0, (int)(end - begin), k1 > k0 ? (int)(k1 - k0) : 0};
+    it.q0 = (int)pair * X;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        it.tokens[x] = min(NT, max(0, it.s.n - it.q0 - x * NT));
+        const int last = it.tokens[x] > 0 ? max(0, it.s.len - it.s.n + it.q0 + x * NT + it.tokens[x]) : 0;
+        it.tiles[x] = (last + kKeys - 1) / kKeys;
+    }
+    it.n_tiles = max(it.tiles[0], it.tiles[1]);
+    it.part = max(max(0, it.s.len - it.s.n + it.q0 + 1) / kKeys, it.n_tiles - kPart);
+    return it;
+}
+
+// ---- a row's scores of 32 keys
+__device__ __forceinline__ float largest(const uint32_t (&r)[32]) {
+    float hi = __uint_as_float(r[0]);
+#pragma unroll
+    for (int e = 1; e < 31; e += 2) hi = fmaxf(hi, fmaxf(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
+    return fmaxf(hi, __uint_as_float(r[31]));
+}
+// Their exponentials as bf16, and added to the row's sum.
+__device__ __forceinline__ void exponentials(const uint32_t (&r)[32], float2 f2, float2 minus_m, float2 &l2, uint32_t *p) {
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        float2 v = __ffma2_rn(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), f2, minus_m);
+        v.x = ex2(v.x);
+        v.y = ex2(v.y);
+        sum = __fadd2_rn(sum, v);
+        p[e] = pack2_rn(v.x, v.y);
+    }
+    l2 = __fadd2_rn(l2, sum);
 }
 
 // One row by a warp, in fp32: the plain form.
@@ -146,60 +215,39 @@ __device__ __noinline__ void plain_row(const PromptArgs &a, const PromptSeq &s, 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ PromptMaps maps, const __grid_constant__ PromptArgs a) {
     using C = Cfg<D>;
+    constexpr int ST = C::ST;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sQ = smem, *ring = smem + 2 * C::kTile;
     __shared__ Bars bar;
+    __shared__ Item items[2];
+    __shared__ int redo[2], far[2][2];        // of an item; of a tile of it
+    __shared__ __align__(16) uint4 answer;    // which block was taken over
     __shared__ uint32_t tmem_base;
-    __shared__ int found[2], redo;
-    __shared__ int64_t scan[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.q_heads / a.kv_heads, NT = 128 / G;
-    const int head = (int)(blockIdx.x % (unsigned)a.kv_heads), place = (int)(blockIdx.x / (unsigned)a.kv_heads);
-
-    // ---- which pair of tiles: from the last sequence's last (which sees most keys) on
-    if (tid == 0) found[0] = -1, redo = 0;
-    __syncthreads();
-    int64_t before = 0;
-    for (int base = 0; base < a.B; base += kThreads) {
-        const int b = a.B - 1 - base - tid;
-        const int pairs = b >= 0 ? (prompt_sequence(a, b).n + 2 * NT - 1) / (2 * NT) : 0;
-        int64_t all;
-        const int64_t mine = before + block_scan<kThreads>((int64_t)pairs, all, scan);
-        if (place >= mine && place < mine + pairs) {
-            found[0] = b;
-            found[1] = pairs - 1 - (int)(place - mine);
-        }
-        before += all;
-        if (place < before) break;
-    }
-    __syncthreads();
-    if (found[0] < 0) return;
-    const PromptSeq s = prompt_sequence(a, found[0]);
-    const int q0 = found[1] * 2 * NT;
-    int tokens[2], tiles[2];  // of tile A and B: tokens, and tiles of keys that the last of them sees
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        tokens[x] = min(NT, max(0, s.n - q0 - x * NT));
-        const int end = tokens[x] > 0 ? max(0, s.len - s.n + q0 + x * NT + tokens[x]) : 0;
-        tiles[x] = (end + kKeys - 1) / kKeys;
-    }
-    const int n_tiles = max(tiles[0], tiles[1]);
 
     if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.item_full[i], 1);
+            mbar_init(&bar.item_empty[i], 11);   // every other warp
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.p_full[i], 128);
+            mbar_init(&bar.pv_done[i], 1);
+            mbar_init(&bar.drained[i], 1);
+            for (int k = 0; k < kPart; ++k) {
+                mbar_init(&bar.go[i][k], 1);
+                mbar_init(&bar.checked[i][k], 1);
+            }
+        }
+        mbar_init(&bar.next, 1);
+        mbar_init(&bar.s_taken, 128);
         mbar_init(&bar.q_full, 1);
-        for (int i = 0; i < C::ST; ++i) {
+        mbar_init(&bar.q_empty, 1);
+        for (int i = 0; i < ST; ++i) {
             mbar_init(&bar.kv_full[i], 1);
-            mbar_init(&bar.kv_empty[i], 2);
+            mbar_init(&bar.kv_empty[i], 1);
         }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(&bar.s_full[x], 1);
-            mbar_init(&bar.p_full[x], 128);
-            mbar_init(&bar.o_full[x], 1);
-            mbar_init(&bar.turn[x], 1);
-        }
-        mbar_init(&bar.fixed, 1);
-        for (int x = 0; x < 2; ++x) mbar_init(&bar.drained[x], 1);
         fence_mbar_init();
         fence_proxy_async_smem();
     }
@@ -216,268 +264,359 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tm = tmem_base;            // columns: S of A, S of B (P over them), O of A, O of B
-    bool dead = false;
-    // The registers of the launch (168 a thread), split anew: 2 * 208 + 88 = 3 * 168.
+    const uint32_t tm = tmem_base;            // columns: S (of either tile), P of A, P of B, O of A, O of B
+    bool dead = false, issued = false;        // a wait gave up; this warp has issued products
     auto finish = [&]() {  // by every thread, at its role's end
         if (dead && lane == 0) atomicOr(a.status, 1u);
         tmem_fence_before();
         named_sync(2, kThreads);
     };
+    // Item t is in slot t % 2, the 1 + t / 2nd there.
+    auto take = [&](int t) {
+        wait(&bar.item_full[t & 1], (t >> 1) & 1, dead);
+        return !dead && items[t & 1].more != 0;
+    };
+    auto leave = [&](int t) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.item_empty[t & 1]);
+    };
 
+    // The registers of the launch (168 a thread), split anew: 2 * 208 + 88 = 3 * 168.
     if (warp < 8) {
         more_registers<208>();
         // ---- a row a thread
         const int x = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tm + lanes + x * 128, tO = tm + lanes + 256 + x * 128;
-        const int i = row / G, g = row - i * G, tok = q0 + x * NT + i;
-        const bool on = i < tokens[x];
-        const int vis = on ? max(0, s.len - s.n + tok + 1) : 0x7fffffff;   // (a row that is none has nothing to hide)
+        const uint32_t tS = tm + lanes, tP = tS + 128 + x * 64, tO = tS + 256 + x * 128;
+        const int i = row / G, g = row - i * G;
         const float f = a.sm_scale * kLog2e;
-        float m = -INFINITY;
-        float2 l2 = make_float2(0.f, 0.f);
-        const int n = tiles[x];
         const float2 f2 = make_float2(f, f);
-        uint32_t r[4][32];                    // the row's scores, 32 keys at a time
-        float hi[4];
-        auto maximum = [&](int c) {
-            hi[c] = __uint_as_float(r[c][0]);
+        uint32_t n_s = 0, n_pv = 0;           // scores so far, products with V waited for
+        for (int t = 0; take(t); ++t) {
+            const Item &it = items[t & 1];
+            const int tok = it.q0 + x * NT + i, n = it.tiles[x], slot = t & 1;
+            const bool on = i < it.tokens[x];
+            const int vis = on ? max(0, it.s.len - it.s.n + tok + 1) : 0x7fffffff;   // (a row that is none has nothing to hide)
+            float m = -INFINITY;
+            float2 l2 = make_float2(0.f, 0.f);
+            for (int j = 0; j < n; ++j, ++n_s) {
+                wait(&bar.s_full[x], n_s & 1, dead);
+                if (dead) break;
+                tmem_fence_after();
+                uint32_t r[4][32];
 #pragma unroll
-            for (int e = 1; e < 31; e += 2) hi[c] = fmaxf(hi[c], fmaxf(__uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1])));
-            hi[c] = fmaxf(hi[c], __uint_as_float(r[c][31]));
-        };
-        auto exponentials = [&](int c, float2 nb) {  // P of chunk c, over S's first columns (loaded by then)
-            uint32_t p[16];
-            float2 sum = make_float2(0.f, 0.f);
+                for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, r[c]);
+                tmem_wait_ld();
+                tmem_fence_before();
+                mbar_arrive(&bar.s_taken);    // (the next scores may come, the other tile's)
+                const int lim = vis - j * kKeys;
+                if (__any_sync(0xffffffffu, lim < kKeys)) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float2 v = __ffma2_rn(make_float2(__uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1])), f2, nb);
-                v.x = ex2(v.x);
-                v.y = ex2(v.y);
-                sum = __fadd2_rn(sum, v);
-                p[e] = pack2_rn(v.x, v.y);
-            }
-            l2 = __fadd2_rn(l2, sum);
-            tmem_st16(tS + 16 * c, p);
-        };
-        for (int j = 0; j < n && !dead; ++j) {
-            wait(&bar.s_full[x], j & 1, dead);
-            if (dead) break;
-            tmem_fence_after();
-            const int lim = vis - j * kKeys;
-            const float2 before_l = l2;
+                    for (int c = 0; c < 4; ++c) {
+                        const int seen = lim - 32 * c;                           // of the chunk's keys, as bits
+                        const uint32_t bits = seen >= 32 ? 0xffffffffu : seen <= 0 ? 0u : (1u << seen) - 1u;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, r[c]);
-            tmem_wait_ld();
-            if (__any_sync(0xffffffffu, lim < kKeys)) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int seen = lim - 32 * c;                           // of the chunk's keys, as bits
-                    const uint32_t bits = seen >= 32 ? 0xffffffffu : seen <= 0 ? 0u : (1u << seen) - 1u;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) r[c][e] = bits >> e & 1u ? r[c][e] : 0xff800000u;
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) maximum(c);
-            const float top = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])) * f;
-            if (__any_sync(0xffffffffu, top > m + kLazy)) {
-                const float m1 = fmaxf(m, top), al = m == -INFINITY ? 0.f : ex2(m - m1);
-                if (on && fabsf(m1) > kFar && fabsf(m1) < INFINITY) redo = 1;
-                m = m1;
-                l2 = make_float2(before_l.x * al, before_l.y * al);
-                if (j > 0) {
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + 32 * c, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                        tmem_st32(tO + 32 * c, o);
+                        for (int e = 0; e < 32; ++e) r[c][e] = bits >> e & 1u ? r[c][e] : 0xff800000u;
                     }
                 }
-            }
-            const float base = m == -INFINITY ? 0.f : m;
+                const float top = fmaxf(fmaxf(largest(r[0]), largest(r[1])), fmaxf(largest(r[2]), largest(r[3]))) * f;
+                bool idle = j == 0;           // the products with the P before are done
+                auto pv_done = [&]() {
+                    if (idle) return;
+                    wait(&bar.pv_done[x], n_pv & 1, dead);
+                    ++n_pv;
+                    idle = true;
+                    tmem_fence_after();
+                };
+                if (__any_sync(0xffffffffu, top > m + kLazy)) {
+                    const float m1 = fmaxf(m, top), al = m == -INFINITY ? 0.f : ex2(m - m1);
+                    if (on && fabsf(m1) > kFar && fabsf(m1) < INFINITY) far[slot][x] = 1;
+                    m = m1;
+                    l2 = make_float2(l2.x * al, l2.y * al);
+                    if (j > 0) {   // (few columns at a time: the scores are in registers)
+                        pv_done();
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + 16 * c, o);
+                            tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) exponentials(c, make_float2(-base, -base));
-            tmem_wait_st();
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                            tmem_st16(tO + 16 * c, o);
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                uint32_t p[2][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) exponentials(r[c], f2, make_float2(-base, -base), l2, &p[c / 2][c % 2 * 16]);
+                pv_done();
+                tmem_st32(tP, p[0]);
+                tmem_st32(tP + 32, p[1]);
+                tmem_wait_st();
+                tmem_fence_before();
+                mbar_arrive(&bar.p_full[x]);
+            }
+            if (dead) break;
+            if (n > 0) {
+                wait(&bar.pv_done[x], n_pv & 1, dead);
+                ++n_pv;
+            }
+            for (int k = 0; k < kPart; ++k) wait(&bar.checked[slot][k], (t >> 1) & 1, dead);
+            if (dead) break;
+            tmem_fence_after();
+            named_sync(3 + x, 128);               // (`far` of all the tile's rows is known)
+            if (redo[slot] | far[slot][x]) {
+                for (int r = warp & 3; r < it.tokens[x] * G; r += 4) plain_row<D>(a, it.s, it.q0 + x * NT + r / G, it.head, r % G);
+            } else {
+                const float l = l2.x + l2.y, inv = vis > 0 ? 1.f / l : 0.f;   // (scores that are all -inf: NaN, 0 * inf)
+                const int64_t at_row = (it.s.begin + tok) * a.q_heads + it.head * G + g;
+                uint32_t scales = 0;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (n > 0) {
+                        tmem_ld32(tO + 32 * c, o);
+                        tmem_wait_ld();
+                    }
+                    float v[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = n > 0 && vis > 0 ? __uint_as_float(o[e]) * inv : 0.f;
+                    const int64_t at = at_row * D + 32 * c;
+                    if (on && a.o.out != nullptr) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4 *>(a.o.out + at + e) =
+                                make_uint4(pack2_rn(v[e], v[e + 1]), pack2_rn(v[e + 2], v[e + 3]), pack2_rn(v[e + 4], v[e + 5]), pack2_rn(v[e + 6], v[e + 7]));
+                    }
+                    if (on && a.o.mx.q != nullptr) {
+                        float amax = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) amax = fmaxf(amax, fabsf(v[e]));
+                        const int E = mx_exp(amax, a.o.mx.mode);
+                        const float k = __uint_as_float((uint32_t)(127 - E) << 23);
+                        uint32_t w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            w[e] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * e] * k, v[4 * e + 1] * k), __NV_SATFINITE, __NV_E4M3) |
+                                   (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * e + 2] * k, v[4 * e + 3] * k), __NV_SATFINITE, __NV_E4M3) << 16;
+                        *reinterpret_cast<uint4 *>(a.o.mx.q + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(a.o.mx.q + at + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+                        scales |= (uint32_t)(E + 127) << (8 * c);
+                    }
+                    __syncwarp();
+                }
+                if (on && a.o.mx.q != nullptr) {  // the head's blocks lie next to each other in a scale tile
+                    uint8_t *p = a.o.mx.scale + mx_scale_offset(it.s.begin + tok, (it.head * G + g) * (D / 32), a.q_heads * D);
+                    if constexpr (D == 128) *reinterpret_cast<uint32_t *>(p) = scales;
+                    else *reinterpret_cast<uint16_t *>(p) = (uint16_t)scales;
+                }
+                if (on && a.o.lse != nullptr) a.o.lse[at_row] = vis > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+            }
             tmem_fence_before();
-            mbar_arrive(&bar.p_full[x]);
-        }
-        if (n > 0) wait(&bar.o_full[x], 0, dead);
-        tmem_fence_after();
-        named_sync(1, 288);                   // (with the copies' warp: `redo` is known)
-        if (redo) {
-            for (int r = warp; r < (tokens[0] + tokens[1]) * G; r += 8) plain_row<D>(a, s, q0 + r / G, head, r % G);
-        } else if (!dead) {
-            const float l = l2.x + l2.y, inv = vis > 0 ? 1.f / l : 0.f;   // (scores that are all -inf: NaN, 0 * inf)
-            const int64_t t = s.begin + tok;
-            const int hq = head * G + g;
-            uint32_t scales = 0;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                if (n > 0) {
-                    tmem_ld32(tO + 32 * c, o);
-                    tmem_wait_ld();
-                }
-                float v[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = vis > 0 ? __uint_as_float(o[e]) * inv : 0.f;
-                const int64_t at = (t * a.q_heads + hq) * (int64_t)D + 32 * c;
-                if (on && a.o.out != nullptr) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4 *>(a.o.out + at + e) =
-                            make_uint4(pack2_rn(v[e], v[e + 1]), pack2_rn(v[e + 2], v[e + 3]), pack2_rn(v[e + 4], v[e + 5]), pack2_rn(v[e + 6], v[e + 7]));
-                }
-                if (on && a.o.mx.q != nullptr) {
-                    float amax = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) amax = fmaxf(amax, fabsf(v[e]));
-                    const int E = mx_exp(amax, a.o.mx.mode);
-                    const float k = __uint_as_float((uint32_t)(127 - E) << 23);
-                    uint32_t w[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w[e] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * e] * k, v[4 * e + 1] * k), __NV_SATFINITE, __NV_E4M3) |
-                               (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * e + 2] * k, v[4 * e + 3] * k), __NV_SATFINITE, __NV_E4M3) << 16;
-                    *reinterpret_cast<uint4 *>(a.o.mx.q + at) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4 *>(a.o.mx.q + at + 16) = make_uint4(w[4], w[5], w[6], w[7]);
-                    scales |= (uint32_t)(E + 127) << (8 * c);
-                }
-                __syncwarp();
-            }
-            if (on && a.o.mx.q != nullptr) {  // the head's blocks lie next to each other in a scale tile
-                uint8_t *p = a.o.mx.scale + mx_scale_offset(t, hq * (D / 32), a.q_heads * D);
-                if constexpr (D == 128) *reinterpret_cast<uint32_t *>(p) = scales;
-                else *reinterpret_cast<uint16_t *>(p) = (uint16_t)scales;
-            }
-            if (on && a.o.lse != nullptr) a.o.lse[t * a.q_heads + hq] = vis > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+            leave(t);
         }
         finish();
         return;
     }
     fewer_registers<88>();
-    if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-        // ---- products of tile A, of tile B: what one warp spends on waits and commits, the other's products cover
-        constexpr uint32_t idS = idesc_bf16_f32(128, kKeys), idO = idesc_bf16_f32(128, D) | (1u << 16);   // (V: N contiguous)
-        const int x = warp - kMmaWarp, n = tiles[x];
-        const uint32_t tS = tm + x * 128, tO = tm + 256 + x * 128, q = smem_u32(sQ + x * C::kTile);
-        auto scores = [&](int use) {  // S of the K that use number `use` of the ring holds; then K is done with
-            const uint32_t k = smem_u32(ring + (use % C::ST) * C::kTile);
-            if (elect_one()) {
+    if (warp == kMmaWarp) {
+        // ---- S = Q K^T: A's, B's, A's ... as soon as the one before has been taken
+        constexpr uint32_t id = idesc_bf16_f32(128, kKeys);
+        uint32_t use0 = 0, n_q = 0, n_s = 0;  // uses of the ring before this item; items with copies, scores so far
+        for (int t = 0; take(t); leave(t), ++t) {
+            const Item &it = items[t & 1];
+            const int n_tiles = it.n_tiles, tiles[2] = {it.tiles[0], it.tiles[1]};
+            if (n_tiles == 0) continue;
+            wait(&bar.q_full, n_q & 1, dead);
+            ++n_q;
+            for (int j = 0; j < n_tiles; ++j) {
+                const uint32_t use = use0 + 2 * j, k = smem_u32(ring + use % ST * C::kTile);
+                wait(&bar.kv_full[use % ST], (use / ST) & 1, dead);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t o = (kk / 4) * C::kHalf + (kk % 4) * 32;
-                    umma_ss(tS, sdesc_kmajor_sw128(q + o, 1024), sdesc_kmajor_sw128(k + o, 1024), idS, kk > 0);
+                for (int x = 0; x < 2; ++x) {
+                    if (j >= tiles[x]) continue;
+                    if (n_s > 0) wait(&bar.s_taken, (n_s - 1) & 1, dead);
+                    ++n_s;
+                    if (dead) break;
+                    tmem_fence_after();
+                    const uint32_t q = smem_u32(sQ + x * C::kTile);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t o = (kk / 4) * C::kHalf + (kk % 4) * 32;
+                            umma_ss(tm, sdesc_kmajor_sw128(q + o, 1024), sdesc_kmajor_sw128(k + o, 1024), id, kk > 0);
+                        }
+                        umma_commit(&bar.s_full[x]);
+                    }
+                    __syncwarp();
+                    issued = true;
                 }
-                umma_commit(&bar.s_full[x]);
-                umma_commit(&bar.kv_empty[use % C::ST]);
-            }
-            __syncwarp();
-        };
-        if (n > 0) {
-            wait(&bar.q_full, 0, dead);
-            wait(&bar.kv_full[0], 0, dead);
-            tmem_fence_after();
-            if (!dead) scores(0);
-        }
-        for (int j = 0; j < n && !dead; ++j) {
-            const int uv = 2 * j + 1, uk = 2 * j + 2;
-            wait(&bar.kv_full[uv % C::ST], (uv / C::ST) & 1, dead);
-            if (j == n_tiles - 1 && n_tiles * kKeys > s.len) wait(&bar.fixed, 0, dead);
-            if (j + 1 < n) wait(&bar.kv_full[uk % C::ST], (uk / C::ST) & 1, dead);
-            wait(&bar.p_full[x], j & 1, dead);
-            if (x == 0 ? j > 0 && j - 1 < tiles[1] : j < tiles[0]) wait(&bar.turn[x], (x == 0 ? j - 1 : j) & 1, dead);
-            if (dead) break;
-            tmem_fence_after();
-            const uint32_t v = smem_u32(ring + (uv % C::ST) * C::kTile);
-            if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk) umma_tmemA(tO, tS + kk * 8, sdesc_v(v + kk * 2048, C::kHalf), idO, j > 0 || kk > 0);
-                umma_commit(&bar.kv_empty[uv % C::ST]);
-                if (j == n - 1) umma_commit(&bar.o_full[x]);
-            }
-            __syncwarp();
-            if (j + 1 < n) scores(uk);
-            if (lane == 0) mbar_arrive(&bar.turn[1 - x]);
-            __syncwarp();
-        }
-        // (the ring is the other tile's too: what this one does not use)
-        for (int use = 2 * n; use < 2 * n_tiles && !dead; ++use) {
-            wait(&bar.kv_full[use % C::ST], (use / C::ST) & 1, dead);
-            if (lane == 0) mbar_arrive(&bar.kv_empty[use % C::ST]);
-            __syncwarp();
-        }
-        if (dead) {  // the products in flight must end before their operands and accumulators go
-            if (elect_one()) umma_commit(&bar.drained[x]);
-            __syncwarp();
-            bool d = false;
-            wait(&bar.drained[x], 0, d);
-        }
-    } else if (warp == kLoadWarp) {
-        // ---- copies
-        const int uses = 2 * n_tiles;
-        int i = 0;
-        if (n_tiles > 0) {
-            if (elect_one()) {
-                const uint32_t bytes = (uint32_t)(C::NH * NT * G * 128);
-                mbar_arrive_expect_tx(&bar.q_full, 2 * bytes);
-                for (int x = 0; x < 2; ++x)
-                    for (int h = 0; h < C::NH; ++h)
-                        tma_load_4d(sQ + x * C::kTile + h * C::kHalf, &maps.q, 64 * h, 0, head, (int)(s.begin + q0 + x * NT), &bar.q_full);
-            }
-            __syncwarp();
-            for (; i < uses; ++i) {
-                const int st = i % C::ST;
-                wait(&bar.kv_empty[st], ((i / C::ST) & 1) ^ 1, dead);
                 if (dead) break;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&bar.kv_full[st], C::kTile);
-                    for (int h = 0; h < C::NH; ++h)
-                        tma_load_3d(ring + st * C::kTile + h * C::kHalf, i & 1 ? &maps.v : &maps.k, 64 * h, head, (int)(s.k0 + (i / 2) * kKeys), &bar.kv_full[st]);
+                    umma_commit(&bar.kv_empty[use % ST]);
+                    if (j == n_tiles - 1) umma_commit(&bar.q_empty);
                 }
                 __syncwarp();
             }
-            // ---- what else the last tiles of V hold (those that some row sees only in part: the tokens of both tiles lie
-            // in three of them at most, and nothing is copied over the last three)
-            static_assert(C::ST >= 5, "");
-            const int first = max(0, s.len - s.n + q0 + 1) / kKeys;
-            for (int j = max(first, n_tiles - 3); j < n_tiles && !dead; ++j) {
-                const int use = 2 * j + 1;
-                wait(&bar.kv_full[use % C::ST], (use / C::ST) & 1, dead);
-                uint8_t *v = ring + (use % C::ST) * C::kTile;
-                const int rows = min(kKeys, s.len - j * kKeys);
-                if (rows < kKeys) {   // rows behind the sequence
-                    for (int h = 0; h < C::NH; ++h)
-                        for (int o = rows * 128 + lane * 16; o < C::kHalf; o += 512) *reinterpret_cast<uint4 *>(v + h * C::kHalf + o) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.fixed);
-                }
-                uint32_t bad = 0;
-                for (int h = 0; h < C::NH; ++h)
-#pragma unroll 4
-                    for (int o = lane * 16; o < rows * 128; o += 512) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(v + h * C::kHalf + o);
-                        // an exponent of all ones carries into the sign's place
-                        bad |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) | ((w.z & 0x7f807f80u) + 0x00800080u) |
-                               ((w.w & 0x7f807f80u) + 0x00800080u);
+            use0 += 2 * n_tiles;
+            if (dead) break;
+        }
+    } else if (warp == kMmaWarp + 1) {
+        // ---- O += P V
+        constexpr uint32_t id = idesc_bf16_f32(128, D) | (1u << 16);   // (V: N contiguous)
+        uint32_t use0 = 0, n_p[2] = {0, 0};
+        for (int t = 0; take(t); leave(t), ++t) {
+            const Item &it = items[t & 1];
+            const int n_tiles = it.n_tiles, part = it.part, tiles[2] = {it.tiles[0], it.tiles[1]};
+            for (int j = 0; j < n_tiles; ++j) {
+                const uint32_t use = use0 + 2 * j + 1, v = smem_u32(ring + use % ST * C::kTile);
+                wait(&bar.kv_full[use % ST], (use / ST) & 1, dead);
+                if (j >= part) wait(&bar.checked[t & 1][j - part], (t >> 1) & 1, dead);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (j >= tiles[x]) continue;
+                    wait(&bar.p_full[x], n_p[x] & 1, dead);
+                    ++n_p[x];
+                    if (dead) break;
+                    tmem_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk)
+                            umma_tmemA(tm + 256 + x * 128, tm + 128 + x * 64 + kk * 8, sdesc_v(v + kk * 2048, C::kHalf), id, j > 0 || kk > 0);
+                        umma_commit(&bar.pv_done[x]);
                     }
-                if (bad & 0x80008000u) redo = 1;
+                    __syncwarp();
+                    issued = true;
+                }
+                if (dead) break;
+                if (elect_one()) umma_commit(&bar.kv_empty[use % ST]);
+                __syncwarp();
             }
-            // every copy has to land before the CTA's shared memory goes (where nothing gave up, they have been used)
-            for (int u = max(0, i - C::ST); u < i; ++u) {
-                bool d = false;
-                wait(&bar.kv_full[u % C::ST], (u / C::ST) & 1, d);
-                dead |= d;
+            use0 += 2 * n_tiles;
+            if (dead) break;
+        }
+    } else if (warp == kLoadWarp) {
+        // ---- copies, and the items
+        unsigned block = blockIdx.x;
+        bool more = true, asked = false;
+        uint32_t use = 0, n_q = 0;
+        for (int t = 0;; ++t) {
+            const int slot = t & 1;
+            wait(&bar.item_empty[slot], ((t >> 1) & 1) ^ 1, dead);
+            if (dead) break;
+            Item it{};
+            if (more) it = locate(a, block, gridDim.x, NT);
+            if (lane == 0) {
+                items[slot] = it;
+                redo[slot] = far[slot][0] = far[slot][1] = 0;
+                mbar_arrive(&bar.item_full[slot]);
+            }
+            __syncwarp();
+            if (!more) break;
+            if (lane < kPart && it.part + lane >= it.n_tiles) mbar_arrive(&bar.go[slot][lane]);   // (a phase of each with every item)
+            __syncwarp();
+            if (elect_one()) {  // a block that has not begun is taken over, if there is one: the next item
+                fence_proxy_async_smem();
+                mbar_arrive_expect_tx(&bar.next, 16);
+                asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_u32(&answer)),
+                             "r"(smem_u32(&bar.next))
+                             : "memory");
+            }
+            __syncwarp();
+            asked = true;
+            if (it.n_tiles > 0) {
+                wait(&bar.q_empty, (n_q & 1) ^ 1, dead);
+                ++n_q;
+                if (dead) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&bar.q_full, (uint32_t)(2 * C::NH * NT * G * 128));
+                    for (int x = 0; x < 2; ++x)
+                        for (int h = 0; h < C::NH; ++h)
+                            tma_load_4d(sQ + x * C::kTile + h * C::kHalf, &maps.q, 64 * h, 0, it.head, (int)(it.s.begin + it.q0 + x * NT), &bar.q_full);
+                }
+                __syncwarp();
+                for (int i = 0; i < 2 * it.n_tiles; ++i, ++use) {
+                    const uint32_t st = use % ST;
+                    wait(&bar.kv_empty[st], ((use / ST) & 1) ^ 1, dead);
+                    if (dead) break;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&bar.kv_full[st], C::kTile);
+                        for (int h = 0; h < C::NH; ++h)
+                            tma_load_3d(ring + st * C::kTile + h * C::kHalf, i & 1 ? &maps.v : &maps.k, 64 * h, it.head, (int)(it.s.k0 + (i / 2) * kKeys),
+                                        &bar.kv_full[st]);
+                        if ((i & 1) && i / 2 >= it.part) mbar_arrive(&bar.go[slot][i / 2 - it.part]);
+                    }
+                    __syncwarp();
+                }
+                if (dead) break;
+            }
+            wait(&bar.next, t & 1, dead);
+            if (dead) break;
+            asked = false;
+            uint32_t ok, first;
+            asm volatile(
+                "{\n .reg .b128 h;\n .reg .pred p;\n ld.shared.b128 h, [%2];\n"
+                " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+                " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}\n"
+                : "=r"(ok), "=r"(first)
+                : "r"(smem_u32(&answer))
+                : "memory");
+            more = ok != 0;
+            block = first;
+            __syncwarp();
+        }
+        if (dead) {  // what was asked for has to land before the CTA's shared memory goes
+            bool d = false;
+            for (uint32_t u = use > (uint32_t)ST ? use - ST : 0; u < use; ++u) wait(&bar.kv_full[u % ST], (u / ST) & 1, d);
+            if (n_q > 0) wait(&bar.q_full, (n_q - 1) & 1, d);
+            if (asked) {
+                for (int p = 0; p < 2; ++p) wait(&bar.next, p, d);
             }
         }
+    } else {
+        // ---- what else V's tiles hold that some row sees only in part
+        uint32_t use0 = 0;
+        for (int t = 0; take(t); leave(t), ++t) {
+            const Item &it = items[t & 1];
+            for (int k = 0; k < kPart; ++k) {
+                const int j = it.part + k;
+                if (j < it.n_tiles) {
+                    const uint32_t use = use0 + 2 * j + 1;
+                    wait(&bar.go[t & 1][k], (t >> 1) & 1, dead);   // (its copy is the barrier's present phase)
+                    wait(&bar.kv_full[use % ST], (use / ST) & 1, dead);
+                    if (dead) break;
+                    uint8_t *v = ring + (use % ST) * C::kTile;
+                    const int rows = min(kKeys, it.s.len - j * kKeys);
+                    if (rows < kKeys) {   // rows behind the sequence
+                        for (int h = 0; h < C::NH; ++h)
+                            for (int o = rows * 128 + lane * 16; o < C::kHalf; o += 512) *reinterpret_cast<uint4 *>(v + h * C::kHalf + o) = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                    }
+                    uint32_t bad = 0;
+                    for (int h = 0; h < C::NH; ++h)
+#pragma unroll 4
+                        for (int o = lane * 16; o < rows * 128; o += 512) {
+                            const uint4 w = *reinterpret_cast<const uint4 *>(v + h * C::kHalf + o);
+                            // an exponent of all ones carries into the sign's place
+                            bad |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) | ((w.z & 0x7f807f80u) + 0x00800080u) |
+                                   ((w.w & 0x7f807f80u) + 0x00800080u);
+                        }
+                    if (bad & 0x80008000u) redo[t & 1] = 1;
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(&bar.checked[t & 1][k]);
+                __syncwarp();
+            }
+            use0 += 2 * it.n_tiles;
+            if (dead) break;
+        }
+    }
+    if (dead && issued) {  // the products in flight must end before their operands and accumulators go
+        if (elect_one()) umma_commit(&bar.drained[warp - kMmaWarp]);
         __syncwarp();
-        named_sync(1, 288);
+        bool d = false;
+        wait(&bar.drained[warp - kMmaWarp], 0, d);
     }
     finish();
     if (warp == kMmaWarp) {
@@ -509,7 +648,7 @@ cudaError_t launch_one(const PromptArgs &a, cudaStream_t stream) {
     auto kern = prompt_kernel<D>;
     static std::atomic<uint64_t> allowed{0};
     if ((e = allow_smem(kern, C::kSmem, allowed)) != cudaSuccess) return e;
-    const int64_t pairs = a.Tq / (2 * NT) + std::min<int64_t>(a.B, a.Tq);   // at most: the lengths are on the device
+    const int64_t pairs = a.Tq / (2 * NT) + a.B;   // places (locate): the lengths are on the device
     mark_main_kernel(stream, true);
     kern<<<(unsigned)(pairs * a.kv_heads), kThreads, C::kSmem, stream>>>(maps, a);
     mark_main_kernel(stream, false);
