@@ -195,6 +195,25 @@ __device__ __forceinline__ void exponentials(const uint32_t (&r)[32], float2 f2,
     l2 = __fadd2_rn(l2, sum);
 }
 
+// Lane a of a group of four gives its units u[0..3] to the lanes of those numbers, and gets unit a of each.
+template <int N>
+__device__ __forceinline__ void transpose4(uint32_t (&u)[4][N]) {
+#pragma unroll
+    for (int m = 1; m < 4; m <<= 1) {
+        const bool high = threadIdx.x & m;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            if (p & m) continue;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t x = __shfl_xor_sync(0xffffffffu, high ? u[p][i] : u[p | m][i], m);
+                if (high) u[p][i] = x;
+                else u[p | m][i] = x;
+            }
+        }
+    }
+}
+
 // One row by a warp, in fp32: the plain form.
 template <int D>
 __device__ __noinline__ void plain_row(const PromptArgs &a, const PromptSeq &s, int i, int head, int g) {
@@ -362,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 wait(&bar.pv_done[x], n_pv & 1, dead);
                 ++n_pv;
             }
-            for (int k = 0; k < kPart; ++k) wait(&bar.checked[slot][k], (t >> 1) & 1, dead);
+            wait(&bar.checked[slot][kPart - 1], (t >> 1) & 1, dead);   // (the last of them)
             if (dead) break;
             tmem_fence_after();
             named_sync(3 + x, 128);               // (`far` of all the tile's rows is known)
@@ -370,9 +389,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 for (int r = warp & 3; r < it.tokens[x] * G; r += 4) plain_row<D>(a, it.s, it.q0 + x * NT + r / G, it.head, r % G);
             } else {
                 const float l = l2.x + l2.y, inv = vis > 0 ? 1.f / l : 0.f;   // (scores that are all -inf: NaN, 0 * inf)
-                const int64_t at_row = (it.s.begin + tok) * a.q_heads + it.head * G + g;
+                const int at_row = (int)((it.s.begin + tok) * a.q_heads + it.head * G + g);   // (below 2^30)
+                // Rows go out by four lanes at a time, 64 or 32 bytes of a row together: a store by a lane for its own row
+                // takes a cycle of the memory pipe for each of 32 lines (4,000 for both tiles).
+                const unsigned rows_on = __ballot_sync(0xffffffffu, on) >> (lane & ~3);
                 uint32_t scales = 0;
-#pragma unroll
+                // (a loop: unrolled, its instructions come from beyond the cache each time)
+#pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
                     if (n > 0) {
@@ -382,29 +405,39 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     float v[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = n > 0 && vis > 0 ? __uint_as_float(o[e]) * inv : 0.f;
-                    const int64_t at = at_row * D + 32 * c;
-                    if (on && a.o.out != nullptr) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4 *>(a.o.out + at + e) =
-                                make_uint4(pack2_rn(v[e], v[e + 1]), pack2_rn(v[e + 2], v[e + 3]), pack2_rn(v[e + 4], v[e + 5]), pack2_rn(v[e + 6], v[e + 7]));
-                    }
-                    if (on && a.o.mx.q != nullptr) {
+                    if (a.o.mx.q != nullptr) {
                         float amax = 0.f;
 #pragma unroll
                         for (int e = 0; e < 32; ++e) amax = fmaxf(amax, fabsf(v[e]));
                         const int E = mx_exp(amax, a.o.mx.mode);
                         const float k = __uint_as_float((uint32_t)(127 - E) << 23);
-                        uint32_t w[8];
+                        uint32_t u[4][2];
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            w[e] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * e] * k, v[4 * e + 1] * k), __NV_SATFINITE, __NV_E4M3) |
-                                   (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * e + 2] * k, v[4 * e + 3] * k), __NV_SATFINITE, __NV_E4M3) << 16;
-                        *reinterpret_cast<uint4 *>(a.o.mx.q + at) = make_uint4(w[0], w[1], w[2], w[3]);
-                        *reinterpret_cast<uint4 *>(a.o.mx.q + at + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+                            u[e / 2][e % 2] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * e] * k, v[4 * e + 1] * k), __NV_SATFINITE, __NV_E4M3) |
+                                              (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * e + 2] * k, v[4 * e + 3] * k), __NV_SATFINITE, __NV_E4M3) << 16;
                         scales |= (uint32_t)(E + 127) << (8 * c);
+                        transpose4(u);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int at = __shfl_sync(0xffffffffu, at_row, (lane & ~3) | r);
+                            if (rows_on >> r & 1u) *reinterpret_cast<uint2 *>(a.o.mx.q + at * (int64_t)D + 32 * c + (lane & 3) * 8) = make_uint2(u[r][0], u[r][1]);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (a.o.out != nullptr) {
+                        uint32_t u[4][4];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) u[e / 4][e % 4] = pack2_rn(v[2 * e], v[2 * e + 1]);
+                        transpose4(u);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int at = __shfl_sync(0xffffffffu, at_row, (lane & ~3) | r);
+                            if (rows_on >> r & 1u)
+                                *reinterpret_cast<uint4 *>(a.o.out + at * (int64_t)D + 32 * c + (lane & 3) * 8) = make_uint4(u[r][0], u[r][1], u[r][2], u[r][3]);
+                        }
+                        __syncwarp();
+                    }
                 }
                 if (on && a.o.mx.q != nullptr) {  // the head's blocks lie next to each other in a scale tile
                     uint8_t *p = a.o.mx.scale + mx_scale_offset(it.s.begin + tok, (it.head * G + g) * (D / 32), a.q_heads * D);
