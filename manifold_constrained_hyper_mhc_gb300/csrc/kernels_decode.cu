@@ -43,7 +43,7 @@ constexpr int kPairCost = 3;
 // sums [row][D], and each row's maximum and sum.
 constexpr size_t kStartBytes = (MHC_MAX_SEQUENCES + 2) * 8;
 constexpr int kFewRows = 1024;          // rows of a call up to which eight warps join one (of 1,824 parts and 8 to a pair's rows, 8 each)
-constexpr int kMaxUnitRows = 128;       // rows of all shares of a CTA
+constexpr int kMaxUnitRows = 144;       // rows of all shares of a CTA
 constexpr size_t kPartFloats = 128 + 2;
 
 template <int D, int NR_, int WR_, int NW_, int ST_>
@@ -53,7 +53,7 @@ struct Cfg {
     static constexpr int kSliceBytes = 2 * CacheLayout<D>::kGroupBytes;
     static constexpr int kRing = WT * ST * kSliceBytes;
     static constexpr int kScale = NW * kSlice * NB * 6;            // a slice's scales, K's in fp32, V's in fp16: a warp's own
-    static constexpr int kQ = NR == 16 ? NW * (D / 16) * 32 * 16 : 0;   // q's fragments
+    static constexpr int kQ = NR > 8 ? NW * (D / 16) * NTILE * 32 * 8 : 0;   // q's fragments
     static constexpr int kSmem = kRing + kScale + kQ;
     static_assert(kSmem <= 231000 && WT * ROWS <= kMaxUnitRows, "");
 };
@@ -196,7 +196,7 @@ __device__ __forceinline__ uint32_t lane_codes() {
 // A slice of 32 tokens from shared memory.  tok0: its first token; vis: tokens that rows 2 (lane % 4) and the next see,
 // vis_g: those that row lane / 4 sees; f: the factors of those rows' scores.
 template <int D, class C, bool kMask>
-__device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32_t (&q)[C::NB][2][C::NTILE * 2], const uint4 *sq,
+__device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32_t (&q)[C::NB][2][C::NTILE * 2], const uint2 *sq,
                                       float *sk, uint32_t *sv, int tok0, int len, uint32_t bad, const float (&f)[C::NTILE][2],
                                       const int (&vis)[C::NTILE][2], const int (&vis_g)[C::NTILE]) {
     using L = CacheLayout<D>;
@@ -261,9 +261,14 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
             if constexpr (NTL == 1) {
                 qb[0][0] = q[b][0][0]; qb[0][1] = q[b][0][1]; qb[0][2] = q[b][1][0]; qb[0][3] = q[b][1][1];
             } else {
-                const uint4 u0 = sq[(b * 2) * 32 + lane], u1 = sq[(b * 2 + 1) * 32 + lane];
-                qb[0][0] = u0.x; qb[1][0] = u0.y; qb[0][1] = u0.z; qb[1][1] = u0.w;
-                qb[0][2] = u1.x; qb[1][2] = u1.y; qb[0][3] = u1.z; qb[1][3] = u1.w;
+#pragma unroll
+                for (int r = 0; r < NTL; ++r)
+#pragma unroll
+                    for (int h2 = 0; h2 < 2; ++h2) {
+                        const uint2 u = sq[((b * 2 + h2) * NTL + r) * 32 + lane];
+                        qb[r][2 * h2] = u.x;
+                        qb[r][2 * h2 + 1] = u.y;
+                    }
             }
 #pragma unroll
             for (int r = 0; r < NTL; ++r) {
@@ -411,6 +416,14 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
     }
 }
 
+struct Pair {
+    Seq seq;
+    int b, pair;             // sequence; head * tiles + row tile
+    int s0, count;           // first place (slices from 0; below 0: the pair's own cost), places in this share
+    int first, n, limit;     // first slice and number of slices; tokens up to the last
+    const uint8_t *src;      // the head in page 0
+};
+
 template <int D, class C>
 __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
     using L = CacheLayout<D>;
@@ -418,9 +431,11 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *ring = smem;
     float *scale = reinterpret_cast<float *>(smem + C::kRing);
-    uint4 *sq = reinterpret_cast<uint4 *>(smem + C::kRing + C::kScale);
+    uint2 *sq = reinterpret_cast<uint2 *>(smem + C::kRing + C::kScale);
     __shared__ int64_t scan[34];
     __shared__ int64_t found[WT][2];
+    __shared__ Pair pairs[C::NW][2];           // a warp's present pair and its next one (in registers they cost the slices theirs)
+    __shared__ int2 look[C::NW][32];           // the next one's first pages
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
     const int wt = warp / WR, wr = warp % WR;                          // which share, which rows
     const int G = a.q_heads / a.c.heads;
@@ -460,19 +475,12 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
     // (from here on no barrier of the CTA)
 
     // ---- a pair, and a share's part of it
-    struct Pair {
-        Seq seq;
-        int b, pair;             // sequence; head * tiles + row tile
-        int s0, count;           // first place (slices from 0; below 0: the pair's own cost), places in this share
-        int first, n, limit;     // first slice and number of slices; tokens up to the last
-        const uint8_t *src;      // the head in page 0, the lane's 16 bytes
-    };
     auto part_of = [&](Pair &p, int64_t left) {
         p.count = (int)min((int64_t)(p.seq.slices - p.s0), left);
         p.first = max(p.s0, 0);
         p.n = max(0, p.s0 + p.count - p.first);
         p.limit = min(p.seq.len, (p.first + p.n) * kSlice);
-        p.src = a.c.data + (int64_t)(p.pair / p.seq.tiles) * (a.c.page >> 4) * L::kGroupBytes + lane * 16;
+        p.src = a.c.data + (int64_t)(p.pair / p.seq.tiles) * (a.c.page >> 4) * L::kGroupBytes;
     };
     auto pages_of = [&](const Pair &p, int k, int (&page)[2]) {  // of slice k of the part, a slice a lane
         const int64_t t0 = (int64_t)(p.first + k) * kSlice;
@@ -482,7 +490,7 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
 
     // ---- the ring
     uint32_t put = 0, got = 0;                                         // slices copied to and taken from it
-    int page_cur[2], page_next[2], page_look[2] = {-1, -1};            // pages of slices k0 + lane, the 32 after, and the next pair's
+    int page_cur[2], page_next[2] = {-1, -1};                                     // pages of slices k0 + lane, and the 32 after
     int copied = 0;                                                    // slices of this part whose copy was started
     uint32_t bad_pages = 0;                                            // two bits a copied slice, the last one's lowest
     const int page_bytes = a.c.heads * (a.c.page >> 4) * L::kGroupBytes;
@@ -499,8 +507,8 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             constexpr int kRest = kChunks - kRound;                                     // 8 or 4: lanes 0 .. for the first group, then the second
             static_assert(2 * kRest <= 32, "");
             const uint32_t dst = smem_u32(ring + (wt * ST + put % ST) * C::kSliceBytes) + lane * 16;
-            const uint8_t *src0 = p.src + (int64_t)p0 * page_bytes + ((t0 & (a.c.page - 1)) >> 4) * L::kGroupBytes;
-            const uint8_t *src1 = p.src + (int64_t)p1 * page_bytes + (((t0 + 16) & (a.c.page - 1)) >> 4) * L::kGroupBytes;
+            const uint8_t *src0 = p.src + lane * 16 + (int64_t)p0 * page_bytes + ((t0 & (a.c.page - 1)) >> 4) * L::kGroupBytes;
+            const uint8_t *src1 = p.src + lane * 16 + (int64_t)p1 * page_bytes + (((t0 + 16) & (a.c.page - 1)) >> 4) * L::kGroupBytes;
             bad_pages = bad_pages << 2 | (p0 < 0 ? 1u : 0u) | (p1 < 0 ? 2u : 0u);
             if ((p0 | p1) >= 0) {
 #pragma unroll
@@ -545,20 +553,26 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
         for (int i = 0; i < ST - 1; ++i) copy(p);
     };
 
-    Pair cur;
-    cur.b = (int)found[wt][0];
-    cur.seq = sequence(a, C::ROWS, cur.b);
-    cur.pair = (int)(found[wt][1] / (cur.seq.slices + kPairCost));
-    cur.s0 = (int)(found[wt][1] % (cur.seq.slices + kPairCost)) - kPairCost;
-    part_of(cur, end - at);
-    pages_of(cur, lane, page_cur);
-    begin(cur);
+    int now = 0;
+    {
+        Pair p;
+        p.b = (int)found[wt][0];
+        p.seq = sequence(a, C::ROWS, p.b);
+        p.pair = (int)(found[wt][1] / (p.seq.slices + kPairCost));
+        p.s0 = (int)(found[wt][1] % (p.seq.slices + kPairCost)) - kPairCost;
+        part_of(p, end - at);
+        pages_of(p, lane, page_cur);
+        if (lane == 0) pairs[warp][0] = p;
+        __syncwarp();
+        begin(p);
+    }
     while (true) {
+        const Pair &cur = pairs[warp][now];
         // ---- what comes next, ahead of its use
         at += cur.count;
         const bool more = at < end;
-        Pair next = cur;
         if (more) {
+            Pair next = cur;
             next.s0 = -kPairCost;
             if (++next.pair == a.c.heads * next.seq.tiles) {
                 next.pair = 0;
@@ -566,11 +580,15 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
                 while (next.seq.n == 0);
             }
             part_of(next, end - at);
+            int page_look[2];
             pages_of(next, lane, page_look);
+            look[warp][lane] = make_int2(page_look[0], page_look[1]);
+            if (lane == 0) pairs[warp][now ^ 1] = next;
+            __syncwarp();
         }
         const int row0 = (cur.pair % cur.seq.tiles) * C::ROWS, rows = min(C::ROWS, cur.seq.n * G - row0), head = cur.pair / cur.seq.tiles;
         // ---- q: row lane / 4 (+ 8) as B fragments, scaled by a power of two to at most 2^4
-        if constexpr (NTL == 2) load_q(cur);
+        if constexpr (NTL > 1) load_q(cur);
         uint32_t q[NB][2][NTL * 2];
         float f[NTL][2];
         int vis[NTL][2], vis_g[NTL];
@@ -605,11 +623,13 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
                 }
         }
         seen = __reduce_min_sync(0xffffffffu, seen);
-        if constexpr (NTL == 2) {
+        if constexpr (NTL > 1) {
 #pragma unroll
             for (int k = 0; k < NB; ++k)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) sq[(warp * NB * 2 + k * 2 + h) * 32 + lane] = make_uint4(q[k][h][0], q[k][h][1], q[k][h][2], q[k][h][3]);
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < NTL; ++r) sq[(((warp * NB + k) * 2 + h) * NTL + r) * 32 + lane] = make_uint2(q[k][h][r], q[k][h][NTL + r]);
             __syncwarp();
         }
 
@@ -638,18 +658,19 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             const uint32_t base = smem_u32(ring + stage * C::kSliceBytes), bad = bad_pages >> (2 * (copied - 1 - k)) & 3u;
             float *sk = scale + warp * (kSlice * NB * 3 / 2);
             uint32_t *sv = reinterpret_cast<uint32_t *>(sk + kSlice * NB);
+            if (wr * NR >= rows) continue;                             // (none of this warp's rows exists: it only copies)
             if (tok0 + kSlice <= seen && bad == 0)
-                slice<D, C, false>(w, base, q, sq + warp * (NB * 2 * 32), sk, sv, tok0, cur.seq.len, bad, f, vis, vis_g);
+                slice<D, C, false>(w, base, q, sq + warp * (NB * 2 * NTL * 32), sk, sv, tok0, cur.seq.len, bad, f, vis, vis_g);
             else
-                slice<D, C, true>(w, base, q, sq + warp * (NB * 2 * 32), sk, sv, tok0, cur.seq.len, bad, f, vis, vis_g);
+                slice<D, C, true>(w, base, q, sq + warp * (NB * 2 * NTL * 32), sk, sv, tok0, cur.seq.len, bad, f, vis, vis_g);
             __syncwarp();                                              // (the scales are written anew)
         }
         group_sync();                                                  // (every warp of the group has read its last slice)
         // ---- the next pair's first copies run while this one is written
         if (more) {
-            page_cur[0] = page_look[0];
-            page_cur[1] = page_look[1];
-            begin(next);
+            page_cur[0] = look[warp][lane].x;
+            page_cur[1] = look[warp][lane].y;
+            begin(pairs[warp][now ^ 1]);
         }
         const bool whole = cur.s0 == -kPairCost && cur.s0 + cur.count == cur.seq.slices;
         const float units = ex2((float)((int)w.top - 127 - kGain));
@@ -697,7 +718,8 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
                 if (on && g4 == 0 && a.o.lse != nullptr) a.o.lse[t * a.q_heads + hq] = sees ? (w.m[r][e] + log2f(l)) * kLn2 : -INFINITY;
             }
         if (!more) break;
-        cur = next;
+        now ^= 1;
+        __syncwarp();                                                  // (the one that was present is written over)
     }
     cp_wait<0>();
 }
@@ -825,7 +847,9 @@ cudaError_t launch_rows(const DecodeArgs &a, int num_sms, cudaStream_t stream) {
     const int64_t rows = (a.T + a.c.B - 1) / a.c.B * (a.q_heads / a.c.heads);
     if (rows <= 8) return launch_one<D, Cfg<D, 8, 1, 12, 3>>(a, num_sms, stream);
     if (rows <= 16) return launch_one<D, Cfg<D, 16, 1, 8, 4>>(a, num_sms, stream);
+    if (rows <= 24) return launch_one<D, Cfg<D, 24, 1, 6, 4>>(a, num_sms, stream);
     if (rows <= 32) return launch_one<D, Cfg<D, 16, 2, 8, 4>>(a, num_sms, stream);
+    if (rows <= 48) return launch_one<D, Cfg<D, 24, 2, 6, 4>>(a, num_sms, stream);
     return launch_one<D, Cfg<D, 16, 4, 8, 4>>(a, num_sms, stream);
 }
 
