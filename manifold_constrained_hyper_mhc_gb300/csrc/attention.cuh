@@ -172,25 +172,43 @@ __device__ __forceinline__ void write_head_row(const AttnOut &o, int64_t t, int 
 // One query's attention over n keys by one warp, in fp32: lane i holds values i * D/32 .. of the query, the keys and
 // the result.  key(j, x) and value(j, x) fetch the lane's part.  One pass with the running maximum m of the scores and
 // the sum l of their exponentials, both in base 2: what was summed before a new maximum is scaled by 2^(m_old - m).
+// Eight keys at a time, their loads in flight together (a key alone takes a load's latency, 0.7 us).
 template <int D, class Key, class Value>
 __device__ __forceinline__ float attend_row(const float (&q)[D / 32], float scale_log2, int64_t n, Key key, Value value, float (&o)[D / 32]) {
-    constexpr int N = D / 32;
+    constexpr int N = D / 32, kBatch = 8;
     float m = -INFINITY, l = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) o[i] = 0.f;
-    for (int64_t j = 0; j < n; ++j) {
-        float x[N], s = 0.f;
-        key(j, x);
+    for (int64_t j = 0; j < n; j += kBatch) {
+        float x[kBatch][N], s[kBatch], m1 = m;
 #pragma unroll
-        for (int i = 0; i < N; ++i) s = fmaf(q[i], x[i], s);
-        s = warp_sum(s) * scale_log2;
-        value(j, x);
-        const float m1 = fmaxf(m, s), base = m1 == -INFINITY ? 0.f : m1;  // (a score of -inf alone adds nothing; NaN stays)
-        const float a = ex2(m - base), p = ex2(s - base);
+        for (int u = 0; u < kBatch; ++u) key(j + u < n ? j + u : n - 1, x[u]);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            s[u] = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[u] = fmaf(q[i], x[u][i], s[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) value(j + u < n ? j + u : n - 1, x[u]);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            s[u] = warp_sum(s[u]) * scale_log2;
+            if (j + u < n) m1 = fmaxf(m1, s[u]);
+        }
+        const float base = m1 == -INFINITY ? 0.f : m1, a = ex2(m - base);  // (scores of -inf alone add nothing; NaN stays)
         m = m1;
-        l = fmaf(l, a, p);
+        l *= a;
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = fmaf(p, x[i], o[i] * a);
+        for (int i = 0; i < N; ++i) o[i] *= a;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (j + u < n) {
+                const float p = ex2(s[u] - base);
+                l += p;
+#pragma unroll
+                for (int i = 0; i < N; ++i) o[i] = fmaf(p, x[u][i], o[i]);
+            }
     }
     const float r = n > 0 ? 1.f / l : 0.f;  // no key: 0; keys whose scores are all -inf: NaN, 0 * inf
 #pragma unroll

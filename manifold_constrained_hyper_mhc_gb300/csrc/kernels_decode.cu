@@ -673,7 +673,9 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             begin(pairs[warp][now ^ 1]);
         }
         const bool whole = cur.s0 == -kPairCost && cur.s0 + cur.count == cur.seq.slices;
-        const float units = ex2((float)((int)w.top - 127 - kGain));
+        // 2^(top - 127 - kGain), below 2^-126 too
+        const int e_units = (int)w.top - kGain;
+        const float units = __uint_as_float(e_units > 0 ? (uint32_t)e_units << 23 : 0x00800000u >> (1 - e_units));
         const int slot = 2 * unit + (cur.s0 == -kPairCost ? 1 : 0);
 #pragma unroll
         for (int r = 0; r < NTL; ++r)
@@ -696,10 +698,10 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
                 const int i = (row0 + row) / G, hq = head * G + (row0 + row) % G;
                 const bool sees = cur.seq.len - cur.seq.n + i >= 0;    // what sees nothing gives zeros and -inf
                 const int64_t t = cur.seq.begin + i;
-                const float inv = units / l;                           // (keys whose scores are all -inf: NaN, 0 * inf)
+                const float inv = 1.f / l;                             // (keys whose scores are all -inf: NaN, 0 * inf)
 #pragma unroll
                 for (int k = 0; k < NB; ++k) {
-                    float v[4] = {w.o[k][0][r][e] * inv, w.o[k][0][r][2 + e] * inv, w.o[k][1][r][e] * inv, w.o[k][1][r][2 + e] * inv};
+                    float v[4] = {w.o[k][0][r][e] * inv * units, w.o[k][0][r][2 + e] * inv * units, w.o[k][1][r][e] * inv * units, w.o[k][1][r][2 + e] * inv * units};
                     if (!sees) v[0] = v[1] = v[2] = v[3] = 0.f;
                     const int64_t o = (t * a.q_heads + hq) * (int64_t)D + 32 * k + 4 * g4;
                     if (on && a.o.out != nullptr) *reinterpret_cast<uint2 *>(a.o.out + o) = make_uint2(pack2_rn(v[0], v[1]), pack2_rn(v[2], v[3]));

@@ -34,7 +34,7 @@ using namespace ptx;
 constexpr int kKeys = 128;                           // of a tile
 constexpr float kLazy = 8.f;
 constexpr float kFar = 268435456.f;                  // 2^28: from here on s - m rounded once may be off by 2^4
-constexpr uint64_t kWaitLimitNs = 1000000000ull;     // 1 s per wait
+constexpr uint64_t kWaitLimitNs = 20000000000ull;    // 20 s per wait: 32 rows of a warp over 2^20 keys, plainly, take 3 s
 constexpr int kMmaWarp = 8 /* and 9 */, kLoadWarp = 10, kThreads = 12 * 32;
 
 template <int D>

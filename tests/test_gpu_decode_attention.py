@@ -228,3 +228,40 @@ def test_more_sequences_than_threads(mhc, ws):
     q = queries(b.T, 2, 64, 4)
     o = mhc.decode_attention_mxfp4(q, b.cache, b.page_table, b.seq_lens, b.offsets, want_lse=True, workspace=ws)
     check(o, b, q, 0.125)
+
+
+@pytest.mark.parametrize("E", [-126, -124, -100, 100])
+def test_values_at_the_ends_of_the_range(mhc, ws, E):
+    """V of the smallest scales, fp32's subnormals among the results, and large ones."""
+    D = 64
+    b = ref.Batch(mhc, [90, 40000], [1, 1], 1, D, 32, seed=3)
+    for i, n in enumerate(b.lens):
+        v = torch.randn(n, 1, D, dtype=torch.float64, device="cuda", generator=torch.Generator("cuda").manual_seed(i)) * 2.0 ** E
+        pos = torch.arange(n, device="cuda")
+        ref.put(b.cache, b.page_table, i, pos, 1, *ref.quantize4(v, 0))
+        b.v[i] = ref.get(b.cache, b.page_table, i, pos, 1)
+    q = queries(2, 4, D, 4)
+    o = mhc.decode_attention_mxfp4(q, b.cache, b.page_table, b.seq_lens, b.offsets, workspace=ws)["attn_out"]
+    for i in range(2):
+        out, _, tol, _ = ref.attend(q[i:i + 1], b.k[i], b.v[i], D ** -0.5, "f16")
+        ref.check_out(o[i:i + 1], out, tol)
+        assert float(o[i].abs().amax()) > 0
+
+
+@pytest.mark.parametrize("n,Hq", [(1, 4), (6, 14)])
+def test_a_query_that_is_not_finite(mhc, ws, n, Hq):
+    """It makes its own rows NaN, and no other."""
+    D = 128
+    b = ref.Batch(mhc, [300, 70], [n, n], 2, D, 32, seed=3)
+    q = queries(b.T, Hq, D, 4)
+    want = mhc.decode_attention_mxfp4(q, b.cache, b.page_table, b.seq_lens, b.offsets, workspace=ws)["attn_out"]
+    q[0, 1, 5], q[n, Hq - 1, 7] = math.nan, math.inf
+    o = mhc.decode_attention_mxfp4(q, b.cache, b.page_table, b.seq_lens, b.offsets, workspace=ws)["attn_out"]
+    bad = torch.zeros(b.T, Hq, dtype=torch.bool, device="cuda")
+    bad[0, 1], bad[n, Hq - 1] = True, True
+    assert bool(o[bad].isnan().all())
+    for i in range(2):   # (a rescale at another time may round otherwise: held to the bound)
+        out, _, tol, _ = ref.attend(q[i * n:i * n + n].nan_to_num(0, 0, 0), b.k[i], b.v[i], D ** -0.5, "f16")
+        keep = ~bad[i * n:i * n + n]
+        ref.check_out(o[i * n:i * n + n][keep], out[keep], tol[keep])
+    assert bool(want.isfinite().all())

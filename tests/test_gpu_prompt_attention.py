@@ -207,3 +207,45 @@ def test_many_short_prompts(mhc, ws):
     q, k, v = make(T, 2, 64, 1), make(T, 1, 64, 2), make(T, 1, 64, 3)
     o = mhc.prompt_attention(q, k, v, cum(n), cum(n), want_lse=True, workspace=ws)
     check(o, q, k, v, n, n, 0.125)
+
+
+def test_no_keys_at_all(mhc, ws):
+    q = make(40, 4, 64, 1)
+    k = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    o = mhc.prompt_attention(q, k, k, cum([3, 37]), cum([0, 0]), want_lse=True, want_mxfp8=True, workspace=ws)
+    assert bool((o["attn_out"] == 0).all()) and bool((o["lse"] == -math.inf).all()) and bool((o["attn_fp8"] == 0).all())
+    mhc.check_status(ws)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_query_that_is_not_finite(mhc, ws, D):
+    """It makes its own row NaN, and no other."""
+    n = [200, 31]
+    q, k, v = make(231, 6, D, 1), make(231, 2, D, 2), make(231, 2, D, 3)
+    want = mhc.prompt_attention(q, k, v, cum(n), cum(n), workspace=ws)["attn_out"]
+    q[100, 4, 9], q[205, 0, 1] = math.nan, -math.inf
+    o = mhc.prompt_attention(q, k, v, cum(n), cum(n), workspace=ws)["attn_out"]
+    bad = torch.zeros(231, 6, dtype=torch.bool, device="cuda")
+    bad[100, 4], bad[205, 0] = True, True
+    assert bool(o[bad].isnan().all()) and bool(o[~bad].isfinite().all())
+    assert torch.equal(o[~bad], want[~bad])
+
+
+def test_more_sequences_than_rows(mhc, ws):
+    """Empty sequences before, between and behind the others, many more than there are rows."""
+    n = [0] * 700 + [1] + [0] * 90 + [5] + [0] * 1100
+    q, k, v = make(6, 4, 64, 1), make(6, 4, 64, 2), make(6, 4, 64, 3)
+    o = mhc.prompt_attention(q, k, v, cum(n), cum(n), want_lse=True, workspace=ws)
+    check(o, q, k, v, n, n, 0.125)
+
+
+def test_rows_that_take_the_plain_way_over_many_keys(mhc, ws):
+    """A value that is not finite behind 20,000 others: its tile's rows are computed plainly, the waits hold."""
+    L = 20000
+    q, k, v = make(70, 8, 128, 1), make(L, 1, 128, 2), make(L, 1, 128, 3)
+    v[L - 1] = math.inf
+    o = mhc.prompt_attention(q, k, v, cum([70]), cum([L]), workspace=ws)["attn_out"]
+    mhc.check_status(ws)
+    want, _, tol, _ = ref.attend(q[:69], k[:L - 1].double(), v[:L - 1].double(), 128 ** -0.5, "bf16")
+    ref.check_out(o[:69], want, tol)
+    assert bool((~o[69].isfinite()).all())
