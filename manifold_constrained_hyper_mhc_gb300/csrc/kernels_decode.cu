@@ -43,8 +43,7 @@ constexpr int kPairCost = 3;
 // sums [row][D], and each row's maximum and sum.
 constexpr size_t kStartBytes = (MHC_MAX_SEQUENCES + 2) * 8;
 constexpr int kFewRows = 1024;          // rows of a call up to which eight warps join one (of 1,824 parts and 8 to a pair's rows, 8 each)
-constexpr int kMaxUnitRows = 144;       // rows of all shares of a CTA
-constexpr size_t kPartFloats = 128 + 2;
+constexpr size_t kPartFloats = 144 * (128 + 2);   // of all shares of a CTA: 144 rows of D = 128, 192 of D = 64
 
 template <int D, int NR_, int WR_, int NW_, int ST_>
 struct Cfg {
@@ -55,7 +54,7 @@ struct Cfg {
     static constexpr int kScale = NW * kSlice * NB * 6;            // a slice's scales, K's in fp32, V's in fp16: a warp's own
     static constexpr int kQ = NR > 8 ? NW * (D / 16) * NTILE * 32 * 8 : 0;   // q's fragments
     static constexpr int kSmem = kRing + kScale + kQ;
-    static_assert(kSmem <= 231000 && WT * ROWS <= kMaxUnitRows, "");
+    static_assert(kSmem <= 226000 && WT * ROWS * (D + 2) <= kPartFloats, "");
 };
 
 // The parts of a launch.
@@ -849,15 +848,17 @@ cudaError_t launch_rows(const DecodeArgs &a, int num_sms, cudaStream_t stream) {
     const int64_t rows = (a.T + a.c.B - 1) / a.c.B * (a.q_heads / a.c.heads);
     if (rows <= 8) return launch_one<D, Cfg<D, 8, 1, 12, 3>>(a, num_sms, stream);
     if (rows <= 16) return launch_one<D, Cfg<D, 16, 1, 8, 4>>(a, num_sms, stream);
-    if (rows <= 24) return launch_one<D, Cfg<D, 24, 1, 6, 4>>(a, num_sms, stream);
+    // (24 rows a warp: six warps where eight warps' parts do not fit the workspace)
+    constexpr int kW = D == 64 ? 8 : 6;
+    if (rows <= 24) return launch_one<D, Cfg<D, 24, 1, kW, 4>>(a, num_sms, stream);
     if (rows <= 32) return launch_one<D, Cfg<D, 16, 2, 8, 4>>(a, num_sms, stream);
-    if (rows <= 48) return launch_one<D, Cfg<D, 24, 2, 6, 4>>(a, num_sms, stream);
+    if (rows <= 48) return launch_one<D, Cfg<D, 24, 2, kW, 4>>(a, num_sms, stream);
     return launch_one<D, Cfg<D, 16, 4, 8, 4>>(a, num_sms, stream);
 }
 
 }  // namespace
 
-size_t decode_workspace_bytes() { return kControlBytes + kStartBytes + (size_t)2 * kMaxCtas * kMaxUnitRows * kPartFloats * 4; }
+size_t decode_workspace_bytes() { return kControlBytes + kStartBytes + (size_t)2 * kMaxCtas * kPartFloats * 4; }
 
 cudaError_t launch_decode(const DecodeArgs &a, int num_sms, cudaStream_t stream) {
     return a.D == 128 ? launch_rows<128>(a, num_sms, stream) : launch_rows<64>(a, num_sms, stream);
