@@ -442,9 +442,11 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
     const Parts parts = parts_of<D, C>(a.ctrl, gridDim.x);
     asm volatile("griddepcontrol.launch_dependents;");                 // (the second kernel waits for all of this one)
 
-    // ---- the shares of the line
-    int64_t total = 0;
-    for (int base = 0; base < a.c.B; base += NT) {
+    // ---- the shares of the line: a sequence a thread, the sum of what is before each (for those beyond NT a second time,
+    // once the line's length is known)
+    int64_t total;
+    const int64_t c0 = tid < a.c.B ? cost(a, sequence(a, C::ROWS, tid)) : 0, before0 = block_scan<NT>(c0, total, scan);
+    for (int base = NT; base < a.c.B; base += NT) {
         int64_t all;
         block_scan<NT>(base + tid < a.c.B ? cost(a, sequence(a, C::ROWS, base + tid)) : 0, all, scan);
         total += all;
@@ -452,20 +454,24 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
     const int64_t share = share_of(total, (int64_t)gridDim.x * WT);
     {
         const int64_t first = share * blockIdx.x * WT;
-        int64_t before = 0;
-        for (int64_t base = 0; base < a.c.B; base += NT) {
-            int64_t all;
-            const int64_t c = base + tid < a.c.B ? cost(a, sequence(a, C::ROWS, (int)base + tid)) : 0;
-            const int64_t mine = before + block_scan<NT>(c, all, scan);
+        auto place = [&](int b, int64_t mine, int64_t c) {  // sequence b is on the line from `mine` on: whose shares begin there
             for (int w = 0; w < WT; ++w)
                 if (first + w * share >= mine && first + w * share < mine + c) {
-                    found[w][0] = base + tid;
+                    found[w][0] = b;
                     found[w][1] = first + w * share - mine;
                 }
-            if (blockIdx.x == 0 && base + tid < a.c.B) parts.start[base + tid] = mine;
+            if (blockIdx.x == 0 && b < a.c.B) parts.start[b] = mine;
+        };
+        place(tid, before0, c0);
+        int64_t before = 0;
+        for (int base = 0; base < a.c.B && a.c.B > NT; base += NT) {
+            int64_t all;
+            const int b = base + tid;
+            const int64_t c = b < a.c.B ? cost(a, sequence(a, C::ROWS, b)) : 0, mine = before + block_scan<NT>(c, all, scan);
+            if (base > 0) place(b, mine, c);
             before += all;
         }
-        if (blockIdx.x == 0 && tid == 0) parts.start[a.c.B] = before;
+        if (blockIdx.x == 0 && tid == 0) parts.start[a.c.B] = total;
     }
     __syncthreads();
     int64_t at = share * unit;
