@@ -5,11 +5,11 @@
 // The cache is read once (17/32 byte a value): that is the floor, and what must not be in its way are the conversions,
 // about three instructions for every four codes.  The keys of all (sequence, kv head) pairs are one long line of slices of
 // 32 tokens, cut into equal shares whatever the lengths (the host knows none of them), a share for each warp of one CTA an
-// SM (a group of warps where there are many rows).  A warp keeps its own running maximum, sum and accumulators, and its
+// SM.  A warp keeps its own running maximum, sum and accumulators, and its
 // copies run ahead into its own ring in shared memory: no two warps wait for each other.  A pair that lies in one share is
 // finished there; of the others each share leaves its part in the workspace, and a second kernel joins them.
 //
-// The rows of a pair are the tokens times the heads of the group.  For NR = 8 or 16 rows a warp computes, on the legacy
+// The rows of a pair are the tokens times the heads of the group, in tiles of 8, 16 or 24.  A warp computes, on the legacy
 // tensor path (operands from registers: the codes are converted there and never written back),
 //   S^T [32 tokens x rows] = K Q^T   m16n8k16, fp16: E2M1 codes are exact there, and a row of q scaled by a power of two
 //                                    has all its 8 bits; each 32 values' sum is multiplied by its scale in fp32
@@ -45,16 +45,16 @@ constexpr size_t kStartBytes = (MHC_MAX_SEQUENCES + 2) * 8;
 constexpr int kFewRows = 1024;          // rows of a call up to which eight warps join one (of 1,824 parts and 8 to a pair's rows, 8 each)
 constexpr size_t kPartFloats = 144 * (128 + 2);   // of all shares of a CTA: 144 rows of D = 128, 192 of D = 64
 
-template <int D, int NR_, int WR_, int NW_, int ST_>
+template <int D, int ROWS_, int NW_, int ST_>
 struct Cfg {
-    static constexpr int NR = NR_, WR = WR_, NW = NW_, ST = ST_;   // rows a warp, warps over rows, warps, ring stages
-    static constexpr int WT = NW / WR, ROWS = NR * WR, NT = NW * 32, NB = D / 32, NTILE = NR / 8;
+    static constexpr int ROWS = ROWS_, NW = NW_, ST = ST_;         // rows of a warp, warps, ring stages of a warp
+    static constexpr int NT = NW * 32, NB = D / 32, NTILE = ROWS / 8;
     static constexpr int kSliceBytes = 2 * CacheLayout<D>::kGroupBytes;
-    static constexpr int kRing = WT * ST * kSliceBytes;
+    static constexpr int kRing = NW * ST * kSliceBytes;
     static constexpr int kScale = NW * kSlice * NB * 6;            // a slice's scales, K's in fp32, V's in fp16: a warp's own
-    static constexpr int kQ = NR > 8 ? NW * (D / 16) * NTILE * 32 * 8 : 0;   // q's fragments
+    static constexpr int kQ = ROWS > 8 ? NW * (D / 16) * NTILE * 32 * 8 : 0;   // q's fragments
     static constexpr int kSmem = kRing + kScale + kQ;
-    static_assert(kSmem <= 226000 && WT * ROWS * (D + 2) <= kPartFloats, "");
+    static_assert(kSmem <= 226000 && NW * ROWS * (D + 2) <= kPartFloats, "");
 };
 
 // The parts of a launch.
@@ -66,7 +66,7 @@ template <int D, class C>
 __host__ __device__ __forceinline__ Parts parts_of(unsigned int *ctrl, int ctas) {
     uint8_t *p = reinterpret_cast<uint8_t *>(ctrl) + kControlBytes;
     float *o = reinterpret_cast<float *>(p + kStartBytes);
-    return {reinterpret_cast<int64_t *>(p), o, o + (size_t)2 * ctas * C::WT * C::ROWS * D};
+    return {reinterpret_cast<int64_t *>(p), o, o + (size_t)2 * ctas * C::NW * C::ROWS * D};
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -426,19 +426,18 @@ struct Pair {
 template <int D, class C>
 __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
     using L = CacheLayout<D>;
-    constexpr int NB = C::NB, NTL = C::NTILE, WT = C::WT, WR = C::WR, ST = C::ST, NT = C::NT, NR = C::NR;
+    constexpr int NB = C::NB, NTL = C::NTILE, NW = C::NW, ST = C::ST, NT = C::NT;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *ring = smem;
     float *scale = reinterpret_cast<float *>(smem + C::kRing);
     uint2 *sq = reinterpret_cast<uint2 *>(smem + C::kRing + C::kScale);
     __shared__ int64_t scan[34];
-    __shared__ int64_t found[WT][2];
+    __shared__ int64_t found[NW][2];
     __shared__ Pair pairs[C::NW][2];           // a warp's present pair and its next one (in registers they cost the slices theirs)
     __shared__ int2 look[C::NW][32];           // the next one's first pages
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
-    const int wt = warp / WR, wr = warp % WR;                          // which share, which rows
     const int G = a.q_heads / a.c.heads;
-    const int unit = (int)blockIdx.x * WT + wt;
+    const int unit = (int)blockIdx.x * NW + warp;                      // which share
     const Parts parts = parts_of<D, C>(a.ctrl, gridDim.x);
     asm volatile("griddepcontrol.launch_dependents;");                 // (the second kernel waits for all of this one)
 
@@ -451,11 +450,11 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
         block_scan<NT>(base + tid < a.c.B ? cost(a, sequence(a, C::ROWS, base + tid)) : 0, all, scan);
         total += all;
     }
-    const int64_t share = share_of(total, (int64_t)gridDim.x * WT);
+    const int64_t share = share_of(total, (int64_t)gridDim.x * NW);
     {
-        const int64_t first = share * blockIdx.x * WT;
+        const int64_t first = share * blockIdx.x * NW;
         auto place = [&](int b, int64_t mine, int64_t c) {  // sequence b is on the line from `mine` on: whose shares begin there
-            for (int w = 0; w < WT; ++w)
+            for (int w = 0; w < NW; ++w)
                 if (first + w * share >= mine && first + w * share < mine + c) {
                     found[w][0] = b;
                     found[w][1] = first + w * share - mine;
@@ -511,23 +510,21 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             constexpr int kChunks = L::kGroupBytes / 16, kRound = kChunks / 32 * 32;   // whole warps' rounds, then both groups' rest
             constexpr int kRest = kChunks - kRound;                                     // 8 or 4: lanes 0 .. for the first group, then the second
             static_assert(2 * kRest <= 32, "");
-            const uint32_t dst = smem_u32(ring + (wt * ST + put % ST) * C::kSliceBytes) + lane * 16;
+            const uint32_t dst = smem_u32(ring + (warp * ST + put % ST) * C::kSliceBytes) + lane * 16;
             const uint8_t *src0 = p.src + lane * 16 + (int64_t)p0 * page_bytes + ((t0 & (a.c.page - 1)) >> 4) * L::kGroupBytes;
             const uint8_t *src1 = p.src + lane * 16 + (int64_t)p1 * page_bytes + (((t0 + 16) & (a.c.page - 1)) >> 4) * L::kGroupBytes;
             bad_pages = bad_pages << 2 | (p0 < 0 ? 1u : 0u) | (p1 < 0 ? 2u : 0u);
             if ((p0 | p1) >= 0) {
 #pragma unroll
-                for (int i = 0; i < kRound * 16; i += WR * 512) {
-                    const int o = i + wr * 512;
-                    if (WR * 512 > kRound * 16 && o >= kRound * 16) continue;   // (D = 64 has two rounds for four warps)
-                    cp_async16(dst + o, src0 + o);
-                    cp_async16(dst + o + L::kGroupBytes, src1 + o);
+                for (int i = 0; i < kRound * 16; i += 512) {
+                    cp_async16(dst + i, src0 + i);
+                    cp_async16(dst + i + L::kGroupBytes, src1 + i);
                 }
-                if (wr == 0 && lane < 2 * kRest)
+                if (lane < 2 * kRest)
                     cp_async16(dst + kRound * 16 + (lane < kRest ? 0 : L::kGroupBytes - kRest * 16), (lane < kRest ? src0 : src1 - kRest * 16) + kRound * 16);
             } else if (p0 >= 0 || p1 >= 0) {
                 const uint8_t *src = p0 >= 0 ? src0 : src1;
-                for (int i = wr * 512; i < L::kGroupBytes; i += WR * 512)
+                for (int i = 0; i < L::kGroupBytes; i += 512)
                     if (i + lane * 16 < L::kGroupBytes) cp_async16(dst + i + (p0 >= 0 ? 0 : L::kGroupBytes), src + i);
             }
             ++put;
@@ -535,16 +532,12 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
         }
         cp_commit();
     };
-    auto group_sync = [&]() {
-        if constexpr (WR == 1) __syncwarp();
-        else named_sync(1 + wt, 32 * WR);
-    };
     uint4 qw[NTL][NB];                                                 // q of the lane's rows, 8 values of each block
     auto load_q = [&](const Pair &p) {
         const int row0 = (p.pair % p.seq.tiles) * C::ROWS, rows = min(C::ROWS, p.seq.n * G - row0), head = p.pair / p.seq.tiles;
 #pragma unroll
         for (int r = 0; r < NTL; ++r) {
-            const int row = wr * NR + r * 8 + g4, i = (row0 + row) / G;
+            const int row = r * 8 + g4, i = (row0 + row) / G;
             const uint16_t *x = a.q + (p.seq.begin + i) * a.q_stride + (head * G + (row0 + row) % G) * D + t4 * 8;
 #pragma unroll
             for (int k = 0; k < NB; ++k) qw[r][k] = row < rows ? __ldg(reinterpret_cast<const uint4 *>(x + k * 32)) : make_uint4(0, 0, 0, 0);
@@ -561,10 +554,10 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
     int now = 0;
     {
         Pair p;
-        p.b = (int)found[wt][0];
+        p.b = (int)found[warp][0];
         p.seq = sequence(a, C::ROWS, p.b);
-        p.pair = (int)(found[wt][1] / (p.seq.slices + kPairCost));
-        p.s0 = (int)(found[wt][1] % (p.seq.slices + kPairCost)) - kPairCost;
+        p.pair = (int)(found[warp][1] / (p.seq.slices + kPairCost));
+        p.s0 = (int)(found[warp][1] % (p.seq.slices + kPairCost)) - kPairCost;
         part_of(p, end - at);
         pages_of(p, lane, page_cur);
         if (lane == 0) pairs[warp][0] = p;
@@ -600,7 +593,7 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
         int seen = 0x7fffffff;                                         // tokens that every row sees
 #pragma unroll
         for (int r = 0; r < NTL; ++r) {
-            const int row = wr * NR + r * 8 + g4;
+            const int row = r * 8 + g4;
             vis_g[r] = row < rows ? max(0, cur.seq.len - cur.seq.n + (row0 + row) / G + 1) : 0;
             seen = min(seen, row < rows ? vis_g[r] : 0x7fffffff);
             float x[NB][8], amax = 0.f;
@@ -655,22 +648,21 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
 
         for (int k = 0; k < cur.n; ++k) {
             cp_wait<ST - 2>();
-            group_sync();                                              // slice k is there for all, and k - 1 is done with
+            __syncwarp();                                              // slice k is there for all lanes, and k - 1 is done with
             copy(cur);
-            const int stage = wt * ST + got % ST;
+            const int stage = warp * ST + got % ST;
             ++got;
             const int tok0 = (cur.first + k) * kSlice;
             const uint32_t base = smem_u32(ring + stage * C::kSliceBytes), bad = bad_pages >> (2 * (copied - 1 - k)) & 3u;
             float *sk = scale + warp * (kSlice * NB * 3 / 2);
             uint32_t *sv = reinterpret_cast<uint32_t *>(sk + kSlice * NB);
-            if (wr * NR >= rows) continue;                             // (none of this warp's rows exists: it only copies)
             if (tok0 + kSlice <= seen && bad == 0)
                 slice<D, C, false>(w, base, q, sq + warp * (NB * 2 * NTL * 32), sk, sv, tok0, cur.seq.len, bad, f, vis, vis_g);
             else
                 slice<D, C, true>(w, base, q, sq + warp * (NB * 2 * NTL * 32), sk, sv, tok0, cur.seq.len, bad, f, vis, vis_g);
             __syncwarp();                                              // (the scales are written anew)
         }
-        group_sync();                                                  // (every warp of the group has read its last slice)
+        __syncwarp();                                                  // (every lane has read the last slice)
         // ---- the next pair's first copies run while this one is written
         if (more) {
             page_cur[0] = look[warp][lane].x;
@@ -687,7 +679,7 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
 #pragma unroll
             for (int e = 0; e < 2; ++e) {  // row 8 r + 2 t4 + e, values 32 k + 4 g4 ..
                 const float l = column_sum(w.l[r][e]);
-                const int row = wr * NR + r * 8 + 2 * t4 + e;
+                const int row = r * 8 + 2 * t4 + e;
                 const bool on = row < rows;
                 if (!whole) {
                     float *o = parts.o + ((size_t)slot * C::ROWS + row) * D + 4 * g4;
@@ -747,7 +739,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) join_kernel(c
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (s.b < 0) return;
     const Parts parts = parts_of<D, C>(a.ctrl, ctas);
-    const int64_t start = __ldcg(parts.start + s.b), share = share_of(__ldcg(parts.start + a.c.B), (int64_t)ctas * C::WT);
+    const int64_t start = __ldcg(parts.start + s.b), share = share_of(__ldcg(parts.start + a.c.B), (int64_t)ctas * C::NW);
     const int r = (int)(t - s.begin) * G + hq % G, row = r % C::ROWS;
     const int64_t place = start + (int64_t)((hq / G) * seq.tiles + r / C::ROWS) * (seq.slices + kPairCost);
     const int u0 = (int)(place / share), u1 = (int)((place + seq.slices + kPairCost - 1) / share);
@@ -848,18 +840,18 @@ cudaError_t launch_one(const DecodeArgs &a, int num_sms, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, join_kernel<D, C, 1>, a, ctas);
 }
 
-// By the rows of an average sequence: as few row tiles as there can be, and no more rows than are needed.
+// By the rows of an average sequence (its tokens times a group's heads): row tiles of 8, 16 or 24, whichever's tiles take
+// least.  A tile of 24 takes as long as 1.2 of 16 for D = 64 and as 1.75 of them for D = 128, where six warps of it fill
+// the registers and the workspace (64 sequences of 8,000 tokens, 48 rows: 252 against 310 us, and 503 against 446; 24 rows of
+// one sequence of 32,003: 22.2 against 24.8, and 30.7 against 32.7); one of 16 as 1.7 of 8.  Warps that share a slice
+// over more rows, and wait for each other at every slice, are slower than tiles that read it again (D = 128, 42 rows:
+// 44.5 us against 39.3).
 template <int D>
 cudaError_t launch_rows(const DecodeArgs &a, int num_sms, cudaStream_t stream) {
     const int64_t rows = (a.T + a.c.B - 1) / a.c.B * (a.q_heads / a.c.heads);
-    if (rows <= 8) return launch_one<D, Cfg<D, 8, 1, 12, 3>>(a, num_sms, stream);
-    if (rows <= 16) return launch_one<D, Cfg<D, 16, 1, 8, 4>>(a, num_sms, stream);
-    // (24 rows a warp: six warps where eight warps' parts do not fit the workspace)
-    constexpr int kW = D == 64 ? 8 : 6;
-    if (rows <= 24) return launch_one<D, Cfg<D, 24, 1, kW, 4>>(a, num_sms, stream);
-    if (rows <= 32) return launch_one<D, Cfg<D, 16, 2, 8, 4>>(a, num_sms, stream);
-    if (rows <= 48) return launch_one<D, Cfg<D, 24, 2, kW, 4>>(a, num_sms, stream);
-    return launch_one<D, Cfg<D, 16, 4, 8, 4>>(a, num_sms, stream);
+    if (rows <= 8) return launch_one<D, Cfg<D, 8, 12, 3>>(a, num_sms, stream);
+    if ((rows + 23) / 24 * (D == 64 ? 120 : 175) <= (rows + 15) / 16 * 100) return launch_one<D, Cfg<D, 24, D == 64 ? 8 : 6, 4>>(a, num_sms, stream);
+    return launch_one<D, Cfg<D, 16, 8, 4>>(a, num_sms, stream);
 }
 
 }  // namespace
