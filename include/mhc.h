@@ -483,9 +483,9 @@ MHC_API mhc_status mhc_kv_read_mxfp4(const uint8_t *cache, int64_t pages, int64_
                                      const int32_t *offsets, const int32_t *seq_lens, const int32_t *page_table, int64_t B,
                                      int64_t table_width, int64_t T, mhc_bf16 *k_out, mhc_bf16 *v_out, void *stream);
 
-/* Workspace bytes of the two attentions, whatever their sizes (zero-filled before the first use; every call that
- * completes leaves it ready).  Calls that share a decode workspace must be ordered; a prompt workspace (the status word
- * alone, as the products') may be shared by any calls. */
+/* Workspace bytes of the two attentions, whatever their sizes (the status word zero-filled before the first use, as the
+ * other workspaces').  Calls that share a decode workspace must be ordered (it holds the parts of long sequences between
+ * a call's two launches); a prompt workspace, the status word alone as the products', may be shared by any calls. */
 MHC_API size_t mhc_decode_workspace_size(void);
 MHC_API size_t mhc_prompt_workspace_size(void);
 
@@ -496,7 +496,9 @@ MHC_API size_t mhc_prompt_workspace_size(void);
  *   attn_fp8, attn_scales   the result as MXFP8 [T][q_heads * head_dim] (scale tiles as above, one scale per 32 values,
  *                scale_mode), quantized from fp32 in one rounding, or both NULL; one form of the result is required
  *   lse          [T][q_heads] fp32 max s + ln sum_j p_j, for a join with other keys, or NULL
- * Deterministic. */
+ * P is held in fp16 and V's scales relative to the largest so far: contributions below 2^-25 of the largest weight times
+ * the largest V of a sequence lose bits.  Meant for a few tokens a sequence; whole chunks go through mhc_kv_read_mxfp4 and
+ * mhc_prompt_attention.  Deterministic.  Two launches, the second for the sequences that were cut. */
 MHC_API mhc_status mhc_decode_attention_mxfp4(const mhc_bf16 *q, int64_t q_stride, int64_t T, int64_t q_heads,
                                               const int32_t *offsets, const int32_t *seq_lens, const int32_t *page_table,
                                               int64_t B, int64_t table_width, const uint8_t *cache, int64_t pages,
@@ -505,7 +507,9 @@ MHC_API mhc_status mhc_decode_attention_mxfp4(const mhc_bf16 *q, int64_t q_strid
                                               float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /* The same over packed bf16 keys and values: the rows q_offsets[b] .. of q are the last of the keys k_offsets[b] .. of k
- * and v (with as many of both: a whole prompt; with more keys: a later chunk of it after its prefix). */
+ * and v (with as many of both: a whole prompt; with more keys: a later chunk of it after its prefix).  P is
+ * held in bf16.  Rows whose scores pass 2^28, or that share a tile of rows with a value of v that is not finite among keys
+ * that some of them see and some do not, are computed plainly in fp32, slowly.  Deterministic.  One launch. */
 MHC_API mhc_status mhc_prompt_attention(const mhc_bf16 *q, int64_t q_stride, const mhc_bf16 *k, int64_t k_stride,
                                         const mhc_bf16 *v, int64_t v_stride, int64_t Tq, int64_t Tk, int64_t q_heads,
                                         int64_t kv_heads, int64_t head_dim, const int32_t *q_offsets, const int32_t *k_offsets,
