@@ -5,9 +5,9 @@
 // The cache is read once (17/32 byte a value): that is the floor, and what must not be in its way are the conversions,
 // about three instructions for every four codes.  The keys of all (sequence, kv head) pairs are one long line of slices of
 // 32 tokens, cut into equal shares whatever the lengths (the host knows none of them), a share for each warp of one CTA an
-// SM.  A warp keeps its own running maximum, sum and accumulators, and its
-// copies run ahead into its own ring in shared memory: no two warps wait for each other.  A pair that lies in one share is
-// finished there; of the others each share leaves its part in the workspace, and a second kernel joins them.
+// SM.  A warp keeps its own running maximum, sum and accumulators, and its copies run ahead into its own ring in shared
+// memory: no two warps wait for each other.  A pair that lies in one share is finished there; of the others each share
+// leaves its part in the workspace, and a second kernel joins them.
 //
 // The rows of a pair are the tokens times the heads of the group, in tiles of 8, 16 or 24.  A warp computes, on the legacy
 // tensor path (operands from registers: the codes are converted there and never written back),
@@ -19,6 +19,11 @@
 // The k order of a product is free: a lane takes 8 neighbouring codes of K (ldmatrix), and 4 of V for two tokens
 // (ldmatrix.trans), as they lie; q and the output follow that order.  P crosses from one product's layout to the other's
 // by movmatrix.
+//
+// Measured: 64 sequences of 100 to 16,000 tokens, 64 / 8 heads of 128: 111 us, 75 % of the copy rate (copies alone take 90 % of
+// that, the arithmetic alone too: about 600 instructions a slice, half of them on the ALU pipe); 32,003 tokens, 6 queries of
+// 56 / 8 heads: 39 us, bound by the conversions, which each row tile does anew; 3 sequences of 60,001 to 131,000, 32 / 4
+// heads of 64: 28 us, 38 %, bound by the arithmetic (half the bytes a token for the same softmax).
 #include "attention.cuh"
 #include "mhc.h"
 #include "sm100_ptx.cuh"
