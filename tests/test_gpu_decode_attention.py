@@ -91,6 +91,15 @@ def test_long_sequences_are_split_and_joined(mhc, ws, D, Hkv, G, lens):
     mhc.check_status(ws)
 
 
+def test_many_rows_and_cut_sequences(mhc, ws):
+    """More rows than eight warps each are joined by, most of their sequences cut."""
+    lens = [2000 + 37 * i for i in range(40)]
+    b = ref.Batch(mhc, lens, [1] * 40, 8, 64, 64, seed=12)
+    q = queries(b.T, 32, 64, 12)
+    o = mhc.decode_attention_mxfp4(q, b.cache, b.page_table, b.seq_lens, b.offsets, want_lse=True, want_mxfp8=True, workspace=ws)
+    check(o, b, q, 0.125)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("spread,qs", [(6.0, 1.0), (0.0, 40.0), (0.0, 2.0 ** -30), (12.0, 2.0 ** -20)])
 def test_scales_and_queries_of_every_magnitude(mhc, ws, D, spread, qs):
