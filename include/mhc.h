@@ -454,7 +454,9 @@ MHC_API mhc_status mhc_expert_linear_mxfp8(const uint8_t *x_fp8, const uint8_t *
  *     infinities there included.
  * q, k and v may be parts of wider rows: a token every q_stride, k_stride, v_stride values (at least heads * head_dim, a
  * multiple of 8), its heads next to each other.  head_dim is 64 or 128; q_heads is a multiple of kv_heads (q head h reads
- * kv head h / (q_heads / kv_heads)), at most MHC_MAX_HEADS_PER_KV times it, q_heads * head_dim <= MHC_MAX_HIDDEN.
+ * kv head h / (q_heads / kv_heads)), at most MHC_MAX_HEADS_PER_KV times it, q_heads * head_dim <= MHC_MAX_HIDDEN.  Packed
+ * rows (T, Tq, Tk) are at most MHC_MAX_TOKENS, sequences at most MHC_MAX_SEQUENCES; without rows or sequences nothing is
+ * launched.  The int32 arrays and lse are 4-byte aligned, everything else 16.
  *
  * The cache: [pages][kv_heads][page_size / 16] groups of 16 tokens, 17 * head_dim bytes each: of K, 16 rows of
  * head_dim / 2 bytes of E2M1 codes (two a byte, the even value in the low half; row r's 16-byte chunk c stored as chunk
