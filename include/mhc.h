@@ -498,8 +498,8 @@ MHC_API size_t mhc_prompt_workspace_size(void);
  *   attn_fp8, attn_scales   the result as MXFP8 [T][q_heads * head_dim] (scale tiles as above, one scale per 32 values,
  *                scale_mode), quantized from fp32 in one rounding, or both NULL; one form of the result is required
  *   lse          [T][q_heads] fp32 max s + ln sum_j p_j, for a join with other keys, or NULL
- * P is held in fp16 and V's scales relative to the largest so far: contributions below 2^-25 of the largest weight times
- * the largest V of a sequence lose bits.  Meant for a few tokens a sequence; whole chunks go through mhc_kv_read_mxfp4 and
+ * P is held in fp16 and V's scales relative to the largest that a row saw so far: contributions below 2^-25 of a row's
+ * largest weight times the largest V that it sees lose bits.  Meant for a few tokens a sequence; whole chunks go through mhc_kv_read_mxfp4 and
  * mhc_prompt_attention.  Deterministic.  Two launches, the second for the sequences that were cut. */
 MHC_API mhc_status mhc_decode_attention_mxfp4(const mhc_bf16 *q, int64_t q_stride, int64_t T, int64_t q_heads,
                                               const int32_t *offsets, const int32_t *seq_lens, const int32_t *page_table,
@@ -510,7 +510,8 @@ MHC_API mhc_status mhc_decode_attention_mxfp4(const mhc_bf16 *q, int64_t q_strid
 
 /* The same over packed bf16 keys and values: the rows q_offsets[b] .. of q are the last of the keys k_offsets[b] .. of k
  * and v (with as many of both: a whole prompt; with more keys: a later chunk of it after its prefix).  P is
- * held in bf16.  Rows whose scores pass 2^28, or that share a tile of rows with a value of v that is not finite among keys
+ * held in bf16; its products with v (p up to 2^8) are summed in fp32 and divided at the end, so that sums past fp32's range
+ * (v of about 2^120 over the number of keys, and more) are infinite.  Rows whose scores pass 2^28, or that share a tile of rows with a value of v that is not finite among keys
  * that some of them see and some do not, are computed plainly in fp32, slowly.  Deterministic.  One launch. */
 MHC_API mhc_status mhc_prompt_attention(const mhc_bf16 *q, int64_t q_stride, const mhc_bf16 *k, int64_t k_stride,
                                         const mhc_bf16 *v, int64_t v_stride, int64_t Tq, int64_t Tk, int64_t q_heads,

@@ -13,17 +13,17 @@
 // tensor path (operands from registers: the codes are converted there and never written back),
 //   S^T [32 tokens x rows] = K Q^T   m16n8k16, fp16: E2M1 codes are exact there, and a row of q scaled by a power of two
 //                                    has all its 8 bits; each 32 values' sum is multiplied by its scale in fp32
-//   O^T [D x rows] += V^T P'^T       with V's codes, and P' = p * 2^(scale - largest scale so far) in fp16 (2^-11 of p, and
+//   O^T [D x rows] += V^T P'^T       with V's codes, and P' = p * 2^(scale - largest scale that the row saw so far) in fp16 (2^-11 of p, and
 //                                    2^-36 of the largest p; scales below 2^-27 of the largest are lost, as they are in fp32
 //                                    beside that largest)
 // The k order of a product is free: a lane takes 8 neighbouring codes of K (ldmatrix), and 4 of V for two tokens
 // (ldmatrix.trans), as they lie; q and the output follow that order.  P crosses from one product's layout to the other's
 // by movmatrix.
 //
-// Measured: 64 sequences of 100 to 16,000 tokens, 64 / 8 heads of 128: 111 us, 75 % of the copy rate (copies alone take 90 % of
+// Measured: 64 sequences of 100 to 16,000 tokens, 64 / 8 heads of 128: 112 us, 74 % of the copy rate (copies alone take 90 % of
 // that, the arithmetic alone too: about 600 instructions a slice, half of them on the ALU pipe); 32,003 tokens, 6 queries of
 // 56 / 8 heads: 39 us, bound by the conversions, which each row tile does anew; 3 sequences of 60,001 to 131,000, 32 / 4
-// heads of 64: 28 us, 38 %, bound by the arithmetic (half the bytes a token for the same softmax).
+// heads of 64: 29 us, 37 %, bound by the arithmetic (half the bytes a token for the same softmax).
 #include "attention.cuh"
 #include "mhc.h"
 #include "sm100_ptx.cuh"
@@ -165,8 +165,9 @@ template <int D, class C>
 struct Warp {                              // a warp's running state
     float o[C::NB][2][C::NTILE][4];        // O^T: per 32 values two tiles of 16, per 8 rows
     float m[C::NTILE][2], l[C::NTILE][2];  // rows 2 (lane % 4) and the next: reference maximum, sum of the lane's own tokens
-    uint32_t top, low;                     // V's largest scale byte so far: o is in units of 2^(top - 127 - kGain); the
-                                           // smallest whose factor is a normal half
+    uint32_t top, low;                     // V's largest scale byte so far: o is in units of 2^(top - 127 - kGain), or of
+                                           // what it was when a row saw its last token (own); the smallest byte whose
+                                           // factor is a normal half
 };
 
 // 16 tokens' codes (half kHalf of a slice) of K or V (kPart): r0 the first 8 tokens', r1 the others', a block each.
@@ -197,11 +198,51 @@ __device__ __forceinline__ uint32_t lane_codes() {
     return row * L::kRow + (blk ^ L::swizzle(row)) * 16;
 }
 
+// V's scale bytes of a token (the lane's) of a slice.
+template <int D, int NB>
+__device__ __forceinline__ uint32_t v_scales(uint32_t base) {
+    using L = CacheLayout<D>;
+    const uint32_t at = base + ((threadIdx.x & 31) >> 4) * L::kGroupBytes + L::kScales + (threadIdx.x & 15) * NB;
+    uint32_t vw;
+    if constexpr (NB == 4) asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(vw) : "r"(at), "n"(L::kPart));
+    else asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=r"(vw) : "r"(at), "n"(L::kPart));
+    return vw;
+}
+// The largest of a lane's scale bytes that is a number.
+template <int NB>
+__device__ __forceinline__ uint32_t largest_scale(uint32_t vw) {
+    uint32_t mine = 0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const uint32_t e = (vw >> (8 * b)) & 255u;
+        mine = max(mine, e == 255u ? 0u : e);
+    }
+    return mine;
+}
+// Where a slice's next window ends: at the first token from lo on that not every row with tokens left sees.
+template <int NTL>
+__device__ __forceinline__ int window_end(const int (&vis_g)[NTL], int lo, int end) {
+#pragma unroll
+    for (int r = 0; r < NTL; ++r)
+        if (vis_g[r] > lo) end = min(end, vis_g[r]);
+    return __reduce_min_sync(0xffffffffu, end);
+}
+// Whether a slice holds a scale above all those that some row with tokens left sees: that row's p would lose bits to a V
+// which is none of its own, so such a slice is gone through window by window.
+template <int D, int NB, int NTL>
+__device__ __forceinline__ bool needs_windows(uint32_t top, uint32_t base, int tok0, int len, uint32_t bad, const int (&vis_g)[NTL]) {
+    const int lane = threadIdx.x & 31, all = window_end(vis_g, tok0, tok0 + kSlice);   // (seen by all of those rows)
+    const bool on = tok0 + lane < len && !((bad >> (lane >> 4)) & 1u);
+    const uint32_t mine = on ? largest_scale<NB>(v_scales<D, NB>(base)) : 0u;
+    const uint32_t seen = max(top, __reduce_max_sync(0xffffffffu, tok0 + lane < all ? mine : 0u));
+    return __any_sync(0xffffffffu, mine > seen);
+}
+
 // A slice of 32 tokens from shared memory.  tok0: its first token; vis: tokens that rows 2 (lane % 4) and the next see,
-// vis_g: those that row lane / 4 sees; f: the factors of those rows' scores.
+// vis_g: those that row lane / 4 sees; f: the factors of those rows' scores.  With kMask only tokens from .. to - 1.
 template <int D, class C, bool kMask>
 __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32_t (&q)[C::NB][2][C::NTILE * 2], const uint2 *sq,
-                                      float *sk, uint32_t *sv, int tok0, int len, uint32_t bad, const float (&f)[C::NTILE][2],
+                                      float *sk, uint32_t *sv, uint8_t *own, int tok0, int from, int to, int len, uint32_t bad, const float (&f)[C::NTILE][2],
                                       const int (&vis)[C::NTILE][2], const int (&vis_g)[C::NTILE]) {
     using L = CacheLayout<D>;
     constexpr int NB = C::NB, NTL = C::NTILE;
@@ -212,16 +253,12 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
     {
         const uint32_t at = base + (lane >> 4) * L::kGroupBytes + L::kScales + (lane & 15) * NB;
         uint32_t kw;
-        if constexpr (NB == 4) {
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(at));
-            asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(vw) : "r"(at), "n"(L::kPart));
-        } else {
-            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(kw) : "r"(at));
-            asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=r"(vw) : "r"(at), "n"(L::kPart));
-        }
+        if constexpr (NB == 4) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(at));
+        else asm volatile("ld.shared.u16 %0, [%1];" : "=r"(kw) : "r"(at));
+        vw = v_scales<D, NB>(base);
         if constexpr (kMask) {
             if ((bad >> (lane >> 4)) & 1u) kw = vw = 0xffffffffu;   // no such page: NaN
-            if (tok0 + lane >= len) kw = vw = 0u;                   // (what the rest of a page holds)
+            if (tok0 + lane >= min(len, to) || tok0 + lane < from) kw = vw = 0u;   // (what the rest of a page holds; other windows)
         }
         const float2 k01 = ue8m0x2(kw);
         if constexpr (NB == 4) {
@@ -301,22 +338,19 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
                 for (int j = 0; j < 2; ++j) {
                     float &x = s[h][r][2 * j + e];
                     x *= f[r][e];
-                    if (kMask && tok0 + 16 * h + 8 * j + g4 >= vis[r][e]) x = -INFINITY;
+                    if constexpr (kMask) {
+                        const int tok = tok0 + 16 * h + 8 * j + g4;
+                        if (tok < from || tok >= min(vis[r][e], to)) x = -INFINITY;
+                    }
                 }
             hi[r][e] = fmaxf(fmaxf(s[0][r][e], s[0][r][2 + e]), fmaxf(s[1][r][e], s[1][r][2 + e]));
             raise |= hi[r][e] > w.m[r][e] + (kHead + kLazy);
         }
     if (__any_sync(0xffffffffu, raise)) {
-        uint32_t mine = 0;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const uint32_t e = (vw >> (8 * b)) & 255u;
-            mine = max(mine, e == 255u ? 0u : e);
-        }
-        const uint32_t top = max(w.top, __reduce_max_sync(0xffffffffu, mine));
+        const uint32_t top = max(w.top, __reduce_max_sync(0xffffffffu, largest_scale<NB>(vw)));
         w.low = max((int)top - (kNormal - 1), 0);
         far = __any_sync(0xffffffffu, v_hi == 255u || v_lo < w.low);
-        const float unit = ex2((float)((int)w.top - (int)top));
+        const float rise = ex2((float)((int)w.top - (int)top));
         w.top = top;
 #pragma unroll
         for (int r = 0; r < NTL; ++r)
@@ -324,6 +358,9 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
             for (int e = 0; e < 2; ++e) {
                 const float m = fmaxf(w.m[r][e], column_max(hi[r][e]) - kHead);
                 const float al = w.m[r][e] == -INFINITY ? 0.f : ex2(w.m[r][e] - m);
+                const bool on = !kMask || vis[r][e] > from;            // a row that has seen all of its own keeps its unit
+                const float unit = on ? rise : 1.f;
+                if (on) own[r * 8 + 2 * t4 + e] = (uint8_t)top;
                 w.m[r][e] = m;
                 w.l[r][e] *= al;
 #pragma unroll
@@ -404,7 +441,8 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
                     pb[r][j] = mul_half2(p16[r][2 * h + j], sc[j][b]);
                     if constexpr (kMask) {  // (0 times a NaN scale is no part of what a row does not see)
                         const int tok = tok0 + 16 * h + 8 * j + 2 * t4;
-                        pb[r][j] &= (tok < vis_g[r] ? 0xffffu : 0u) | (tok + 1 < vis_g[r] ? 0xffff0000u : 0u);
+                        const int end = min(vis_g[r], to);
+                        pb[r][j] &= (tok >= from && tok < end ? 0xffffu : 0u) | (tok + 1 >= from && tok + 1 < end ? 0xffff0000u : 0u);
                     }
                 }
             const uint32_t e0 = e2m1x2<0>(v0[b]), e1 = e2m1x2<2>(v0[b]), e2 = e2m1x2<0>(v1[b]), e3 = e2m1x2<2>(v1[b]);
@@ -440,6 +478,7 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
     __shared__ int64_t found[NW][2];
     __shared__ Pair pairs[C::NW][2];           // a warp's present pair and its next one (in registers they cost the slices theirs)
     __shared__ int2 look[C::NW][32];           // the next one's first pages
+    __shared__ uint8_t own[C::NW][C::ROWS];    // the rows' units (Warp)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
     const int G = a.q_heads / a.c.heads;
     const int unit = (int)blockIdx.x * NW + warp;                      // which share
@@ -650,6 +689,7 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
 #pragma unroll
             for (int e = 0; e < 2; ++e) w.m[r][e] = -INFINITY, w.l[r][e] = 0.f;
         w.top = w.low = 0;
+        if (lane < C::ROWS) own[warp][lane] = 0;                       // (a barrier follows before it is used)
 
         for (int k = 0; k < cur.n; ++k) {
             cp_wait<ST - 2>();
@@ -662,10 +702,16 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             float *sk = scale + warp * (kSlice * NB * 3 / 2);
             uint32_t *sv = reinterpret_cast<uint32_t *>(sk + kSlice * NB);
             if (tok0 + kSlice <= seen && bad == 0)
-                slice<D, C, false>(w, base, q, sq + warp * (NB * 2 * NTL * 32), sk, sv, tok0, cur.seq.len, bad, f, vis, vis_g);
-            else
-                slice<D, C, true>(w, base, q, sq + warp * (NB * 2 * NTL * 32), sk, sv, tok0, cur.seq.len, bad, f, vis, vis_g);
-            __syncwarp();                                              // (the scales are written anew)
+                slice<D, C, false>(w, base, q, sq + warp * (NB * 2 * NTL * 32), sk, sv, own[warp], tok0, tok0, tok0 + kSlice, cur.seq.len, bad, f, vis, vis_g);
+            else {
+                const bool windows = needs_windows<D, NB, NTL>(w.top, base, tok0, cur.seq.len, bad, vis_g);
+                for (int lo = tok0, hi; lo < tok0 + kSlice; lo = hi) {
+                    hi = windows ? window_end(vis_g, lo, tok0 + kSlice) : tok0 + kSlice;
+                    slice<D, C, true>(w, base, q, sq + warp * (NB * 2 * NTL * 32), sk, sv, own[warp], tok0, lo, hi, cur.seq.len, bad, f, vis, vis_g);
+                    __syncwarp();                                      // (the scales are written anew)
+                }
+            }
+            __syncwarp();
         }
         __syncwarp();                                                  // (every lane has read the last slice)
         // ---- the next pair's first copies run while this one is written
@@ -675,9 +721,6 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             begin(pairs[warp][now ^ 1]);
         }
         const bool whole = cur.s0 == -kPairCost && cur.s0 + cur.count == cur.seq.slices;
-        // 2^(top - 127 - kGain), below 2^-126 too
-        const int e_units = (int)w.top - kGain;
-        const float units = __uint_as_float(e_units > 0 ? (uint32_t)e_units << 23 : 0x00800000u >> (1 - e_units));
         const int slot = 2 * unit + (cur.s0 == -kPairCost ? 1 : 0);
 #pragma unroll
         for (int r = 0; r < NTL; ++r)
@@ -686,13 +729,16 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
                 const float l = column_sum(w.l[r][e]);
                 const int row = r * 8 + 2 * t4 + e;
                 const bool on = row < rows;
-                if (!whole) {
+                const int e_units = (int)own[warp][row] - kGain;         // 2^(own - 127 - kGain), below 2^-126 too
+                const float units = __uint_as_float(e_units > 0 ? (uint32_t)e_units << 23 : 0x00800000u >> (1 - e_units));
+                if (!whole) {                                          // divided: the sums may pass fp32's end where V does not
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
                     float *o = parts.o + ((size_t)slot * C::ROWS + row) * D + 4 * g4;
                     if (on) {
 #pragma unroll
                         for (int k = 0; k < NB; ++k)
                             *reinterpret_cast<float4 *>(o + 32 * k) =
-                                make_float4(w.o[k][0][r][e] * units, w.o[k][0][r][2 + e] * units, w.o[k][1][r][e] * units, w.o[k][1][r][2 + e] * units);
+                                make_float4(w.o[k][0][r][e] * inv * units, w.o[k][0][r][2 + e] * inv * units, w.o[k][1][r][e] * inv * units, w.o[k][1][r][2 + e] * inv * units);
                         if (g4 == 0) *reinterpret_cast<float2 *>(parts.ml + ((size_t)slot * C::ROWS + row) * 2) = make_float2(w.m[r][e], l);
                     }
                     continue;
@@ -758,9 +804,10 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) join_kernel(c
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
         top = fmaxf(top, m);
-        const float old = m == -INFINITY ? 0.f : ex2(m - top), weight = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+        const float before = m == -INFINITY ? 0.f : l * ex2(m - top), mine = ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - top);
         m = top;
-        l = fmaf(ml.y, weight, l * old);
+        l = before + warp_sum(mine);
+        const float inv = l == 0.f ? 0.f : 1.f / l, old = before * inv, weight = mine * inv;   // o stays a mean
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] *= old;
         const int n = min(32, hi - base);
@@ -785,7 +832,6 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) join_kernel(c
             }
         }
     }
-    l = warp_sum(l);
     if constexpr (kWarps > 1) {
         __shared__ float so[kWarps][D], sm[kWarps], sl[kWarps];
 #pragma unroll
@@ -801,18 +847,20 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) join_kernel(c
         for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm[w]);
         l = 0.f;
 #pragma unroll
+        for (int w = 0; w < kWarps; ++w) l += sm[w] == -INFINITY ? 0.f : sl[w] * ex2(sm[w] - m);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
         for (int i = 0; i < N; ++i) o[i] = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float x = sm[w] == -INFINITY ? 0.f : ex2(sm[w] - m);
-            l = fmaf(sl[w], x, l);
+            const float x = sm[w] == -INFINITY ? 0.f : sl[w] * ex2(sm[w] - m) * inv;
 #pragma unroll
             for (int i = 0; i < N; ++i) o[i] = fmaf(so[w][lane * N + i], x, o[i]);
         }
     }
     const bool sees = seq.len - seq.n + (int)(t - s.begin) >= 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = sees ? o[i] / l : 0.f;
+    for (int i = 0; i < N; ++i) o[i] = !sees ? 0.f : l == 0.f ? o[i] / l : o[i];   // (keys whose scores are all -inf: NaN)
     write_head_row<D>(a.o, t, hq, o, sees ? (m + log2f(l)) * kLn2 : -INFINITY);
 }
 

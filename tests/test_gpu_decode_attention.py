@@ -131,6 +131,46 @@ def test_a_small_v_under_a_large_one_that_is_not_looked_at(mhc, ws):
     ref.check_out(o["attn_out"], out, small + 2.0 ** -24)
 
 
+@pytest.mark.parametrize("D,G,lens,new,E", [(128, 4, [300, 70, 5], [6, 3, 5], 60), (64, 7, [97, 33, 40000], [40, 2, 6], 24), (128, 1, [64, 31], [64, 9], 100)])
+def test_a_later_large_v_leaves_earlier_rows_their_bits(mhc, ws, D, G, lens, new, E):
+    """V grows by 2^E from each new token to the next two: a row's result is bounded by the V that it sees itself."""
+    b = ref.Batch(mhc, lens, new, 2, D, 16, seed=E)
+    for i, (n, m) in enumerate(zip(lens, new)):
+        pos = torch.arange(n, device="cuda")
+        v = torch.randn(n, 2, D, dtype=torch.float64, device="cuda", generator=torch.Generator("cuda").manual_seed(i))
+        up = ((pos - (n - m)).clamp(min=0) // 2 * E).clamp(max=120).double()
+        v = v * torch.exp2(up - 20)[:, None, None]
+        ref.put(b.cache, b.page_table, i, pos, 1, *ref.quantize4(v, 0))
+        b.v[i] = ref.get(b.cache, b.page_table, i, pos, 1)
+    q = queries(b.T, G * 2, D, 8)
+    o = mhc.decode_attention_mxfp4(q, b.cache, b.page_table, b.seq_lens, b.offsets, want_lse=True, workspace=ws)
+    mhc.check_status(ws)
+    t = 0
+    for i, (n, m) in enumerate(zip(lens, new)):
+        for j in range(m):
+            end = n - m + j + 1
+            if end > 0:
+                out, lse, tol, tol_lse = ref.attend(q[t:t + 1], b.k[i][:end], b.v[i][:end], D ** -0.5, "f16")
+                ref.check_out(o["attn_out"][t:t + 1], out, tol)
+                ref.check_lse(o["lse"][t:t + 1], lse, tol_lse)
+            t += 1
+
+
+@pytest.mark.parametrize("lens", [[90, 40000], [2000 + 37 * i for i in range(40)]])
+def test_the_largest_v_of_cut_sequences(mhc, ws, lens):
+    """Magnitudes up to bf16's last binades: neither the parts' sums nor their join leave fp32's range."""
+    D, Hkv = 64, 8
+    b = ref.Batch(mhc, lens, [1] * len(lens), Hkv, D, 64, seed=13)
+    for i, n in enumerate(lens):
+        v = torch.rand(n, Hkv, D, dtype=torch.float64, device="cuda", generator=torch.Generator("cuda").manual_seed(i)) * 2.0 ** 127
+        pos = torch.arange(n, device="cuda")
+        ref.put(b.cache, b.page_table, i, pos, 1, *ref.quantize4(v, 0))
+        b.v[i] = ref.get(b.cache, b.page_table, i, pos, 1)
+    q = queries(b.T, 32, D, 13)
+    o = mhc.decode_attention_mxfp4(q, b.cache, b.page_table, b.seq_lens, b.offsets, want_lse=True, workspace=ws)
+    check(o, b, q, D ** -0.5)
+
+
 @pytest.mark.parametrize("page", [16, 128])
 def test_what_is_not_seen_is_not_read_into_the_result(mhc, ws, page):
     """NaN scales and every code in the rest of a page (Batch fills it with 255), NaN in the later tokens of a block."""
