@@ -29,6 +29,7 @@
 
 #include "attention.cuh"
 #include "sm100_ptx.cuh"
+#include "tile_ring.h"
 #include "tma_encode.h"
 
 namespace mhc {
@@ -49,6 +50,8 @@ struct Cfg {
     static constexpr int kTile = NH * kHalf;         // Q of a tile, or 128 keys' K or V
     static constexpr int ST = D == 128 ? 5 : 8;      // ring
     static constexpr int kSmem = 1024 + 2 * kTile + ST * kTile;
+    using Ring = TileRing<ST>;
+    static_assert(Ring::kFull <= 10 && ST <= 8, "");   // (Bars)
 };
 
 struct PromptMaps {
@@ -57,9 +60,14 @@ struct PromptMaps {
 
 constexpr int kPart = 3;   // tiles of keys that a pair's rows see only in part: its tokens are at most 256 neighbours
 
+// A wait by parity needs the phase before to be complete (tile_ring.h).  It is, at each of them: a waiter goes through every
+// phase of item_full, item_empty, next, q_full, q_empty, kv_empty, s_full, s_taken, p_full, pv_done and of its own kv_full
+// (warp 8 K's, warp 9 V's).  Those that skip phases are warp 9 at `checked` and warp 11 at `go` (tiles of keys that an item
+// does not have) and at kv_full: an item's slot is written anew only when every role has left it, and `checked` and `go` have
+// completed their phases of it by then; `go` itself comes after kv_full's phase has begun.
 struct Bars {
     uint64_t item_full[2], item_empty[2], next;
-    uint64_t q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], s_taken, p_full[2], pv_done[2];
+    uint64_t q_full, q_empty, kv_full[10], kv_empty[8], s_full[2], s_taken, p_full[2], pv_done[2];
     uint64_t go[2][kPart], checked[2][kPart], drained[2];
 };
 
@@ -239,7 +247,7 @@ __device__ __noinline__ void plain_row(const PromptArgs &a, const PromptSeq &s, 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ PromptMaps maps, const __grid_constant__ PromptArgs a) {
     using C = Cfg<D>;
-    constexpr int ST = C::ST;
+    using Ring = typename C::Ring;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sQ = smem, *ring = smem + 2 * C::kTile;
@@ -268,10 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         mbar_init(&bar.s_taken, 128);
         mbar_init(&bar.q_full, 1);
         mbar_init(&bar.q_empty, 1);
-        for (int i = 0; i < ST; ++i) {
-            mbar_init(&bar.kv_full[i], 1);
-            mbar_init(&bar.kv_empty[i], 1);
-        }
+        for (uint32_t i = 0; i < Ring::kFull; ++i) mbar_init(&bar.kv_full[i], 1);
+        for (int i = 0; i < C::ST; ++i) mbar_init(&bar.kv_empty[i], 1);
         fence_mbar_init();
         fence_proxy_async_smem();
     }
@@ -469,8 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             wait(&bar.q_full, n_q & 1, dead);
             ++n_q;
             for (int j = 0; j < n_tiles; ++j) {
-                const uint32_t use = use0 + 2 * j, k = smem_u32(ring + use % ST * C::kTile);
-                wait(&bar.kv_full[use % ST], (use / ST) & 1, dead);
+                const uint32_t use = use0 + 2 * j, k = smem_u32(ring + Ring::stage(use) * C::kTile);
+                wait(&bar.kv_full[Ring::full(use)], Ring::full_parity(use), dead);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (j >= tiles[x]) continue;
@@ -492,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 }
                 if (dead) break;
                 if (elect_one()) {
-                    umma_commit(&bar.kv_empty[use % ST]);
+                    umma_commit(&bar.kv_empty[Ring::stage(use)]);
                     if (j == n_tiles - 1) umma_commit(&bar.q_empty);
                 }
                 __syncwarp();
@@ -508,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             const Item &it = items[t & 1];
             const int n_tiles = it.n_tiles, part = it.part, tiles[2] = {it.tiles[0], it.tiles[1]};
             for (int j = 0; j < n_tiles; ++j) {
-                const uint32_t use = use0 + 2 * j + 1, v = smem_u32(ring + use % ST * C::kTile);
-                wait(&bar.kv_full[use % ST], (use / ST) & 1, dead);
+                const uint32_t use = use0 + 2 * j + 1, v = smem_u32(ring + Ring::stage(use) * C::kTile);
+                wait(&bar.kv_full[Ring::full(use)], Ring::full_parity(use), dead);
                 if (j >= part) wait(&bar.checked[t & 1][j - part], (t >> 1) & 1, dead);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     issued = true;
                 }
                 if (dead) break;
-                if (elect_one()) umma_commit(&bar.kv_empty[use % ST]);
+                if (elect_one()) umma_commit(&bar.kv_empty[Ring::stage(use)]);
                 __syncwarp();
             }
             use0 += 2 * n_tiles;
@@ -575,14 +581,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 }
                 __syncwarp();
                 for (int i = 0; i < 2 * it.n_tiles; ++i, ++use) {
-                    const uint32_t st = use % ST;
-                    wait(&bar.kv_empty[st], ((use / ST) & 1) ^ 1, dead);
+                    const uint32_t st = Ring::stage(use);
+                    uint64_t *full = &bar.kv_full[Ring::full(use)];
+                    wait(&bar.kv_empty[st], Ring::empty_parity(use) ^ 1, dead);   // (the release of the use ST before)
                     if (dead) break;
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(&bar.kv_full[st], C::kTile);
+                        mbar_arrive_expect_tx(full, C::kTile);
                         for (int h = 0; h < C::NH; ++h)
-                            tma_load_3d(ring + st * C::kTile + h * C::kHalf, i & 1 ? &maps.v : &maps.k, 64 * h, it.head, (int)(it.s.k0 + (i / 2) * kKeys),
-                                        &bar.kv_full[st]);
+                            tma_load_3d(ring + st * C::kTile + h * C::kHalf, i & 1 ? &maps.v : &maps.k, 64 * h, it.head, (int)(it.s.k0 + (i / 2) * kKeys), full);
                         if ((i & 1) && i / 2 >= it.part) mbar_arrive(&bar.go[slot][i / 2 - it.part]);
                     }
                     __syncwarp();
@@ -606,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         if (dead) {  // what was asked for has to land before the CTA's shared memory goes
             bool d = false;
-            for (uint32_t u = use > (uint32_t)ST ? use - ST : 0; u < use; ++u) wait(&bar.kv_full[u % ST], (u / ST) & 1, d);
+            for (uint32_t u = use > (uint32_t)C::ST ? use - C::ST : 0; u < use; ++u) wait(&bar.kv_full[Ring::full(u)], Ring::full_parity(u), d);
             if (n_q > 0) wait(&bar.q_full, (n_q - 1) & 1, d);
             if (asked) {
                 for (int p = 0; p < 2; ++p) wait(&bar.next, p, d);
@@ -622,9 +628,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 if (j < it.n_tiles) {
                     const uint32_t use = use0 + 2 * j + 1;
                     wait(&bar.go[t & 1][k], (t >> 1) & 1, dead);   // (its copy is the barrier's present phase)
-                    wait(&bar.kv_full[use % ST], (use / ST) & 1, dead);
+                    wait(&bar.kv_full[Ring::full(use)], Ring::full_parity(use), dead);
                     if (dead) break;
-                    uint8_t *v = ring + (use % ST) * C::kTile;
+                    uint8_t *v = ring + Ring::stage(use) * C::kTile;
                     const int rows = min(kKeys, it.s.len - j * kKeys);
                     if (rows < kKeys) {   // rows behind the sequence
                         for (int h = 0; h < C::NH; ++h)
