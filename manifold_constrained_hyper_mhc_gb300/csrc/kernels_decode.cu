@@ -774,6 +774,10 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
     cp_wait<0>();
 }
 
+// A part's sum l at its maximum m, at the maximum `top` of several.  Where m is -inf the part has no weight, and l is 0, or
+// NaN if all its scores are: that stays, in the result and in the log-sum.
+__device__ __forceinline__ float sum_at(float l, float m, float top) { return m == -INFINITY ? l : l * ex2(m - top); }
+
 // Joins the parts of the pairs that were cut: kWarps warps a row (token, q head), each a run of the parts, eight loads in
 // flight.  The order is fixed by the lengths alone.
 template <int D, class C, int kWarps>
@@ -804,7 +808,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) join_kernel(c
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
         top = fmaxf(top, m);
-        const float before = m == -INFINITY ? 0.f : l * ex2(m - top), mine = ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - top);
+        const float before = sum_at(l, m, top), mine = sum_at(ml.y, ml.x, top);
         m = top;
         l = before + warp_sum(mine);
         const float inv = l == 0.f ? 0.f : 1.f / l, old = before * inv, weight = mine * inv;   // o stays a mean
@@ -847,13 +851,13 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) join_kernel(c
         for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm[w]);
         l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) l += sm[w] == -INFINITY ? 0.f : sl[w] * ex2(sm[w] - m);
+        for (int w = 0; w < kWarps; ++w) l += sum_at(sl[w], sm[w], m);
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float x = sm[w] == -INFINITY ? 0.f : sl[w] * ex2(sm[w] - m) * inv;
+            const float x = sum_at(sl[w], sm[w], m) * inv;
 #pragma unroll
             for (int i = 0; i < N; ++i) o[i] = fmaf(so[w][lane * N + i], x, o[i]);
         }
