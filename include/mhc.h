@@ -499,8 +499,9 @@ MHC_API size_t mhc_prompt_workspace_size(void);
  *                scale_mode), quantized from fp32 in one rounding, or both NULL; one form of the result is required
  *   lse          [T][q_heads] fp32 max s + ln sum_j p_j, for a join with other keys, or NULL
  * P is held in fp16 and V's scales relative to the largest that a row saw so far: contributions below 2^-25 of a row's
- * largest weight times the largest V that it sees lose bits.  A row of q is scaled to at most 16 in its
- * products, which are held in fp32: K of 2^112 and more may give infinite scores whatever q is.
+ * largest weight times the largest V that it sees lose bits.  q is held in fp16, each 32 values of a
+ * head at a scale of their own (at most 16; 2^126 times the row's at most): values below 2^-20 of their 32's largest lose
+ * bits, at most 2^-28 of it.  Products are held in fp32: K of 2^112 and more may give infinite scores whatever q is.
  * Meant for a few tokens a sequence; whole chunks go through mhc_kv_read_mxfp4 and mhc_prompt_attention.  Deterministic.  Two launches, the second for the sequences that were cut. */
 MHC_API mhc_status mhc_decode_attention_mxfp4(const mhc_bf16 *q, int64_t q_stride, int64_t T, int64_t q_heads,
                                               const int32_t *offsets, const int32_t *seq_lens, const int32_t *page_table,

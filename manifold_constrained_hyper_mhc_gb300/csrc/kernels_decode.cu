@@ -11,8 +11,11 @@
 //
 // The rows of a pair are the tokens times the heads of the group, in tiles of 8, 16 or 24.  A warp computes, on the legacy
 // tensor path (operands from registers: the codes are converted there and never written back),
-//   S^T [32 tokens x rows] = K Q^T   m16n8k16, fp16: E2M1 codes are exact there, and a row of q scaled by a power of two
-//                                    has all its 8 bits; each 32 values' sum is multiplied by its scale in fp32
+//   S^T [32 tokens x rows] = K Q^T   m16n8k16, fp16: E2M1 codes are exact there, and so is q with its largest of 32 values
+//                                    in [8, 16) down to 2^-20 of that (what lies lower is off by at most 2^-28 of it);
+//                                    each 32 values' sum is multiplied by q's unit and K's scale in fp32, so that a small
+//                                    block of q beside a large one of K counts in full (two sums at once: 64 sequences
+//                                    below in 114.1 us, with one unit a row 114.6; head_dim 64 32.5 against 31.6)
 //   O^T [D x rows] += V^T P'^T       with V's codes, and P' = p * 2^(scale - largest scale that the row saw so far) in fp16 (2^-11 of p, and
 //                                    2^-36 of the largest p; scales below 2^-27 of the largest are lost, as they are in fp32
 //                                    beside that largest)
@@ -58,7 +61,8 @@ struct Cfg {
     static constexpr int kRing = NW * ST * kSliceBytes;
     static constexpr int kScale = NW * kSlice * NB * 6;            // a slice's scales, K's in fp32, V's in fp16: a warp's own
     static constexpr int kQ = ROWS > 8 ? NW * (D / 16) * NTILE * 32 * 8 : 0;   // q's fragments
-    static constexpr int kSmem = kRing + kScale + kQ;
+    static constexpr int kUnits = NW * NB * ROWS * 4;              // the units of q's blocks
+    static constexpr int kSmem = kRing + kScale + kQ + kUnits;
     static_assert(kSmem <= 226000 && NW * ROWS * (D + 2) <= kPartFloats, "");
 };
 
@@ -238,10 +242,11 @@ __device__ __forceinline__ bool needs_windows(uint32_t top, uint32_t base, int t
     return __any_sync(0xffffffffu, mine > seen);
 }
 
-// A slice of 32 tokens from shared memory.  tok0: its first token; vis: tokens that rows 2 (lane % 4) and the next see,
-// vis_g: those that row lane / 4 sees; f: the factors of those rows' scores.  With kMask only tokens from .. to - 1.
+// A slice of 32 tokens from shared memory.  units: of q's blocks, for rows 2 (lane % 4) and the next; tok0: its first
+// token; vis: tokens that those rows see, vis_g: those that row lane / 4 sees; f: the factors of those rows' scores.  With
+// kMask only tokens from .. to - 1.
 template <int D, class C, bool kMask>
-__device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32_t (&q)[C::NB][2][C::NTILE * 2], const uint2 *sq,
+__device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32_t (&q)[C::NB][2][C::NTILE * 2], const uint2 *sq, const float2 *units,
                                       float *sk, uint32_t *sv, uint8_t *own, int tok0, int from, int to, int len, uint32_t bad, const float (&f)[C::NTILE][2],
                                       const int (&vis)[C::NTILE][2], const int (&vis_g)[C::NTILE]) {
     using L = CacheLayout<D>;
@@ -316,10 +321,14 @@ __device__ __forceinline__ void slice(Warp<D, C> &w, uint32_t base, const uint32
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
                 mma(acc, a0, qb[r][0], qb[r][1]);
                 mma(acc, a1, qb[r][2], qb[r][3]);
+                const float2 u = units[(b * NTL + r) * 4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float k = e < 2 ? sc0[b] : sc1[b];
-                    s[h][r][e] = b == 0 ? acc[e] * k : fmaf(acc[e], k, s[h][r][e]);
+                for (int j = 0; j < 2; ++j) {
+                    const float k = j ? sc1[b] : sc0[b];
+                    const float2 x = __fmul2_rn(make_float2(acc[2 * j], acc[2 * j + 1]), u);
+                    const float2 y = b == 0 ? __fmul2_rn(x, make_float2(k, k)) : __ffma2_rn(x, make_float2(k, k), make_float2(s[h][r][2 * j], s[h][r][2 * j + 1]));
+                    s[h][r][2 * j] = y.x;
+                    s[h][r][2 * j + 1] = y.y;
                 }
             }
         }
@@ -629,8 +638,10 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             __syncwarp();
         }
         const int row0 = (cur.pair % cur.seq.tiles) * C::ROWS, rows = min(C::ROWS, cur.seq.n * G - row0), head = cur.pair / cur.seq.tiles;
-        // ---- q: row lane / 4 (+ 8) as B fragments, scaled by a power of two to at most 2^4
+        // ---- q: row lane / 4 (+ 8) as B fragments, each block scaled by a power of two of its own to at most 2^4; its unit is
+        // relative to the row's, which the scores are multiplied by at the end
         if constexpr (NTL > 1) load_q(cur);
+        float *su = reinterpret_cast<float *>(smem + C::kRing + C::kScale + C::kQ) + warp * (NB * C::ROWS);
         uint32_t q[NB][2][NTL * 2];
         float f[NTL][2];
         int vis[NTL][2], vis_g[NTL];
@@ -640,16 +651,17 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             const int row = r * 8 + g4;
             vis_g[r] = row < rows ? max(0, cur.seq.len - cur.seq.n + (row0 + row) / G + 1) : 0;
             seen = min(seen, row < rows ? vis_g[r] : 0x7fffffff);
-            float x[NB][8], amax = 0.f;
+            float x[NB][8], amax[NB], most = 0.f;
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
                 unpack8(qw[r][k], x[k]);
+                amax[k] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[k][e]));
+                for (int e = 0; e < 8; ++e) amax[k] = fmaxf(amax[k], fabsf(x[k][e]));
+                amax[k] = quad_max(amax[k]);
+                most = fmaxf(most, amax[k]);
             }
-            amax = quad_max(amax);
-            const int up = min(126, 3 + 127 - (int)(__float_as_uint(amax) >> 23));   // amax * 2^up is in [8, 16)
-            const float mul = __uint_as_float((uint32_t)(up + 127) << 23);
+            const int up = min(126, 3 + 127 - (int)(__float_as_uint(most) >> 23));   // the largest * 2^up is in [8, 16)
             const float fg = a.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -657,12 +669,16 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
                 vis[r][e] = __shfl_sync(0xffffffffu, vis_g[r], 8 * t4 + 4 * e);
             }
 #pragma unroll
-            for (int k = 0; k < NB; ++k)
+            for (int k = 0; k < NB; ++k) {
+                const int own_up = min(min(126, up + 126), 3 + 127 - (int)(__float_as_uint(amax[k]) >> 23));
+                const float mul = __uint_as_float((uint32_t)(own_up + 127) << 23);
+                if (t4 == k) su[(k * NTL + r) * 8 + g4] = __uint_as_float((uint32_t)(up - own_up + 127) << 23);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     q[k][h][r] = pack_half(x[k][4 * h] * mul, x[k][4 * h + 1] * mul);
                     q[k][h][NTL + r] = pack_half(x[k][4 * h + 2] * mul, x[k][4 * h + 3] * mul);
                 }
+            }
         }
         seen = __reduce_min_sync(0xffffffffu, seen);
         if constexpr (NTL > 1) {
@@ -672,8 +688,8 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int r = 0; r < NTL; ++r) sq[(((warp * NB + k) * 2 + h) * NTL + r) * 32 + lane] = make_uint2(q[k][h][r], q[k][h][NTL + r]);
-            __syncwarp();
         }
+        __syncwarp();
 
         Warp<D, C> w;
 #pragma unroll
@@ -701,13 +717,14 @@ __global__ void __launch_bounds__(C::NT, 1) decode_kernel(const __grid_constant_
             const uint32_t base = smem_u32(ring + stage * C::kSliceBytes), bad = bad_pages >> (2 * (copied - 1 - k)) & 3u;
             float *sk = scale + warp * (kSlice * NB * 3 / 2);
             uint32_t *sv = reinterpret_cast<uint32_t *>(sk + kSlice * NB);
+            const float2 *units = reinterpret_cast<const float2 *>(su) + t4;
             if (tok0 + kSlice <= seen && bad == 0)
-                slice<D, C, false>(w, base, q, sq + warp * (NB * 2 * NTL * 32), sk, sv, own[warp], tok0, tok0, tok0 + kSlice, cur.seq.len, bad, f, vis, vis_g);
+                slice<D, C, false>(w, base, q, sq + warp * (NB * 2 * NTL * 32), units, sk, sv, own[warp], tok0, tok0, tok0 + kSlice, cur.seq.len, bad, f, vis, vis_g);
             else {
                 const bool windows = needs_windows<D, NB, NTL>(w.top, base, tok0, cur.seq.len, bad, vis_g);
                 for (int lo = tok0, hi; lo < tok0 + kSlice; lo = hi) {
                     hi = windows ? window_end(vis_g, lo, tok0 + kSlice) : tok0 + kSlice;
-                    slice<D, C, true>(w, base, q, sq + warp * (NB * 2 * NTL * 32), sk, sv, own[warp], tok0, lo, hi, cur.seq.len, bad, f, vis, vis_g);
+                    slice<D, C, true>(w, base, q, sq + warp * (NB * 2 * NTL * 32), units, sk, sv, own[warp], tok0, lo, hi, cur.seq.len, bad, f, vis, vis_g);
                     __syncwarp();                                      // (the scales are written anew)
                 }
             }
