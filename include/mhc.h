@@ -513,8 +513,9 @@ MHC_API mhc_status mhc_decode_attention_mxfp4(const mhc_bf16 *q, int64_t q_strid
 /* The same over packed bf16 keys and values: the rows q_offsets[b] .. of q are the last of the keys k_offsets[b] .. of k
  * and v (with as many of both: a whole prompt; with more keys: a later chunk of it after its prefix).  P is
  * held in bf16; its products with v (p up to 2^8) are summed in fp32 and divided at the end, so that sums past fp32's range
- * (v of about 2^120 over the number of keys, and more) are infinite.  Rows whose scores pass 2^28, or that share a tile of rows with a value of v that is not finite among keys
- * that some of them see and some do not, are computed plainly in fp32, slowly.  Deterministic.  One launch. */
+ * (v of about 2^120 over the number of keys, and more) are infinite.  Rows whose
+ * scores pass 2^28, and neighbouring rows (of at most 256 / (q_heads / kv_heads) tokens) one of which sees a value of v that
+ * is not finite and another does not, are computed plainly in fp32, slowly.  Deterministic.  One launch. */
 MHC_API mhc_status mhc_prompt_attention(const mhc_bf16 *q, int64_t q_stride, const mhc_bf16 *k, int64_t k_stride,
                                         const mhc_bf16 *v, int64_t v_stride, int64_t Tq, int64_t Tk, int64_t q_heads,
                                         int64_t kv_heads, int64_t head_dim, const int32_t *q_offsets, const int32_t *k_offsets,

@@ -12,9 +12,10 @@
 //                   it is there, so the next one is computed beside the exponentials of this one
 //   warp 9          O += P V with P from tensor memory
 //   warp 10         the copies: Q, then K and V in turn into a ring (TMA, rows of a sequence in 128-byte swizzles)
-//   warp 11         what else the last tiles of V hold: rows behind the sequence are zeroed, and the tiles that some row sees
-//                   only in part are searched for values that are not finite (0 times such a value is not 0).  One
-//                   found, or scores beyond 2^28, sends the tile's rows through a plain fp32 loop instead.
+//   warp 11         what else the last tiles of V hold: rows that none of the pair sees are zeroed, and the tiles that some
+//                   row sees only in part are searched for values that are not finite (0 times such a value is not 0).
+//                   One that some rows of a tile do not see, or scores beyond 2^28, sends the tile's rows through a plain
+//                   fp32 loop instead.
 // The grid has a block for every pair of tiles; a CTA that has issued its pair's copies takes over a block that has not
 // begun (cluster launch control), so that its next pair's copies and first products run beside the present one's end, and
 // pairs of all lengths fill the device.
@@ -144,6 +145,7 @@ struct Item {
     PromptSeq s;
     int more, head, q0;      // whether there is one; its kv head, and its first token
     int tokens[2], tiles[2]; // of tile A and B: tokens, and tiles of keys that the last of them sees
+    int first[2], seen;      // keys that the first token of each sees, and those that the pair's last one sees
     int n_tiles, part;       // tiles of keys, and the first that some row sees only in part
 };
 
@@ -181,6 +183,8 @@ __device__ __forceinline__ Item locate(const PromptArgs &a, unsigned block, unsi
         it.tokens[x] = min(NT, max(0, it.s.n - it.q0 - x * NT));
         const int last = it.tokens[x] > 0 ? max(0, it.s.len - it.s.n + it.q0 + x * NT + it.tokens[x]) : 0;
         it.tiles[x] = (last + kKeys - 1) / kKeys;
+        it.first[x] = max(0, it.s.len - it.s.n + it.q0 + x * NT + 1);
+        it.seen = max(it.seen, last);
     }
     it.n_tiles = max(it.tiles[0], it.tiles[1]);
     it.part = max(max(0, it.s.len - it.s.n + it.q0 + 1) / kKeys, it.n_tiles - kPart);
@@ -253,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     uint8_t *sQ = smem, *ring = smem + 2 * C::kTile;
     __shared__ Bars bar;
     __shared__ Item items[2];
-    __shared__ int redo[2], far[2][2];        // of an item; of a tile of it
+    __shared__ int redo[2][2], far[2][2];     // of an item's tiles
     __shared__ __align__(16) uint4 answer;    // which block was taken over
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             if (dead) break;
             tmem_fence_after();
             named_sync(3 + x, 128);               // (`far` of all the tile's rows is known)
-            if (redo[slot] | far[slot][x]) {
+            if (redo[slot][x] | far[slot][x]) {
                 for (int r = warp & 3; r < it.tokens[x] * G; r += 4) plain_row<D>(a, it.s, it.q0 + x * NT + r / G, it.head, r % G);
             } else {
                 const float l = l2.x + l2.y, inv = vis > 0 ? 1.f / l : 0.f;   // (scores that are all -inf: NaN, 0 * inf)
@@ -553,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             if (more) it = locate(a, block, gridDim.x, NT);
             if (lane == 0) {
                 items[slot] = it;
-                redo[slot] = far[slot][0] = far[slot][1] = 0;
+                redo[slot][0] = redo[slot][1] = far[slot][0] = far[slot][1] = 0;
                 mbar_arrive(&bar.item_full[slot]);
             }
             __syncwarp();
@@ -631,22 +635,27 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     wait(&bar.kv_full[Ring::full(use)], Ring::full_parity(use), dead);
                     if (dead) break;
                     uint8_t *v = ring + Ring::stage(use) * C::kTile;
-                    const int rows = min(kKeys, it.s.len - j * kKeys);
-                    if (rows < kKeys) {   // rows behind the sequence
+                    const int rows = min(kKeys, it.seen - j * kKeys);
+                    if (rows < kKeys) {   // rows that none sees, or behind the sequence
                         for (int h = 0; h < C::NH; ++h)
                             for (int o = rows * 128 + lane * 16; o < C::kHalf; o += 512) *reinterpret_cast<uint4 *>(v + h * C::kHalf + o) = make_uint4(0, 0, 0, 0);
                         fence_proxy_async_smem();
                     }
-                    uint32_t bad = 0;
-                    for (int h = 0; h < C::NH; ++h)
+                    auto not_finite = [&](int from) {   // of the rows from .. rows - 1, by each lane's part of them
+                        uint32_t bad = 0;
+                        for (int h = 0; h < C::NH; ++h)
 #pragma unroll 4
-                        for (int o = lane * 16; o < rows * 128; o += 512) {
-                            const uint4 w = *reinterpret_cast<const uint4 *>(v + h * C::kHalf + o);
-                            // an exponent of all ones carries into the sign's place
-                            bad |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) | ((w.z & 0x7f807f80u) + 0x00800080u) |
-                                   ((w.w & 0x7f807f80u) + 0x00800080u);
-                        }
-                    if (bad & 0x80008000u) redo[t & 1] = 1;
+                            for (int o = from * 128 + lane * 16; o < rows * 128; o += 512) {
+                                const uint4 w = *reinterpret_cast<const uint4 *>(v + h * C::kHalf + o);
+                                // an exponent of all ones carries into the sign's place
+                                bad |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) | ((w.z & 0x7f807f80u) + 0x00800080u) |
+                                       ((w.w & 0x7f807f80u) + 0x00800080u);
+                            }
+                        return (bad & 0x80008000u) != 0;
+                    };
+                    if (__any_sync(0xffffffffu, not_finite(0)))
+                        for (int x = 0; x < 2; ++x)   // which tile has rows that do not see it
+                            if (j < it.tiles[x] && not_finite(max(0, it.first[x] - j * kKeys))) redo[t & 1][x] = 1;
                     __syncwarp();
                 }
                 if (lane == 0) mbar_arrive(&bar.checked[t & 1][k]);
