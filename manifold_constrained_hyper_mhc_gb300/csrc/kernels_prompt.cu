@@ -614,7 +614,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             block = first;
             __syncwarp();
         }
-        if (dead) {  // what was asked for has to land before the CTA's shared memory goes
+        // the last releases, which nobody else waits for, have to arrive before the CTA's shared memory goes
+        for (uint32_t u = use > (uint32_t)C::ST ? use - C::ST : 0; u < use && !dead; ++u) wait(&bar.kv_empty[Ring::stage(u)], Ring::empty_parity(u), dead);
+        if (n_q > 0 && !dead) wait(&bar.q_empty, (n_q - 1) & 1, dead);
+        if (dead) {  // and what was asked for has to land
             bool d = false;
             for (uint32_t u = use > (uint32_t)C::ST ? use - C::ST : 0; u < use; ++u) wait(&bar.kv_full[Ring::full(u)], Ring::full_parity(u), d);
             if (n_q > 0) wait(&bar.q_full, (n_q - 1) & 1, d);

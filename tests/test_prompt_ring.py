@@ -114,7 +114,7 @@ class Model:
             self.slot[t % 2] = item
             self.item_full[t % 2].arrive()
             if item is None:
-                return
+                break
             a, b, part = item
             n = max(a, b)
             for k in range(PART):
@@ -136,6 +136,10 @@ class Model:
                         self.go[t % 2][i // 2 - part].arrive()
                     use += 1
             yield self.next, t
+        for u in range(max(0, use - self.stages), use):
+            yield self.empty[self.ring.stage(u)], u // self.stages
+        if n_q:
+            yield self.q_empty, n_q - 1
 
     def wait_full(self, use):
         return self.full[self.ring.full(use)], self.ring.round(use)
@@ -264,6 +268,8 @@ class Model:
                 self.copies.pop(what)[1]()
             else:
                 self.queue[what].pop(0)()
+            if not at:
+                assert not self.copies and not any(self.queue.values()), "the block ends before what it started"
         assert not at and not self.copies, f"nothing goes on: {sorted(at)} wait"
         assert sorted(self.outputs) == [(t, x) for t in range(len(self.items)) for x in range(2)]
 
