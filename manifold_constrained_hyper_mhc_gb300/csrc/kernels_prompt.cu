@@ -62,14 +62,14 @@ struct PromptMaps {
 constexpr int kPart = 3;   // tiles of keys that a pair's rows see only in part: its tokens are at most 256 neighbours
 
 // A wait by parity needs the phase before to be complete (tile_ring.h).  It is, at each of them: a waiter goes through every
-// phase of item_full, item_empty, next, q_full, q_empty, kv_empty, s_full, s_taken, p_full, pv_done and of its own kv_full
-// (warp 8 K's, warp 9 V's).  Those that skip phases are warp 9 at `checked` and warp 11 at `go` (tiles of keys that an item
+// phase of item_full, item_empty, next, q_full, q_empty, kv_empty, s_full, s_taken, p_full, pv_done, rows_done and of its
+// own kv_full (warp 8 K's, warp 9 V's).  Those that skip phases are warp 9 at `checked` and warp 11 at `go` (tiles of keys that an item
 // does not have) and at kv_full: an item's slot is written anew only when every role has left it, and `checked` and `go` have
 // completed their phases of it by then; `go` itself comes after kv_full's phase has begun.
 struct Bars {
     uint64_t item_full[2], item_empty[2], next;
     uint64_t q_full, q_empty, kv_full[10], kv_empty[8], s_full[2], s_taken, p_full[2], pv_done[2];
-    uint64_t go[2][kPart], checked[2][kPart], drained[2];
+    uint64_t go[2][kPart], checked[2][kPart], rows_done[2], drained[2];
 };
 
 __device__ __forceinline__ bool elect_one() {
@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.p_full[i], 128);
             mbar_init(&bar.pv_done[i], 1);
+            mbar_init(&bar.rows_done[i], 4);   // its warps
             mbar_init(&bar.drained[i], 1);
             for (int k = 0; k < kPart; ++k) {
                 mbar_init(&bar.go[i][k], 1);
@@ -396,10 +397,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 wait(&bar.pv_done[x], n_pv & 1, dead);
                 ++n_pv;
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.rows_done[x]);             // (`far` is known; not a barrier without a limit)
             wait(&bar.checked[slot][kPart - 1], (t >> 1) & 1, dead);   // (the last of them)
+            wait(&bar.rows_done[x], t & 1, dead);
             if (dead) break;
             tmem_fence_after();
-            named_sync(3 + x, 128);               // (`far` of all the tile's rows is known)
             if (redo[slot][x] | far[slot][x]) {
                 for (int r = warp & 3; r < it.tokens[x] * G; r += 4) plain_row<D>(a, it.s, it.q0 + x * NT + r / G, it.head, r % G);
             } else {
@@ -549,7 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         unsigned block = blockIdx.x;
         bool more = true, asked = false;
         uint32_t use = 0, n_q = 0;
-        for (int t = 0;; ++t) {
+        int t = 0;
+        for (;; ++t) {
             const int slot = t & 1;
             wait(&bar.item_empty[slot], ((t >> 1) & 1) ^ 1, dead);
             if (dead) break;
@@ -575,8 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             asked = true;
             if (it.n_tiles > 0) {
                 wait(&bar.q_empty, (n_q & 1) ^ 1, dead);
-                ++n_q;
                 if (dead) break;
+                ++n_q;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(&bar.q_full, (uint32_t)(2 * C::NH * NT * G * 128));
                     for (int x = 0; x < 2; ++x)
@@ -621,9 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             bool d = false;
             for (uint32_t u = use > (uint32_t)C::ST ? use - C::ST : 0; u < use; ++u) wait(&bar.kv_full[Ring::full(u)], Ring::full_parity(u), d);
             if (n_q > 0) wait(&bar.q_full, (n_q - 1) & 1, d);
-            if (asked) {
-                for (int p = 0; p < 2; ++p) wait(&bar.next, p, d);
-            }
+            if (asked) wait(&bar.next, t & 1, d);
         }
     } else {
         // ---- what else V's tiles hold that some row sees only in part

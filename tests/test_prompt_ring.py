@@ -1,5 +1,7 @@
 """The prompt attention's barriers as a model on the CPU: copies and products that finish in any order.  Every wait by parity
 must pass only when its own phase is complete, and a product may read a tile only while it holds what the product takes.
+Waits may also give up, as the kernel's do after their time limit: every role ends all the same, and not before its copies
+and products have.
 
 The places of the ring come from the kernel's own header; the roles (copies, S, P V, the check of V, the rows of two tiles)
 go through the waits and arrivals of the kernel in their order."""
@@ -14,6 +16,8 @@ import pytest
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 PART = 3    # tiles of keys that a pair's rows may see only in part
 SLOTS = 2
+LANDS = "a wait of a role that gave up, for what it started: it has to come"
+LONG = "a wait for what no role is needed for: it gives up only when nothing goes on"
 
 
 class Stale(AssertionError):
@@ -59,15 +63,17 @@ class Tile:
 
 
 class Model:
-    """items: (tiles of A, tiles of B, first tile seen in part).  ring: stage, full, parity by use."""
+    """items: (tiles of A, tiles of B, first tile seen in part).  ring: stage, full, parity by use.  gives_up: how likely a
+    wait is to end without its phase."""
 
-    def __init__(self, items, stages, ring, rng):
-        self.items, self.stages, self.ring, self.rng = items, stages, ring, rng
+    def __init__(self, items, stages, ring, rng, gives_up=0.0):
+        self.items, self.stages, self.ring, self.rng, self.gives_up = items, stages, ring, rng, gives_up
         two = lambda n=1: [Barrier(n) for _ in range(SLOTS)]  # noqa: E731
-        self.item_full, self.item_empty = two(), two(5)
+        self.item_full, self.item_empty = two(), two(11)
         self.next, self.q_full, self.q_empty = Barrier(), Barrier(), Barrier()
         self.full, self.empty = [Barrier() for _ in range(2 * stages)], [Barrier() for _ in range(stages)]
-        self.s_full, self.s_taken, self.p_full, self.pv_done = two(), Barrier(), two(), two()
+        self.s_full, self.s_taken, self.p_full, self.pv_done = two(), Barrier(4), two(4), two()
+        self.rows_done, self.drained = two(4), {"S": Barrier(), "PV": Barrier()}
         self.go, self.checked = [[Barrier() for _ in range(PART)] for _ in range(SLOTS)], [[Barrier() for _ in range(PART)] for _ in range(SLOTS)]
         self.tiles, self.q = [Tile() for _ in range(stages)], Tile()
         self.slot = [None] * SLOTS
@@ -102,14 +108,18 @@ class Model:
     def commit(self, warp, bar):
         self.queue[warp].append(bar.arrive)
 
-    # ---- the roles; each yields (barrier, phase) that it waits for
+    # ---- the roles; each yields (barrier, phase) that it waits for, and is told whether it gave up
     def take(self, t):
-        yield self.item_full[t % 2], t // 2
+        return (yield self.item_full[t % 2], t // 2)
 
     def load(self):
-        use = n_q = 0
-        for t in range(len(self.items) + 1):
-            yield self.item_empty[t % 2], t // 2 - 1
+        use = n_q = t = 0
+        asked = False
+        dead = False
+        while True:
+            dead = yield self.item_empty[t % 2], t // 2 - 1
+            if dead:
+                break
             item = self.items[t] if t < len(self.items) else None
             self.slot[t % 2] = item
             self.item_full[t % 2].arrive()
@@ -122,84 +132,114 @@ class Model:
                     self.go[t % 2][k].arrive()
             self.next.expect(1)
             self.copies.append(("next", self.next.landed))
+            asked = True
             if n:
-                yield self.q_empty, n_q - 1
+                dead = yield self.q_empty, n_q - 1
+                if dead:
+                    break
                 self.q_full.expect(1)
                 self.copy("q", self.q, n_q, self.q_full)
                 n_q += 1
                 for i in range(2 * n):
-                    yield self.empty[self.ring.stage(use)], use // self.stages - 1
+                    dead = yield self.empty[self.ring.stage(use)], use // self.stages - 1
+                    if dead:
+                        break
                     bar = self.full[self.ring.full(use)]
                     bar.expect(1)
                     self.copy("v" if i & 1 else "k", self.tiles[self.ring.stage(use)], use, bar)
                     if i & 1 and i // 2 >= part:
                         self.go[t % 2][i // 2 - part].arrive()
                     use += 1
-            yield self.next, t
+            dead = dead or (yield self.next, t)
+            if dead:
+                break
+            asked = False
+            t += 1
         for u in range(max(0, use - self.stages), use):
-            yield self.empty[self.ring.stage(u)], u // self.stages
+            dead = dead or (yield self.empty[self.ring.stage(u)], u // self.stages, LONG)
         if n_q:
-            yield self.q_empty, n_q - 1
+            dead = dead or (yield self.q_empty, n_q - 1, LONG)
+        if not dead:
+            return
+        for u in range(max(0, use - self.stages), use):
+            yield (*self.wait_full(u), LANDS)
+        if n_q:
+            yield self.q_full, n_q - 1, LANDS
+        if asked:
+            yield self.next, t, LANDS
 
     def wait_full(self, use):
         return self.full[self.ring.full(use)], self.ring.round(use)
 
+    def drain(self, warp):
+        """What a warp that gave up does about its products."""
+        self.commit(warp, self.drained[warp])
+        yield self.drained[warp], 0, LANDS
+
     def scores(self):
         use0 = n_q = n_s = t = 0
-        while True:
-            yield from self.take(t)
+        while not (yield from self.take(t)):
             item = self.slot[t % 2]
             if item is None:
                 return
             n = max(item[:2])
             if n:
-                yield self.q_full, n_q
+                if (yield self.q_full, n_q):
+                    break
                 n_q += 1
                 for j in range(n):
                     use = use0 + 2 * j
-                    yield self.wait_full(use)
+                    dead = yield self.wait_full(use)
                     for x in range(2):
-                        if j < item[x]:
+                        if j < item[x] and not dead:
                             if n_s:
-                                yield self.s_taken, n_s - 1
+                                dead = yield self.s_taken, n_s - 1
                             n_s += 1
-                            self.product("S", [(self.q, n_q - 1), (self.tiles[self.ring.stage(use)], use)])
-                            self.commit("S", self.s_full[x])
+                            if not dead:
+                                self.product("S", [(self.q, n_q - 1), (self.tiles[self.ring.stage(use)], use)])
+                                self.commit("S", self.s_full[x])
+                    if dead:
+                        yield from self.drain("S")
+                        return
                     self.commit("S", self.empty[self.ring.stage(use)])
                     if j == n - 1:
                         self.commit("S", self.q_empty)
                 use0 += 2 * n
             self.item_empty[t % 2].arrive()
             t += 1
+        yield from self.drain("S")
 
     def sums(self):
         use0, n_p, t = 0, [0, 0], 0
-        while True:
-            yield from self.take(t)
+        while not (yield from self.take(t)):
             item = self.slot[t % 2]
             if item is None:
                 return
             n = max(item[:2])
             for j in range(n):
                 use = use0 + 2 * j + 1
-                yield self.wait_full(use)
-                if j >= item[2]:
-                    yield self.checked[t % 2][j - item[2]], t // 2
+                dead = yield self.wait_full(use)
+                if j >= item[2] and not dead:
+                    dead = yield self.checked[t % 2][j - item[2]], t // 2
                 for x in range(2):
-                    if j < item[x]:
-                        yield self.p_full[x], n_p[x]
+                    if j < item[x] and not dead:
+                        dead = yield self.p_full[x], n_p[x]
                         n_p[x] += 1
-                        self.product("PV", [(self.tiles[self.ring.stage(use)], use)])
-                        self.commit("PV", self.pv_done[x])
+                        if not dead:
+                            self.product("PV", [(self.tiles[self.ring.stage(use)], use)])
+                            self.commit("PV", self.pv_done[x])
+                if dead:
+                    yield from self.drain("PV")
+                    return
                 self.commit("PV", self.empty[self.ring.stage(use)])
             use0 += 2 * n
             self.item_empty[t % 2].arrive()
             t += 1
+        yield from self.drain("PV")
 
     def check(self):
         use0 = t = 0
-        while True:
-            yield from self.take(t)
+        while not (yield from self.take(t)):
             item = self.slot[t % 2]
             if item is None:
                 return
@@ -208,8 +248,8 @@ class Model:
                 j = item[2] + k
                 if j < n:
                     use = use0 + 2 * j + 1
-                    yield self.go[t % 2][k], t // 2
-                    yield self.wait_full(use)
+                    if (yield self.go[t % 2][k], t // 2) or (yield self.wait_full(use)):
+                        return
                     if self.tiles[self.ring.stage(use)].holds != use:
                         raise Stale("the check of V reads another tile")
                 self.checked[t % 2][k].arrive()
@@ -217,38 +257,54 @@ class Model:
             self.item_empty[t % 2].arrive()
             t += 1
 
-    def rows(self, x):
+    def rows(self, x, warp):
         n_s = n_pv = t = 0
-        while True:
-            yield from self.take(t)
+        while not (yield from self.take(t)):
             item = self.slot[t % 2]
             if item is None:
                 return
             for j in range(item[x]):
-                yield self.s_full[x], n_s
+                if (yield self.s_full[x], n_s):
+                    return
                 n_s += 1
                 self.s_taken.arrive()
                 if j:
-                    yield self.pv_done[x], n_pv
+                    if (yield self.pv_done[x], n_pv):
+                        return
                     n_pv += 1
                 self.p_full[x].arrive()
             if item[x]:
-                yield self.pv_done[x], n_pv
+                if (yield self.pv_done[x], n_pv):
+                    return
                 n_pv += 1
-            yield self.checked[t % 2][PART - 1], t // 2
-            self.outputs.append((t, x))
+            self.rows_done[x].arrive()
+            if (yield self.checked[t % 2][PART - 1], t // 2):
+                return
+            if (yield self.rows_done[x], t, *self.tile_sync):
+                return
+            self.outputs.append((t, x, warp))
             self.item_empty[t % 2].arrive()
             t += 1
 
+    tile_sync = ()
+
     # ---- any order
     def run(self):
-        roles = {"load": self.load(), "S": self.scores(), "PV": self.sums(), "check": self.check(), "A": self.rows(0), "B": self.rows(1)}
+        roles = {"load": self.load(), "S": self.scores(), "PV": self.sums(), "check": self.check()}
+        roles.update({"AB"[x] + str(w): self.rows(x, w) for x in range(2) for w in range(4)})
         kinds = [*roles, "k", "v", "q", "next", "S done", "PV done"]
         pace = {k: 10.0 ** -self.rng.randrange(4) for k in kinds}
         at = {k: next(g) for k, g in roles.items()}
+        gave_up = False
+
+        def go_on(k, dead):
+            try:
+                at[k] = roles[k].send(dead)
+            except StopIteration:
+                del at[k]
         while True:
             ways, seen = [], set()
-            for k, (bar, phase) in at.items():
+            for k, (bar, phase, *_) in at.items():
                 if bar.passes(phase):
                     ways.append((k, None))
             for i, (kind, _) in enumerate(self.copies):
@@ -256,14 +312,16 @@ class Model:
                     seen.add(kind)
                     ways.append((kind, i))
             ways += [(w + " done", w) for w in self.queue if self.queue[w]]
+            out = [k for k, w in at.items() if (len(w) == 2 or w[2] == LONG and not ways) and not w[0].passes(w[1])]   # may run out of time
+            if self.gives_up and out and (not ways or self.rng.random() < self.gives_up):
+                gave_up = True
+                go_on(self.rng.choice(out), True)
+                continue
             if not ways:
                 break
             k, what = self.rng.choices(ways, [pace[w[0]] for w in ways])[0]
             if k in at:
-                try:
-                    at[k] = next(roles[k])
-                except StopIteration:
-                    del at[k]
+                go_on(k, False)
             elif isinstance(what, int):
                 self.copies.pop(what)[1]()
             else:
@@ -271,7 +329,8 @@ class Model:
             if not at:
                 assert not self.copies and not any(self.queue.values()), "the block ends before what it started"
         assert not at and not self.copies, f"nothing goes on: {sorted(at)} wait"
-        assert sorted(self.outputs) == [(t, x) for t in range(len(self.items)) for x in range(2)]
+        if not gave_up:
+            assert sorted(self.outputs) == [(t, x, w) for t in range(len(self.items)) for x in range(2) for w in range(4)]
 
 
 class Ring:
@@ -325,7 +384,7 @@ def lib(tmp_path_factory):
 @pytest.mark.parametrize("stages", [5, 8])   # head_dim 128 and 64
 def test_no_wait_passes_early_and_no_product_reads_another_tile(lib, stages):
     ring = Ring(stages, lib)
-    for seed in range(1500):
+    for seed in range(800):
         rng = random.Random(seed)
         Model(some_items(rng), stages, ring, rng).run()
 
@@ -349,3 +408,25 @@ def test_the_model_sees_one_barrier_for_k_and_v():
         rng = random.Random(seed)
         Model([(7, 0, 5), (1, 0, 0), (9, 0, 8)], 8, Ring(8), rng).run()
     assert stale > 0
+
+
+@pytest.mark.parametrize("stages", [5, 8])
+def test_a_wait_that_gives_up_ends_every_role(lib, stages):
+    ring = Ring(stages, lib)
+    for seed in range(800):
+        rng = random.Random(seed)
+        Model(some_items(rng), stages, ring, rng, gives_up=rng.choice([0.002, 0.02, 0.2])).run()
+
+
+def test_the_model_sees_a_barrier_without_a_limit(lib):
+    """The warps of a tile at a barrier that none of them leaves before all have come: one that gave up never comes."""
+    class Unlimited(Model):
+        tile_sync = ("no limit",)
+    hung = 0
+    for seed in range(400):
+        rng = random.Random(seed)
+        try:
+            Unlimited([(2, 2, 1), (0, 0, 0), (3, 3, 1)], 5, Ring(5, lib), rng, gives_up=0.02).run()
+        except AssertionError as e:
+            hung += "nothing goes on" in str(e)
+    assert hung > 0
