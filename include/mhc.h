@@ -512,8 +512,8 @@ MHC_API mhc_status mhc_decode_attention_mxfp4(const mhc_bf16 *q, int64_t q_strid
 
 /* The same over packed bf16 keys and values: the rows q_offsets[b] .. of q are the last of the keys k_offsets[b] .. of k
  * and v (with as many of both: a whole prompt; with more keys: a later chunk of it after its prefix).  P is
- * held in bf16; its products with v (p up to 2^8) are summed in fp32 and divided at the end, so that sums past fp32's range
- * (v of about 2^120 over the number of keys, and more) are infinite.  Rows whose
+ * held in bf16 (at most 1; weights below 2^-118 of a row's largest may be lost); its products with v are summed in fp32 and
+ * divided at the end, so that sums past fp32's range (v of about 2^128 over the number of keys, and more) are infinite.  Rows whose
  * scores pass 2^28, and neighbouring rows (of at most 256 / (q_heads / kv_heads) tokens) one of which sees a value of v that
  * is not finite and another does not, are computed plainly in fp32, slowly.  Deterministic.  One launch. */
 MHC_API mhc_status mhc_prompt_attention(const mhc_bf16 *q, int64_t q_stride, const mhc_bf16 *k, int64_t k_stride,

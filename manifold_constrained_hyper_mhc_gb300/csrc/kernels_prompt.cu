@@ -1,13 +1,14 @@
 // Causal attention over packed prompts, with grouped heads.
 //
-//   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(s_j - m),  s_j = sm_scale log2(e) <q, k_j>,  m near the largest s so far
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(s_j - m),  s_j = sm_scale log2(e) <q, k_j>,  m at or above the largest s so far
 //
 // 4 D operations for each query head and visible key: the tensor cores are the floor.  The rows of one kv head are its
 // tokens times the heads of the group, NT = 128 / G whole tokens to a tile of 128 rows, so that a tile's rows see nearly
 // the same keys whatever G is.  A CTA takes two such tiles (A and B) over all their keys, 128 at a time:
 //   warps 0-3, 4-7  A's and B's rows, a row a thread: S from tensor memory, the row's maximum and sum, P as bf16 back to
-//                   tensor memory (2^-8 of p: the products take it beside bf16 v); a maximum is raised only when a score
-//                   is kLazy above it (p is then at most 2^kLazy), so the accumulators are rescaled a few times a row
+//                   tensor memory (2^-8 of p: the products take it beside bf16 v); m is set kLazy above the largest score
+//                   and raised when one passes it, so the accumulators are rescaled a few times a row and p is at most 1
+//                   (sums of p v end where fp32 sums of weights and v do; p ends at 2^-126, 2^-118 of the largest)
 //   warp 8          S = Q K^T from shared memory, A's and B's in turn into the same columns: S is in registers soon after
 //                   it is there, so the next one is computed beside the exponentials of this one
 //   warp 9          O += P V with P from tensor memory
@@ -363,8 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     idle = true;
                     tmem_fence_after();
                 };
-                if (__any_sync(0xffffffffu, top > m + kLazy)) {
-                    const float m1 = fmaxf(m, top), al = m == -INFINITY ? 0.f : ex2(m - m1);
+                if (__any_sync(0xffffffffu, top > m)) {
+                    const float m1 = fmaxf(m, top + kLazy), al = m == -INFINITY ? 0.f : ex2(m - m1);
                     if (on && fabsf(m1) > kFar && fabsf(m1) < INFINITY) far[slot][x] = 1;
                     m = m1;
                     l2 = make_float2(l2.x * al, l2.y * al);
