@@ -153,8 +153,7 @@ int rows_per_warp(int rows, int step, int64_t T, int num_sms) {
 
 }  // namespace
 
-cudaError_t launch_kv_write(const CacheArgs &c, const CacheWriteArgs &a, int64_t T, int D, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
+cudaError_t launch_kv_write(const CacheArgs &c, const CacheWriteArgs &a, int64_t T, int D, cudaStream_t stream) {
     const int64_t warps = T * ((2 * c.heads * (D / 32) + 31) / 32);
     const unsigned grid = (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
     mark_main_kernel(stream, true);

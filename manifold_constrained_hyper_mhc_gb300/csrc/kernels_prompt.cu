@@ -716,8 +716,7 @@ cudaError_t launch_one(const PromptArgs &a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_prompt(const PromptArgs &a, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
+cudaError_t launch_prompt(const PromptArgs &a, cudaStream_t stream) {
     return a.D == 128 ? launch_one<128>(a, stream) : launch_one<64>(a, stream);
 }
 

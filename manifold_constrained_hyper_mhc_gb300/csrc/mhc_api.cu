@@ -986,7 +986,7 @@ mhc_status mhc_kv_write_mxfp4(const void *k, const void *v, int value_type, int6
     Device dev;
     if ((st = current_device(dev)) != MHC_OK) return st;
     const cudaError_t e = mhc::launch_kv_write(cache_args(cache, pages, kv_heads, page_size, page_table, seq_lens, offsets, B, table_width),
-                                               {k, v, k_stride, v_stride, value_type == MHC_OUT_F32, scale_mode}, T, (int)head_dim, dev.sms,
+                                               {k, v, k_stride, v_stride, value_type == MHC_OUT_F32, scale_mode}, T, (int)head_dim,
                                                static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
     g_launches = 1;
@@ -1079,7 +1079,7 @@ mhc_status mhc_prompt_attention(const mhc_bf16 *q, int64_t q_stride, const mhc_b
     if ((st = current_device(dev)) != MHC_OK) return st;
     mhc::PromptArgs a{q, k, v, q_stride, k_stride, v_stride, Tq, Tk, (int)q_heads, (int)kv_heads, (int)head_dim, (int)B, q_offsets, k_offsets,
                       sm_scale, {attn_out, {attn_fp8, attn_scales, scale_mode}, lse, (int)q_heads}, static_cast<unsigned int *>(workspace)};
-    const cudaError_t e = mhc::launch_prompt(a, dev.sms, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = mhc::launch_prompt(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
     g_launches = 1;
     return MHC_OK;

@@ -187,7 +187,7 @@ struct CacheWriteArgs {
     bool f32;
     int mode;                    // mhc_mx_scale_mode
 };
-cudaError_t launch_kv_write(const CacheArgs &c, const CacheWriteArgs &a, int64_t T, int D, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_write(const CacheArgs &c, const CacheWriteArgs &a, int64_t T, int D, cudaStream_t stream);
 cudaError_t launch_kv_read(const CacheArgs &c, uint16_t *k, uint16_t *v, int64_t T, int D, int num_sms, cudaStream_t stream);
 
 // Where an attention's result goes: any of out [T][heads][D] bf16, mx [T][heads * D] and lse [T][heads] fp32.
@@ -221,7 +221,7 @@ struct PromptArgs {
     AttnOut o;
     unsigned int *status;        // bit 0 is set when a bounded wait gives up
 };
-cudaError_t launch_prompt(const PromptArgs &a, int num_sms, cudaStream_t stream);
+cudaError_t launch_prompt(const PromptArgs &a, cudaStream_t stream);
 
 cudaError_t launch_post(const uint16_t *R, const uint16_t *Y, const float *prev_post,
                         const float *prev_comb, int64_t T, int H, uint16_t *R_out, int num_sms,
