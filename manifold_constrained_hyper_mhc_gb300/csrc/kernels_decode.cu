@@ -23,10 +23,12 @@
 // (ldmatrix.trans), as they lie; q and the output follow that order.  P crosses from one product's layout to the other's
 // by movmatrix.
 //
-// Measured: 64 sequences of 100 to 16,000 tokens, 64 / 8 heads of 128: 112 us, 74 % of the copy rate (copies alone take 90 % of
-// that, the arithmetic alone too: about 600 instructions a slice, half of them on the ALU pipe); 32,003 tokens, 6 queries of
-// 56 / 8 heads: 39 us, bound by the conversions, which each row tile does anew; 3 sequences of 60,001 to 131,000, 32 / 4
-// heads of 64: 29 us, 37 %, bound by the arithmetic (half the bytes a token for the same softmax).
+// Measured (in a graph): 64 sequences of 100 to 16,000 tokens, 64 / 8 heads of 128: 110 us, 76 % of the copy rate (at 118 us
+// the copies alone took 98, the arithmetic alone 103: about 600 instructions a slice, half of them on the ALU pipe, which is
+// 64 % busy); 32,003 tokens, 6 queries of 56 / 8 heads: 38 us, the conversions, which each row tile does anew, by two warps
+// a scheduler with no pipe full (ALU 39 %, tensor 30 %); 3 sequences of 60,001 to 131,000, 32 / 4 heads of 64: 29 us, 37 %,
+// no pipe full either (ALU 53 %, issue 59 %, DRAM 36 %): the latency of 12 warps with half the bytes a slice, and the
+// join behind them.
 #include "attention.cuh"
 #include "mhc.h"
 #include "sm100_ptx.cuh"

@@ -22,10 +22,12 @@
 // pairs of all lengths fill the device.
 // Every mbarrier wait is bounded in time; one that gives up sets bit 0 of the status word.
 //
-// Measured: 8,192 tokens, 56 / 8 heads of 128: 617 us, 1,560 TFLOP/s, 81 % of the measured bf16 rate (670 in long runs,
-// where the power limit lowers the clock; the tensor pipe is 68 % active); 2,000 tokens after 30,001: 1,085 us, 85 %;
-// 8,192 tokens, 32 / 4 heads of 64: 245 us, 1,122 TFLOP/s, bound by the exponentials.  Short prompts lose about 2 us a pair to
-// its last products and its result (nine of 37 to 1,500 tokens, 32 / 8 heads: 88 us, 39 %).
+// Measured: 8,192 tokens, 56 / 8 heads of 128: 660 us a call among calls, 1,457 TFLOP/s, 75 % of the measured bf16 rate (84 %
+// of that of long runs: the power limit lowers the clock) and 620 us alone, 80 %; the tensor pipe is 67 % active.  2,000
+// tokens after 30,001: 1,170 us, 79 %, and 1,120 alone.  8,192 tokens, 32 / 4 heads of 64: 247 us, 1,113 TFLOP/s, no pipe
+// full (tensor 47 % active, exponentials 47 %, ALU 37 %, issue 53 %): the chain from S over the exponentials to P.  Short
+// prompts (nine of 37 to 1,500 tokens, 32 / 8 heads: 85 us, 40 %, tensor pipe 40 %) have that chain, the last products and
+// the result of a pair in a row, 14 us, of which the products take 6.4.
 #include <algorithm>
 #include <cstring>
 
